@@ -24,12 +24,15 @@ LOWRANK, HEADWISE = 0, 1
 F32, BF16 = 0, 1
 ALGO_AUTO, ALGO_SIMT, ALGO_TC = 0, 1, 2
 TOKEN_MAJOR, CHANNEL_FIRST = 0, 1
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 
 # Every entry point the header declares (checked against the library's exports by the tests).
 EXPORTS = ("dynconv_workspace_bytes", "dynconv_fwd", "dynconv_fwd_varlen", "dynconv_bwd",
            "dynconv_device_status", "dynconv_last_error", "dynconv_status_string", "dynconv_version",
            "dynconv_profile_enable", "dynconv_profile_read", "dynconv_selftest_umma", "dynconv_fwd_noalloc",
-           "dynconv_decode_step", "dynconv_noalloc_status", "dynconv_query_family", "dynconv_selftest_wait")
+           "dynconv_decode_step", "dynconv_noalloc_status", "dynconv_query_family", "dynconv_selftest_wait",
+           "dynconv_rope", "dynconv_attn_workspace_bytes", "dynconv_attn_query_family", "dynconv_attn_fwd",
+           "dynconv_attn_bwd")
 
 
 class DynConvError(RuntimeError):
@@ -50,6 +53,22 @@ class dynconv_desc(ctypes.Structure):
                 ("deterministic", ctypes.c_int32), ("algo", ctypes.c_int32), ("layout", ctypes.c_int32),
                 ("rope_channels", ctypes.c_int64), ("rope_head_dim", ctypes.c_int64), ("rope_max_pos", ctypes.c_int64),
                 ("rope_cos_sin", ctypes.c_void_p)]
+
+
+class dynconv_rope_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("batch", ctypes.c_int64),
+                ("seqlen", ctypes.c_int64), ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int64), ("x_row_stride", ctypes.c_int64), ("y_row_stride", ctypes.c_int64),
+                ("max_pos", ctypes.c_int64), ("cos_sin", ctypes.c_void_p), ("inverse", ctypes.c_int32)]
+
+
+class dynconv_attn_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("algo", ctypes.c_int32), ("batch", ctypes.c_int64),
+                ("seqlen", ctypes.c_int64), ("heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("q_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
+                ("v_row_stride", ctypes.c_int64), ("o_row_stride", ctypes.c_int64), ("do_row_stride", ctypes.c_int64),
+                ("dq_row_stride", ctypes.c_int64), ("dk_row_stride", ctypes.c_int64), ("dv_row_stride", ctypes.c_int64),
+                ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -95,6 +114,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.dynconv_selftest_umma.restype = ctypes.c_int
     lib.dynconv_selftest_wait.argtypes = [ctypes.c_uint64, vp, vp, vp]
     lib.dynconv_selftest_wait.restype = ctypes.c_int
+    RD, AD = ctypes.POINTER(dynconv_rope_desc), ctypes.POINTER(dynconv_attn_desc)
+    lib.dynconv_rope.argtypes = [RD, vp, i64, vp, vp, vp, vp, sz, vp]
+    lib.dynconv_attn_workspace_bytes.argtypes = [AD]
+    lib.dynconv_attn_workspace_bytes.restype = sz
+    lib.dynconv_attn_query_family.argtypes = [AD, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
+    lib.dynconv_attn_fwd.argtypes = [AD, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.dynconv_attn_bwd.argtypes = [AD, vp, i64] + [vp] * 10 + [sz, vp]
+    for f in (lib.dynconv_rope, lib.dynconv_attn_query_family, lib.dynconv_attn_fwd, lib.dynconv_attn_bwd):
+        f.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib
@@ -126,6 +154,23 @@ def make_desc(kind: int, dtype: int, batch: int, seqlen: int, d_model: int, chan
     rope_ptr = ctypes.c_void_p(rope_table.data_ptr()) if rope_table is not None else None
     return dynconv_desc(kind, dtype, batch, seqlen, d_model, channels, ksize, rank, head_dim, u_row_stride,
                         h_row_stride, deterministic, algo, layout, rope_channels, rope_head_dim, rope_max, rope_ptr)
+
+
+def make_rope_desc(dtype: int, layout: int, batch: int, seqlen: int, heads: int, head_dim: int,
+                   table: torch.Tensor, inverse: int = 0, x_row_stride: int = 0,
+                   y_row_stride: int = 0) -> dynconv_rope_desc:
+    """table: device fp32 [max_pos, rot_dim] (cos, sin pairs), kept alive by the caller."""
+    return dynconv_rope_desc(dtype, layout, batch, seqlen, heads, head_dim, int(table.shape[1]), x_row_stride,
+                             y_row_stride, int(table.shape[0]), ctypes.c_void_p(table.data_ptr()), inverse)
+
+
+def make_attn_desc(dtype: int, batch: int, seqlen: int, heads: int, kv_heads: int, head_dim: int, algo: int = ALGO_AUTO,
+                   scale: float = 0.0, q_row_stride: int = 0, k_row_stride: int = 0, v_row_stride: int = 0,
+                   o_row_stride: int = 0, do_row_stride: int = 0, dq_row_stride: int = 0, dk_row_stride: int = 0,
+                   dv_row_stride: int = 0) -> dynconv_attn_desc:
+    return dynconv_attn_desc(dtype, algo, batch, seqlen, heads, kv_heads, head_dim, q_row_stride, k_row_stride,
+                             v_row_stride, o_row_stride, do_row_stride, dq_row_stride, dk_row_stride, dv_row_stride,
+                             scale)
 
 
 def dynconv_workspace_bytes(desc: dynconv_desc) -> int:
@@ -171,6 +216,37 @@ def dynconv_decode_step(desc, u, h, A, B_or_W, state, y, ws, stream=None):
 def dynconv_device_status(ws, stream=None) -> int:
     """Synchronises the stream; returns the status (does not raise)."""
     return int(load().dynconv_device_status(_ptr(ws), ws.numel() * ws.element_size(), _stream(stream, ws)))
+
+
+def _docs(cu_seqlens) -> int:
+    return 0 if cu_seqlens is None else cu_seqlens.numel() - 1
+
+
+def dynconv_rope(desc, cu_seqlens, positions, x, y, ws, stream=None):
+    _check(load().dynconv_rope(ctypes.byref(desc), _ptr(cu_seqlens), _docs(cu_seqlens), _ptr(positions), _ptr(x),
+                               _ptr(y), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream, x)))
+
+
+def dynconv_attn_workspace_bytes(desc: dynconv_attn_desc) -> int:
+    return int(load().dynconv_attn_workspace_bytes(ctypes.byref(desc)))
+
+
+def dynconv_attn_fwd(desc, cu_seqlens, q, k, v, o, lse, ws, stream=None):
+    _check(load().dynconv_attn_fwd(ctypes.byref(desc), _ptr(cu_seqlens), _docs(cu_seqlens), _ptr(q), _ptr(k), _ptr(v),
+                                   _ptr(o), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream, q)))
+
+
+def dynconv_attn_bwd(desc, cu_seqlens, d_o, q, k, v, o, lse, dq, dk, dv, ws, stream=None):
+    _check(load().dynconv_attn_bwd(ctypes.byref(desc), _ptr(cu_seqlens), _docs(cu_seqlens), _ptr(d_o), _ptr(q),
+                                   _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
+                                   ws.numel() * ws.element_size(), _stream(stream, q)))
+
+
+def dynconv_attn_query_family(desc: dynconv_attn_desc):
+    """(forward family, backward family, reason) of an attention descriptor; host-only."""
+    f, b = ctypes.c_int32(0), ctypes.c_int32(0)
+    _check(load().dynconv_attn_query_family(ctypes.byref(desc), ctypes.byref(f), ctypes.byref(b)))
+    return FAMILY_NAMES[f.value], FAMILY_NAMES[b.value], dynconv_last_error()
 
 
 FAMILY_TENSOR_CORE, FAMILY_CUDA_CORE = 1, 2

@@ -353,9 +353,10 @@ dynconv_status dynconv_device_status(void* ws, size_t ws_bytes, void* stream) {
     if (word == 0) return DYNCONV_OK;
     if ((s = cuda_status(cudaMemsetAsync(ws, 0, sizeof(word), st), "clear error word"))) return s;
     if ((s = cuda_status(cudaStreamSynchronize(st), "stream synchronize"))) return s;
-    set_error("device check failed:%s%s%s", (word & kErrBadSeqlens) ? " malformed cu_seqlens" : "",
+    set_error("device check failed:%s%s%s%s", (word & kErrBadSeqlens) ? " malformed cu_seqlens" : "",
               (word & kErrWaitTimeout) ? " pipeline wait timed out" : "",
-              (word & kErrRopePos) ? " a packed document is longer than rope_max_pos" : "");
+              (word & kErrRopePos) ? " a packed document is longer than rope_max_pos, or a position is outside the table" : "",
+              (word & kErrCacheLen) ? " cached plus new tokens exceed the cache" : "");
     return DYNCONV_ERR_DEVICE_CHECK;
 }
 

@@ -1,0 +1,49 @@
+// attn.h -- host-side structures of the rotary, attention and cache-attention operators.
+#pragma once
+
+#include "internal.h"
+
+namespace dynconv {
+
+// A validated rotary problem.
+struct RopeProb {
+    int dtype;              // 0 fp32, 1 bf16
+    int half;               // 0 interleaved pairs, 1 pairs (i, i + rot / 2)
+    int inverse;
+    int64_t N, seqlen;
+    int heads, hd, rot;
+    int64_t xs, ys;         // row strides of x and y, elements
+    int64_t max_pos;
+    const float* cs;
+    const int32_t* cu;      // packed documents or nullptr
+    int64_t n_docs;
+    const int32_t* pos;     // explicit positions or nullptr
+};
+cudaError_t rope_launch(const RopeProb& p, const void* x, void* y, uint32_t* err, cudaStream_t st);
+
+// A validated attention problem (N < 2^31).
+struct AttnProb {
+    int dtype, algo;
+    int64_t N, seqlen;
+    int heads, kvh, hd, group;
+    int64_t qs, ks, vs, os, dos, dqs, dks, dvs;   // row strides, elements
+    float scale;            // of the scores
+    const int32_t* cu;
+    int64_t n_docs;
+};
+// Workspace of the attention passes: the error word, then D[heads][N] of the backward.
+struct AttnWs {
+    size_t delta, total;
+};
+AttnWs attn_ws(const AttnProb& p);
+// Why the tensor-core kernels do not take the problem (nullptr when they do).
+const char* attn_tc_refusal(const AttnProb& p);
+
+cudaError_t attn_simt_fwd(const AttnProb& p, const void* q, const void* k, const void* v, void* o, float* lse,
+                          cudaStream_t st);
+cudaError_t attn_simt_bwd(const AttnProb& p, const void* d_o, const void* q, const void* k, const void* v,
+                          const float* lse, const float* delta, void* dq, void* dk, void* dv, cudaStream_t st);
+// D[h][n] = d_o[n, h] . o[n, h], fp32.
+cudaError_t attn_delta(const AttnProb& p, const void* d_o, const void* o, float* delta, cudaStream_t st);
+
+}  // namespace dynconv

@@ -1,0 +1,499 @@
+// attn_simt.cu -- causal attention on the CUDA cores, forward and backward: fp32 storage (never
+// rounded to a tensor-core input type) and the bf16 shapes the tensor-core kernels do not take.
+//
+//   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i.k_j - lse_i),  s(i) <= j <= i
+//   dp_ij = do_i.v_j,  ds_ij = p_ij (dp_ij - D_i),  D_i = do_i.o_i
+//   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij do_i
+//
+// A block takes 64 query rows (forward, dq) or 64 keys (dk, dv) of one head and walks the 64-row
+// tiles of the other side; tiles follow the packed token index, so documents need no list of
+// work: a row's first visible key is its document's start, and only the tiles that a diagonal or a
+// document start crosses are masked.  256 threads each hold a 4 x 4 block of the 64 x 64 scores
+// (rows 4 ty + i, columns tx + 16 j) and 4 rows x HD / 16 channels of the accumulators; operands
+// are fp32 in shared memory, rows padded to HD + 4 floats so that the 16 column rows of a warp's
+// 16-byte loads fall in different banks.  Per 4 channels a thread loads 8 x 16 bytes for 64 FMAs
+// (12 of 16 shared-memory cycles), so the FMA pipe is the bound.
+//
+// Masked places: the score is replaced before the maximum, and in masked tiles a product with a
+// masked probability is not added at all (0 x NaN would be NaN).
+#include <algorithm>
+
+#include "attn.h"
+#include "common.cuh"
+#include "prof.h"
+
+namespace dynconv {
+namespace {
+
+constexpr int kTile = 64;
+constexpr int kThreads = 256;
+constexpr int kLdP = kTile + 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int HD>
+constexpr int ld_of() { return HD + 4; }
+
+struct SimtArgs {
+    int32_t N, seqlen, n_docs;
+    int heads, kvh, group, hd;
+    int64_t qs, ks, vs, os, dos, dqs, dks, dvs;
+    float scale;
+    const int32_t* cu;
+};
+
+// rows row0 .. row0 + 63 of one head (channels hd, zero beyond hd and beyond N) into fp32 shared memory
+template <typename T, int HD>
+__device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ src, int64_t stride, int32_t row0, int32_t N,
+                                          int hd, bool vec) {
+    constexpr int LD = ld_of<HD>();
+    if (vec) {
+        for (int i = threadIdx.x; i < kTile * (HD / 4); i += kThreads) {
+            const int r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row0 + r < N && c < hd) {
+                const T* p = src + (int64_t)(row0 + r) * stride + c;
+                if (sizeof(T) == 4) {
+                    f = *reinterpret_cast<const float4*>(p);
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(p);
+                    f = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                                    __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+                }
+            }
+            *reinterpret_cast<float4*>(dst + r * LD + c) = f;
+        }
+    } else {
+        for (int i = threadIdx.x; i < kTile * HD; i += kThreads) {
+            const int r = i / HD, c = i % HD;
+            dst[r * LD + c] = row0 + r < N && c < hd ? to_f32(src[(int64_t)(row0 + r) * stride + c]) : 0.f;
+        }
+    }
+}
+
+// acc[i][j] = A[4 ty + i] . B[tx + 16 j] over HD channels
+template <int HD>
+__device__ __forceinline__ void tile_nt(const float* A, const float* B, float (&acc)[4][4], int ty, int tx) {
+    constexpr int LD = ld_of<HD>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < HD; c += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * LD + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * LD + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
+                acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
+                acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
+                acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+            }
+    }
+}
+
+// acc[i][4 jj + e] += sum_c P[4 ty + i][c] X[c][4 tx + 64 jj + e]; with MASK only over c in [lo_i, hi_i]
+template <int HD, bool MASK>
+__device__ __forceinline__ void tile_nn(const float* P, const float* X, float (&acc)[4][HD / 16], int ty, int tx,
+                                        const int (&lo)[4], const int (&hi)[4]) {
+    constexpr int LD = ld_of<HD>();
+    constexpr int NJ = HD / 64;
+#pragma unroll 2
+    for (int c = 0; c < kTile; c += 4) {
+        float p[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 f = *reinterpret_cast<const float4*>(P + (4 * ty + i) * kLdP + c);
+            p[i][0] = f.x; p[i][1] = f.y; p[i][2] = f.z; p[i][3] = f.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int jj = 0; jj < NJ; ++jj) {
+                const float4 x = *reinterpret_cast<const float4*>(X + (c + e) * LD + 4 * tx + 64 * jj);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (MASK && (c + e < lo[i] || c + e > hi[i])) continue;
+                    acc[i][4 * jj + 0] = fmaf(p[i][e], x.x, acc[i][4 * jj + 0]);
+                    acc[i][4 * jj + 1] = fmaf(p[i][e], x.y, acc[i][4 * jj + 1]);
+                    acc[i][4 * jj + 2] = fmaf(p[i][e], x.z, acc[i][4 * jj + 2]);
+                    acc[i][4 * jj + 3] = fmaf(p[i][e], x.w, acc[i][4 * jj + 3]);
+                }
+            }
+    }
+}
+
+// reductions over the 16 lanes (tx) of a row
+__device__ __forceinline__ float row_max(float x) {
+#pragma unroll
+    for (int o = 8; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+    return x;
+}
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int o = 8; o; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    return x;
+}
+
+template <typename T, int HD>
+__device__ __forceinline__ void store_rows(T* dst, int64_t stride, int32_t row0, int32_t N, int hd,
+                                           const float (&acc)[4][HD / 16], const float (&mul)[4], int ty, int tx) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int32_t n = row0 + 4 * ty + i;
+        if (n >= N) continue;
+        T* p = dst + (int64_t)n * stride;
+#pragma unroll
+        for (int jj = 0; jj < HD / 64; ++jj)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = 4 * tx + 64 * jj + e;
+                if (c < hd) p[c] = from_f32<T>(acc[i][4 * jj + e] * mul[i]);
+            }
+    }
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                                 const T* __restrict__ v, T* __restrict__ o,
+                                                                 float* __restrict__ lse, SimtArgs a, int vec) {
+    constexpr int LD = ld_of<HD>();
+    extern __shared__ float sm[];
+    float* sQ = sm;
+    float* sK = sQ + kTile * LD;
+    float* sV = sK + kTile * LD;
+    float* sP = sK;                        // the keys are read before the probabilities are written
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int head = blockIdx.x % a.heads, kv = head / a.group;
+    const int32_t tiles = (a.N + kTile - 1) / kTile;
+    const int32_t row0 = (tiles - 1 - (int32_t)(blockIdx.x / a.heads)) * kTile;   // long rows first
+    q += (int64_t)head * a.hd;
+    o += (int64_t)head * a.hd;
+    k += (int64_t)kv * a.hd;
+    v += (int64_t)kv * a.hd;
+    load_tile<T, HD>(sQ, q, a.qs, row0, a.N, a.hd, vec);
+    const int32_t last = min(row0 + kTile, a.N) - 1;
+    const int32_t first_key = seg_start32(row0, a.cu, a.n_docs, a.seqlen);
+    const int32_t full_from = seg_start32(last, a.cu, a.n_docs, a.seqlen);
+    int32_t start[4];
+    float m[4], l[4], acc[4][HD / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        start[i] = seg_start32(min(row0 + 4 * ty + i, a.N - 1), a.cu, a.n_docs, a.seqlen);
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < HD / 16; ++c) acc[i][c] = 0.f;
+    }
+    const float cs = a.scale * kLog2e;
+    for (int32_t k0 = first_key / kTile * kTile; k0 <= last; k0 += kTile) {
+        __syncthreads();
+        load_tile<T, HD>(sK, k, a.ks, k0, a.N, a.hd, vec);
+        load_tile<T, HD>(sV, v, a.vs, k0, a.N, a.hd, vec);
+        __syncthreads();
+        float s[4][4];
+        tile_nt<HD>(sQ, sK, s, ty, tx);
+        const bool masked = k0 + kTile - 1 > row0 || k0 < full_from;
+        int lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = start[i] - k0;
+            hi[i] = row0 + 4 * ty + i - k0;
+            float mx = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = tx + 16 * j;
+                if (masked && (c < lo[i] || c > hi[i])) s[i][j] = -INFINITY;
+                mx = fmaxf(mx, s[i][j] * cs);
+            }
+            mx = row_max(mx);
+            const float use = mx == -INFINITY ? 0.f : mx;     // a row that has seen no key yet
+            const float corr = exp2f(m[i] - use);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = exp2f(fmaf(s[i][j], cs, -use));
+                sum += s[i][j];
+            }
+            l[i] = l[i] * corr + sum;
+            m[i] = mx;
+#pragma unroll
+            for (int c = 0; c < HD / 16; ++c) acc[i][c] *= corr;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sP[(4 * ty + i) * kLdP + tx + 16 * j] = s[i][j];
+        __syncthreads();
+        if (masked) tile_nn<HD, true>(sP, sV, acc, ty, tx, lo, hi);
+        else tile_nn<HD, false>(sP, sV, acc, ty, tx, lo, hi);
+    }
+    float inv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        l[i] = row_sum(l[i]);
+        inv[i] = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+        const int32_t n = row0 + 4 * ty + i;
+        if (lse != nullptr && tx == 0 && n < a.N) lse[(int64_t)head * a.N + n] = (m[i] + log2f(l[i])) * kLn2;
+    }
+    store_rows<T, HD>(o, a.os, row0, a.N, a.hd, acc, inv, ty, tx);
+}
+
+// dq of 64 query rows of one head: the tiles of keys walked as in the forward.
+template <typename T, int HD>
+__global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restrict__ d_o, const T* __restrict__ q,
+                                                                const T* __restrict__ k, const T* __restrict__ v,
+                                                                const float* __restrict__ lse,
+                                                                const float* __restrict__ delta, T* __restrict__ dq,
+                                                                SimtArgs a, int vec) {
+    constexpr int LD = ld_of<HD>();
+    extern __shared__ float sm[];
+    float* sQ = sm;
+    float* sO = sQ + kTile * LD;
+    float* sK = sO + kTile * LD;
+    float* sV = sK + kTile * LD;
+    float* sD = sV;                        // the values are read before ds is written
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int head = blockIdx.x % a.heads, kv = head / a.group;
+    const int32_t tiles = (a.N + kTile - 1) / kTile;
+    const int32_t row0 = (tiles - 1 - (int32_t)(blockIdx.x / a.heads)) * kTile;
+    load_tile<T, HD>(sQ, q + (int64_t)head * a.hd, a.qs, row0, a.N, a.hd, vec);
+    load_tile<T, HD>(sO, d_o + (int64_t)head * a.hd, a.dos, row0, a.N, a.hd, vec);
+    k += (int64_t)kv * a.hd;
+    v += (int64_t)kv * a.hd;
+    const int32_t last = min(row0 + kTile, a.N) - 1;
+    const int32_t first_key = seg_start32(row0, a.cu, a.n_docs, a.seqlen);
+    const int32_t full_from = seg_start32(last, a.cu, a.n_docs, a.seqlen);
+    int32_t start[4];
+    float ls[4], dl[4], acc[4][HD / 16], mul[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int32_t n = min(row0 + 4 * ty + i, a.N - 1);
+        start[i] = seg_start32(n, a.cu, a.n_docs, a.seqlen);
+        ls[i] = lse[(int64_t)head * a.N + n] * kLog2e;
+        dl[i] = delta[(int64_t)head * a.N + n];
+        mul[i] = a.scale;
+#pragma unroll
+        for (int c = 0; c < HD / 16; ++c) acc[i][c] = 0.f;
+    }
+    const float cs = a.scale * kLog2e;
+    for (int32_t k0 = first_key / kTile * kTile; k0 <= last; k0 += kTile) {
+        __syncthreads();
+        load_tile<T, HD>(sK, k, a.ks, k0, a.N, a.hd, vec);
+        load_tile<T, HD>(sV, v, a.vs, k0, a.N, a.hd, vec);
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        tile_nt<HD>(sQ, sK, s, ty, tx);
+        tile_nt<HD>(sO, sV, dp, ty, tx);
+        const bool masked = k0 + kTile - 1 > row0 || k0 < full_from;
+        int lo[4], hi[4];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = start[i] - k0;
+            hi[i] = row0 + 4 * ty + i - k0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = tx + 16 * j;
+                const float p = exp2f(fmaf(s[i][j], cs, -ls[i]));
+                const bool hide = masked && (c < lo[i] || c > hi[i]);
+                sD[(4 * ty + i) * kLdP + c] = hide ? 0.f : p * (dp[i][j] - dl[i]);
+            }
+        }
+        __syncthreads();
+        if (masked) tile_nn<HD, true>(sD, sK, acc, ty, tx, lo, hi);
+        else tile_nn<HD, false>(sD, sK, acc, ty, tx, lo, hi);
+    }
+    store_rows<T, HD>(dq + (int64_t)head * a.hd, a.dqs, row0, a.N, a.hd, acc, mul, ty, tx);
+}
+
+// dk and dv of 64 keys of one key/value head: every head of the group, every tile of queries that sees
+// a key of the tile, in order (no atomics).  Scores are held transposed: rows are keys.
+template <typename T, int HD>
+__global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __restrict__ d_o, const T* __restrict__ q,
+                                                                 const T* __restrict__ k, const T* __restrict__ v,
+                                                                 const float* __restrict__ lse,
+                                                                 const float* __restrict__ delta, T* __restrict__ dk,
+                                                                 T* __restrict__ dv, SimtArgs a, int vec) {
+    constexpr int LD = ld_of<HD>();
+    extern __shared__ float sm[];
+    float* sK = sm;
+    float* sV = sK + kTile * LD;
+    float* sQ = sV + kTile * LD;
+    float* sO = sQ + kTile * LD;
+    float* sP = sO + kTile * LD;
+    float* sD = sP + kTile * kLdP;
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int kv = blockIdx.x % a.kvh;
+    const int32_t row0 = (int32_t)(blockIdx.x / a.kvh) * kTile;           // early keys have the most queries
+    load_tile<T, HD>(sK, k + (int64_t)kv * a.hd, a.ks, row0, a.N, a.hd, vec);
+    load_tile<T, HD>(sV, v + (int64_t)kv * a.hd, a.vs, row0, a.N, a.hd, vec);
+    const int32_t last = min(row0 + kTile, a.N) - 1;
+    int32_t s0, first_end, e_last;
+    seg_bounds32(row0, a.cu, a.n_docs, a.seqlen, a.N, s0, first_end);
+    seg_bounds32(last, a.cu, a.n_docs, a.seqlen, a.N, s0, e_last);        // queries end with the last key's document
+    int32_t end[4];
+    float acck[4][HD / 16], accv[4][HD / 16], mk[4], mv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        seg_bounds32(min(row0 + 4 * ty + i, a.N - 1), a.cu, a.n_docs, a.seqlen, a.N, s0, end[i]);
+        mk[i] = a.scale;
+        mv[i] = 1.f;
+#pragma unroll
+        for (int c = 0; c < HD / 16; ++c) acck[i][c] = accv[i][c] = 0.f;
+    }
+    const float cs = a.scale * kLog2e;
+    for (int g = 0; g < a.group; ++g) {
+        const int head = kv * a.group + g;
+        for (int32_t q0 = row0; q0 < e_last; q0 += kTile) {
+            __syncthreads();
+            load_tile<T, HD>(sQ, q + (int64_t)head * a.hd, a.qs, q0, a.N, a.hd, vec);
+            load_tile<T, HD>(sO, d_o + (int64_t)head * a.hd, a.dos, q0, a.N, a.hd, vec);
+            float ls[4], dl[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int32_t n = min(q0 + tx + 16 * j, a.N - 1);
+                ls[j] = lse[(int64_t)head * a.N + n] * kLog2e;
+                dl[j] = delta[(int64_t)head * a.N + n];
+            }
+            __syncthreads();
+            float s[4][4], dp[4][4];
+            tile_nt<HD>(sK, sQ, s, ty, tx);
+            tile_nt<HD>(sV, sO, dp, ty, tx);
+            const bool masked = q0 < row0 + kTile || q0 + kTile > first_end;
+            int lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo[i] = row0 + 4 * ty + i - q0;
+                hi[i] = end[i] - 1 - q0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = tx + 16 * j;
+                    const float p = exp2f(fmaf(s[i][j], cs, -ls[j]));
+                    const bool hide = masked && (c < lo[i] || c > hi[i]);
+                    sP[(4 * ty + i) * kLdP + c] = hide ? 0.f : p;
+                    sD[(4 * ty + i) * kLdP + c] = hide ? 0.f : p * (dp[i][j] - dl[j]);
+                }
+            }
+            __syncthreads();
+            if (masked) {
+                tile_nn<HD, true>(sP, sO, accv, ty, tx, lo, hi);
+                tile_nn<HD, true>(sD, sQ, acck, ty, tx, lo, hi);
+            } else {
+                tile_nn<HD, false>(sP, sO, accv, ty, tx, lo, hi);
+                tile_nn<HD, false>(sD, sQ, acck, ty, tx, lo, hi);
+            }
+        }
+    }
+    store_rows<T, HD>(dk + (int64_t)kv * a.hd, a.dks, row0, a.N, a.hd, acck, mk, ty, tx);
+    store_rows<T, HD>(dv + (int64_t)kv * a.hd, a.dvs, row0, a.N, a.hd, accv, mv, ty, tx);
+}
+
+// A warp per (token, head); lanes over the channels.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) attn_delta_kernel(const T* __restrict__ d_o, const T* __restrict__ o,
+                                                              int64_t dos, int64_t os, int64_t N, int heads, int hd,
+                                                              float* __restrict__ delta) {
+    const int64_t w = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / 32;
+    const int lane = threadIdx.x % 32;
+    const int64_t n = w / heads;
+    if (n >= N) return;
+    const int h = (int)(w - n * heads);
+    float s = 0.f;
+    for (int c = lane; c < hd; c += 32)
+        s = fmaf(to_f32(d_o[n * dos + (int64_t)h * hd + c]), to_f32(o[n * os + (int64_t)h * hd + c]), s);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
+    if (lane == 0) delta[(int64_t)h * N + n] = s;
+}
+
+SimtArgs args_of(const AttnProb& p) {
+    return SimtArgs{(int32_t)p.N, (int32_t)p.seqlen, (int32_t)p.n_docs, p.heads, p.kvh, p.group, p.hd, p.qs, p.ks, p.vs,
+                    p.os, p.dos, p.dqs, p.dks, p.dvs, p.scale, p.cu};
+}
+
+// 16-byte (fp32) or 8-byte (bf16) loads of four channels: head starts and rows on such boundaries
+int vec_ok(const AttnProb& p, bool bwd) {
+    return p.hd % 4 == 0 && p.qs % 4 == 0 && p.ks % 4 == 0 && p.vs % 4 == 0 && (!bwd || p.dos % 4 == 0);
+}
+
+template <typename F>
+cudaError_t big_smem(F* f, size_t bytes) {
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, int HD>
+cudaError_t fwd_t(const AttnProb& p, const void* q, const void* k, const void* v, void* o, float* lse,
+                  cudaStream_t st) {
+    constexpr size_t smem = sizeof(float) * 3 * kTile * ld_of<HD>();
+    cudaError_t e = big_smem(attn_fwd_simt_kernel<T, HD>, smem);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)((p.N + kTile - 1) / kTile * p.heads);
+    DC_LAUNCH(kAttnSimtFwd, st, attn_fwd_simt_kernel<T, HD><<<grid, kThreads, smem, st>>>(
+                                    static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
+                                    static_cast<T*>(o), lse, args_of(p), vec_ok(p, false)));
+    return cudaGetLastError();
+}
+
+template <typename T, int HD>
+cudaError_t bwd_t(const AttnProb& p, const void* d_o, const void* q, const void* k, const void* v, const float* lse,
+                  const float* delta, void* dq, void* dk, void* dv, cudaStream_t st) {
+    constexpr size_t smem_q = sizeof(float) * 4 * kTile * ld_of<HD>();
+    constexpr size_t smem_kv = smem_q + sizeof(float) * 2 * kTile * kLdP;
+    cudaError_t e = big_smem(attn_dq_simt_kernel<T, HD>, smem_q);
+    if (e == cudaSuccess) e = big_smem(attn_dkv_simt_kernel<T, HD>, smem_kv);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (p.N + kTile - 1) / kTile;
+    DC_LAUNCH(kAttnSimtDkv, st, attn_dkv_simt_kernel<T, HD><<<(unsigned)(tiles * p.kvh), kThreads, smem_kv, st>>>(
+                                    static_cast<const T*>(d_o), static_cast<const T*>(q), static_cast<const T*>(k),
+                                    static_cast<const T*>(v), lse, delta, static_cast<T*>(dk), static_cast<T*>(dv),
+                                    args_of(p), vec_ok(p, true)));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    DC_LAUNCH(kAttnSimtDq, st, attn_dq_simt_kernel<T, HD><<<(unsigned)(tiles * p.heads), kThreads, smem_q, st>>>(
+                                   static_cast<const T*>(d_o), static_cast<const T*>(q), static_cast<const T*>(k),
+                                   static_cast<const T*>(v), lse, delta, static_cast<T*>(dq), args_of(p),
+                                   vec_ok(p, true)));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attn_simt_fwd(const AttnProb& p, const void* q, const void* k, const void* v, void* o, float* lse,
+                          cudaStream_t st) {
+    if (p.dtype == 0)
+        return p.hd <= 64 ? fwd_t<float, 64>(p, q, k, v, o, lse, st) : fwd_t<float, 128>(p, q, k, v, o, lse, st);
+    return p.hd <= 64 ? fwd_t<__nv_bfloat16, 64>(p, q, k, v, o, lse, st)
+                      : fwd_t<__nv_bfloat16, 128>(p, q, k, v, o, lse, st);
+}
+
+cudaError_t attn_simt_bwd(const AttnProb& p, const void* d_o, const void* q, const void* k, const void* v,
+                          const float* lse, const float* delta, void* dq, void* dk, void* dv, cudaStream_t st) {
+    if (p.dtype == 0)
+        return p.hd <= 64 ? bwd_t<float, 64>(p, d_o, q, k, v, lse, delta, dq, dk, dv, st)
+                          : bwd_t<float, 128>(p, d_o, q, k, v, lse, delta, dq, dk, dv, st);
+    return p.hd <= 64 ? bwd_t<__nv_bfloat16, 64>(p, d_o, q, k, v, lse, delta, dq, dk, dv, st)
+                      : bwd_t<__nv_bfloat16, 128>(p, d_o, q, k, v, lse, delta, dq, dk, dv, st);
+}
+
+cudaError_t attn_delta(const AttnProb& p, const void* d_o, const void* o, float* delta, cudaStream_t st) {
+    const int64_t warps = p.N * p.heads;
+    const unsigned grid = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
+    if (p.dtype == 0)
+        DC_LAUNCH(kAttnDelta, st, attn_delta_kernel<float><<<grid, kThreads, 0, st>>>(
+                                      static_cast<const float*>(d_o), static_cast<const float*>(o), p.dos, p.os, p.N,
+                                      p.heads, p.hd, delta));
+    else
+        DC_LAUNCH(kAttnDelta, st, attn_delta_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(
+                                      static_cast<const __nv_bfloat16*>(d_o), static_cast<const __nv_bfloat16*>(o),
+                                      p.dos, p.os, p.N, p.heads, p.hd, delta));
+    return cudaGetLastError();
+}
+
+}  // namespace dynconv

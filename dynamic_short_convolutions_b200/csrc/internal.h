@@ -11,7 +11,8 @@ namespace dynconv {
 enum : uint32_t {
     kErrBadSeqlens = 1u,   // cu_seqlens not 0 ... N, non-decreasing
     kErrWaitTimeout = 2u,  // an mbarrier wait ran out of its iteration limit
-    kErrRopePos = 4u,      // a packed document longer than the RoPE table
+    kErrRopePos = 4u,      // a packed document longer than the RoPE table, or a position outside it
+    kErrCacheLen = 8u,     // cached plus new tokens above the cache's capacity
 };
 
 // A validated problem: all sizes resolved, strides filled in.

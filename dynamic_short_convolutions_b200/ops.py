@@ -3,6 +3,7 @@ autograd Function.  Marshalling only; the arithmetic runs in libdynconv.so.
 """
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import torch
@@ -18,13 +19,96 @@ def _dtype_code(t: torch.Tensor) -> int:
     raise TypeError(f"storage dtype must be bf16 or fp32, got {t.dtype}")
 
 
-def rope_table(max_pos: int, head_dim: int, base: float = 10000.0, device=None) -> torch.Tensor:
+def rope_table(max_pos: int, head_dim: int, base: float = 10000.0, device=None, scaling: Optional[str] = None,
+               factor: float = 1.0, original_max_pos: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
+               gain: Optional[float] = None) -> torch.Tensor:
     """The RoPE table the C ABI reads: fp32 [max_pos, head_dim] with entries 2i, 2i+1 of row p
-    the cosine and sine of p * base^(-2i/head_dim) (RoFormer's angles), computed once in fp64."""
+    the cosine and sine of p * base^(-2i/head_dim) (RoFormer's angles), computed once in fp64.
+    For a part of the head, head_dim is the number of rotated channels.
+
+    ``scaling`` stretches the table to contexts ``factor`` times the ``original_max_pos`` of training:
+    ``"linear"`` divides every angle by factor (position interpolation); ``"ntk"`` raises the base by
+    factor^(d/(d-2)), which leaves the fastest pair and slows the slowest by factor; ``"yarn"`` divides
+    the angles of pairs that turn at most ``beta_slow`` times over original_max_pos by factor, leaves
+    those of ``beta_fast`` turns and more, ramps in between, and multiplies cosine and sine by ``gain``
+    (0.1 ln factor + 1 unless given)."""
+    if head_dim < 2 or head_dim % 2:
+        raise ValueError(f"the rotated channels must be even and at least 2, got {head_dim}")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    if factor < 1.0:
+        raise ValueError(f"factor must be at least 1, got {factor}")
     p = torch.arange(max_pos, dtype=torch.float64).unsqueeze(1)
+    if scaling == "ntk" and head_dim > 2:
+        base = base * factor ** (head_dim / (head_dim - 2))
     theta = base ** (-torch.arange(0, head_dim, 2, dtype=torch.float64) / head_dim)
+    scale = 1.0 if gain is None else gain
+    if scaling == "linear":
+        theta = theta / factor
+    elif scaling == "yarn":
+        # the pair that makes `turns` turns over original_max_pos positions
+        at = [head_dim * math.log(original_max_pos / (turns * 2 * math.pi)) / (2 * math.log(base))
+              for turns in (beta_fast, beta_slow)]
+        low, high = max(math.floor(at[0]), 0), min(math.ceil(at[1]), head_dim - 1)
+        slow = ((torch.arange(head_dim // 2, dtype=torch.float64) - low) / max(high - low, 1e-3)).clamp(0, 1)
+        theta = theta * (1 - slow) + theta / factor * slow
+        if gain is None:
+            scale = 0.1 * math.log(factor) + 1.0
     ang = p * theta
-    return torch.stack((ang.cos(), ang.sin()), dim=-1).reshape(max_pos, head_dim).float().to(device or "cuda")
+    table = torch.stack((ang.cos(), ang.sin()), dim=-1).reshape(max_pos, head_dim)
+    return (table if scale == 1.0 else scale * table).float().to(device or "cuda")
+
+
+def _rows(t: torch.Tensor, name: str, rows: int, width: int, dtype: torch.dtype, stride: int) -> None:
+    """A tensor of `rows` rows of `width` contiguous elements, `stride` (0: width) elements apart."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"{name} must be [{rows}, {width}], got {list(t.shape)}")
+    if (width > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (stride or width)):
+        raise ValueError(f"{name} must have contiguous channels and a row stride of {stride or width}, "
+                         f"got strides {t.stride()}")
+
+
+def _ints(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape=None) -> None:
+    if t is None:
+        return
+    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor" + (f" of shape {list(shape)}" if shape else "")
+                         + f", got {t.dtype} {list(t.shape)}")
+
+
+def _cu(t: Optional[torch.Tensor]) -> None:
+    _ints(t, "cu_seqlens", torch.int32)
+    if t is not None and (t.dim() != 1 or t.numel() < 2):
+        raise ValueError(f"cu_seqlens must be [documents + 1], got {list(t.shape)}")
+
+
+def _one_device(device: torch.device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {t.device} and {device}: a call's tensors must be on its plan's device")
+
+
+def _device(device) -> torch.device:
+    d = torch.device(device or "cuda")
+    return torch.device(d.type, torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+
+
+class _On:
+    """Makes a CUDA device current for a call where it is not (kernels launch on the current device)."""
+
+    def __init__(self, device: torch.device):
+        self.to = device.index if device.index is not None and device.index != torch.cuda.current_device() else None
+
+    def __enter__(self):
+        if self.to is not None:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.to)
+
+    def __exit__(self, *exc):
+        if self.to is not None:
+            torch.cuda.set_device(self.back)
 
 
 class DynConvPlan:
@@ -148,3 +232,175 @@ def dynamic_short_conv(u: torch.Tensor, h: torch.Tensor, A: Optional[torch.Tenso
     """Functional form with autograd: u [N, C] token-major (N = batch * seqlen) or
     [batch, C, seqlen] channel-first; h [N, d]."""
     return DynamicShortConv.apply(u, h, A, B_or_W, ksize, head_dim, batch, cu_seqlens, algo)
+
+
+class RopePlan:
+    """Rotary positions for rows of ``heads`` heads of ``head_dim`` channels, the first
+    ``table.shape[1]`` channels of each head rotated.
+
+    x and y: [N, heads * head_dim], N = batch * seqlen (rows may be strided, so x may be the Q and K
+    columns of a fused QKV buffer).  A token's position is its place in its sequence, its packed
+    document (``cu_seqlens``, batch = 1) or ``positions`` (int32 [N]).  ``table``: fp32
+    [max_pos, rotated channels], see :func:`rope_table`."""
+
+    def __init__(self, dtype: torch.dtype, batch: int, seqlen: int, heads: int, head_dim: int, table: torch.Tensor,
+                 layout: int = L.ROPE_INTERLEAVED, x_row_stride: int = 0, y_row_stride: int = 0, device=None):
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"storage dtype must be bf16 or fp32, got {dtype}")
+        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
+            raise ValueError("table must be a contiguous fp32 [max_pos, rotated channels] tensor")
+        self.device = table.device if device is None else _device(device)
+        _one_device(self.device, table)
+        self.table = table                      # kept alive: the descriptors hold its address
+        code = L.BF16 if dtype == torch.bfloat16 else L.F32
+        self.desc = [L.make_rope_desc(code, layout, batch, seqlen, heads, head_dim, table, inv, x_row_stride,
+                                      y_row_stride) for inv in (0, 1)]
+        self.ws = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        self.dtype, self.N, self.width = dtype, batch * seqlen, heads * head_dim
+        self.strides = (x_row_stride, y_row_stride)
+
+    def apply(self, x, y=None, positions=None, cu_seqlens=None, inverse: bool = False, stream=None):
+        """y = R(p) x, or the transposed rotation (the backward).  ``y=x`` rotates in place."""
+        if y is None:
+            if self.strides[1] not in (0, self.width):
+                raise ValueError("a plan with a strided y needs the y to write")
+            y = torch.empty((self.N, self.width), dtype=self.dtype, device=self.device)
+        _rows(x, "x", self.N, self.width, self.dtype, self.strides[0])
+        _rows(y, "y", self.N, self.width, self.dtype, self.strides[1])
+        _ints(positions, "positions", torch.int32, (self.N,))
+        _cu(cu_seqlens)
+        _one_device(self.device, x, y, positions, cu_seqlens)
+        with _On(self.device):
+            L.dynconv_rope(self.desc[int(inverse)], cu_seqlens, positions, x, y, self.ws, stream)
+        return y
+
+
+class AttnPlan:
+    """Causal attention for one problem shape: q [N, heads * head_dim], k and v
+    [N, kv_heads * head_dim], N = batch * seqlen, rows optionally strided (column slices of a fused
+    QKV buffer).  For packed documents pass ``cu_seqlens`` (int32 device tensor [docs + 1]) and
+    batch = 1, seqlen = N.  Query head i reads key/value head i // (heads // kv_heads)."""
+
+    def __init__(self, dtype: torch.dtype, batch: int, seqlen: int, heads: int, kv_heads: int, head_dim: int,
+                 scale: float = 0.0, q_row_stride: int = 0, k_row_stride: int = 0, v_row_stride: int = 0,
+                 dq_row_stride: int = 0, dk_row_stride: int = 0, dv_row_stride: int = 0, algo: int = L.ALGO_AUTO,
+                 device=None):
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"storage dtype must be bf16 or fp32, got {dtype}")
+        self.desc = L.make_attn_desc(L.BF16 if dtype == torch.bfloat16 else L.F32, batch, seqlen, heads, kv_heads,
+                                     head_dim, algo, scale, q_row_stride, k_row_stride, v_row_stride, 0, 0,
+                                     dq_row_stride, dk_row_stride, dv_row_stride)
+        nbytes = L.dynconv_attn_workspace_bytes(self.desc)
+        if nbytes == 0:
+            raise L.DynConvError(1, L.dynconv_last_error() or "invalid descriptor")
+        self.device = _device(device)
+        self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self.dtype, self.N, self.heads = dtype, batch * seqlen, heads
+        self.wq, self.wk = heads * head_dim, kv_heads * head_dim
+        self.strides = (q_row_stride, k_row_stride, v_row_stride)
+        self.grad_strides = (dq_row_stride, dk_row_stride, dv_row_stride)
+
+    def _inputs(self, q, k, v, cu_seqlens):
+        _rows(q, "q", self.N, self.wq, self.dtype, self.strides[0])
+        _rows(k, "k", self.N, self.wk, self.dtype, self.strides[1])
+        _rows(v, "v", self.N, self.wk, self.dtype, self.strides[2])
+        _cu(cu_seqlens)
+        _one_device(self.device, q, k, v, cu_seqlens)
+
+    def forward(self, q, k, v, cu_seqlens=None, o=None, want_lse: bool = False, stream=None):
+        """o [N, heads * head_dim]; with ``want_lse`` (o, lse), lse fp32 [heads, N] for :meth:`backward`."""
+        self._inputs(q, k, v, cu_seqlens)
+        if o is None:
+            o = torch.empty((self.N, self.wq), dtype=self.dtype, device=self.device)
+        _rows(o, "o", self.N, self.wq, self.dtype, 0)
+        _one_device(self.device, o)
+        lse = torch.empty((self.heads, self.N), dtype=torch.float32, device=self.device) if want_lse else None
+        with _On(self.device):
+            L.dynconv_attn_fwd(self.desc, cu_seqlens, q, k, v, o, lse, self.ws, stream)
+        return (o, lse) if want_lse else o
+
+    def backward(self, d_o, q, k, v, o, lse, cu_seqlens=None, out=None, stream=None):
+        """{"dq", "dk", "dv"} from the forward's o and lse; ``out`` gives tensors to write (dq_row_stride and
+        so on apart), for instance column slices of one gradient buffer."""
+        self._inputs(q, k, v, cu_seqlens)
+        if out is None:
+            if any(self.grad_strides):
+                raise ValueError("a plan with strided gradients needs the tensors to write (out)")
+            out = {"dq": torch.empty((self.N, self.wq), dtype=self.dtype, device=self.device),
+                   "dk": torch.empty((self.N, self.wk), dtype=self.dtype, device=self.device),
+                   "dv": torch.empty((self.N, self.wk), dtype=self.dtype, device=self.device)}
+        for name, t, width, stride in (("d_o", d_o, self.wq, 0), ("o", o, self.wq, 0),
+                                       ("dq", out["dq"], self.wq, self.grad_strides[0]),
+                                       ("dk", out["dk"], self.wk, self.grad_strides[1]),
+                                       ("dv", out["dv"], self.wk, self.grad_strides[2])):
+            _rows(t, name, self.N, width, self.dtype, stride)
+            _one_device(self.device, t)
+        _ints(lse, "lse", torch.float32, (self.heads, self.N))
+        _one_device(self.device, lse)
+        with _On(self.device):
+            L.dynconv_attn_bwd(self.desc, cu_seqlens, d_o, q, k, v, o, lse, out["dq"], out["dk"], out["dv"], self.ws,
+                               stream)
+        return out
+
+
+class QKVAttention(torch.autograd.Function):
+    """Causal attention of a fused QKV buffer, with the rotation of Q and K where a table is given.
+
+    qkv [N, (heads + 2 kv_heads) * head_dim] is what the QKV convolution leaves; the backward writes
+    one buffer of that shape, which the convolution's backward takes as its g."""
+
+    @staticmethod
+    def forward(ctx, qkv, table, heads: int, kv_heads: int, head_dim: int, batch: int, cu_seqlens, scale: float,
+                layout: int, algo: int):
+        N, C = qkv.shape
+        wq, wk = heads * head_dim, kv_heads * head_dim
+        if C != wq + 2 * wk:
+            raise ValueError(f"qkv must be [N, (heads + 2 kv_heads) * head_dim] = [N, {wq + 2 * wk}], got {list(qkv.shape)}")
+        if N % batch:
+            raise ValueError(f"{N} tokens are not {batch} sequences of one length")
+        if qkv.stride(1) != 1 or (N > 1 and qkv.stride(0) < C):
+            qkv = qkv.contiguous()
+        row = qkv.stride(0) if N > 1 else C
+        qk, rope, qk_row = qkv[:, :wq + wk], None, row
+        if table is not None:
+            rope = (batch, N // batch, heads + kv_heads, head_dim, table, layout)
+            qk = RopePlan(qkv.dtype, *rope, x_row_stride=row, device=qkv.device).apply(qk, cu_seqlens=cu_seqlens)
+            qk_row = wq + wk
+        q, k, v = qk[:, :wq], qk[:, wq:], qkv[:, wq + wk:]
+        plan = AttnPlan(qkv.dtype, batch, N // batch, heads, kv_heads, head_dim, scale, qk_row, qk_row, row, C, C, C,
+                        algo=algo, device=qkv.device)
+        o, lse = plan.forward(q, k, v, cu_seqlens, want_lse=True)
+        ctx.plan, ctx.rope, ctx.width = plan, rope, (C, wq, wk)
+        ctx.save_for_backward(qkv, qk, o, lse, cu_seqlens)
+        return o
+
+    @staticmethod
+    def backward(ctx, go):
+        qkv, qk, o, lse, cu_seqlens = ctx.saved_tensors
+        C, wq, wk = ctx.width
+        d = torch.empty((qkv.shape[0], C), dtype=qkv.dtype, device=qkv.device)
+        out = {"dq": d[:, :wq], "dk": d[:, wq:wq + wk], "dv": d[:, wq + wk:]}
+        ctx.plan.backward(go.contiguous(), qk[:, :wq], qk[:, wq:wq + wk], qkv[:, wq + wk:], o, lse, cu_seqlens, out)
+        if ctx.rope is not None:
+            RopePlan(qkv.dtype, *ctx.rope, x_row_stride=C, y_row_stride=C, device=qkv.device).apply(
+                d[:, :wq + wk], y=d[:, :wq + wk], cu_seqlens=cu_seqlens, inverse=True)
+        return d, None, None, None, None, None, None, None, None, None
+
+
+def qkv_attention(qkv: torch.Tensor, heads: int, kv_heads: int, head_dim: int, table: Optional[torch.Tensor] = None,
+                  batch: int = 1, cu_seqlens: Optional[torch.Tensor] = None, scale: float = 0.0,
+                  layout: int = L.ROPE_INTERLEAVED, algo: int = L.ALGO_AUTO) -> torch.Tensor:
+    """Functional form with autograd: rotary positions (``table``, see :func:`rope_table`) on the Q and K
+    columns of qkv [N, (heads + 2 kv_heads) * head_dim], then causal attention; o [N, heads * head_dim]."""
+    return QKVAttention.apply(qkv, table, heads, kv_heads, head_dim, batch, cu_seqlens, scale, layout, algo)
+
+
+def dynamic_conv_attention(u: torch.Tensor, h: torch.Tensor, A: Optional[torch.Tensor], B_or_W: torch.Tensor,
+                           ksize: int, heads: int, kv_heads: int, head_dim: int, table: Optional[torch.Tensor] = None,
+                           filter_head_dim: int = 0, batch: int = 1, cu_seqlens: Optional[torch.Tensor] = None,
+                           scale: float = 0.0, layout: int = L.ROPE_INTERLEAVED, algo: int = L.ALGO_AUTO) -> torch.Tensor:
+    """The QKV placement as a layer runs it: the dynamic short convolution of the fused QKV rows u [N, C]
+    (C = (heads + 2 kv_heads) * head_dim; head-wise filters where filter_head_dim > 0), rotary positions on
+    Q and K, causal attention.  With autograd; o [N, heads * head_dim]."""
+    y = dynamic_short_conv(u, h, A, B_or_W, ksize, filter_head_dim, batch, cu_seqlens, algo)
+    return qkv_attention(y, heads, kv_heads, head_dim, table, batch, cu_seqlens, scale, layout, algo)
