@@ -208,7 +208,9 @@ dynconv_status dynconv_attn_fwd(const dynconv_attn_desc* desc, const int32_t* cu
     if (cu_seqlens &&
         (s = cuda_status(launch_check_seqlens(cu_seqlens, n_docs, p.N, err_of(ws), st), "cu_seqlens check")))
         return s;
-    return cuda_status(attn_simt_fwd(p, q, k, v, o, lse, st), "attention forward launch");
+    return cuda_status(attn_tc(p) ? attn_tc_fwd(p, q, k, v, o, lse, err_of(ws), st)
+                                  : attn_simt_fwd(p, q, k, v, o, lse, st),
+                       "attention forward launch");
 }
 
 dynconv_status dynconv_attn_bwd(const dynconv_attn_desc* desc, const int32_t* cu_seqlens, int64_t n_docs,
@@ -238,8 +240,3 @@ dynconv_status dynconv_attn_bwd(const dynconv_attn_desc* desc, const int32_t* cu
 }
 
 }  // extern "C"
-
-namespace dynconv {
-// No tensor-core kernels yet.
-const char* attn_tc_refusal(const AttnProb&) { return "not built"; }
-}  // namespace dynconv
