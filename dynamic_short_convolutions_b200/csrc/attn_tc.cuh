@@ -94,11 +94,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&f)[32]) 
           "r"(__float_as_uint(f[29])), "r"(__float_as_uint(f[30])), "r"(__float_as_uint(f[31])), "r"(taddr)
         : "memory");
 }
-// Moves registers between warpgroups: every warp of a warpgroup calls one of the two.
-template <int R>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -120,6 +115,22 @@ __device__ __forceinline__ void fma2(float& x, float& y, float f, float g) {
     asm("mov.b64 %0, {%1, %1};" : "=l"(b) : "f"(f));
     asm("mov.b64 %0, {%1, %1};" : "=l"(c) : "f"(g));
     asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a) : "l"(b), "l"(c));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+}
+// (x, y) = (x f + g0, y f + g1)
+__device__ __forceinline__ void fma2v(float& x, float& y, float f, float g0, float g1) {
+    uint64_t a, b, c;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(b) : "f"(f));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(g0), "f"(g1));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a) : "l"(b), "l"(c));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+}
+__device__ __forceinline__ void mul2v(float& x, float& y, float f0, float f1) {
+    uint64_t a, b;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(x), "f"(y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(f0), "f"(f1));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
 }
 __device__ __forceinline__ void add2(float& x, float& y, float a0, float a1) {
