@@ -14,6 +14,6 @@ from ._lib import (  # noqa: F401
     dynconv_workspace_bytes, load, make_desc,
 )
 from .ops import (  # noqa: F401
-    AttnPlan, DynamicShortConv, DynConvPlan, QKVAttention, RopePlan, dynamic_conv_attention, dynamic_short_conv,
-    qkv_attention, rope_table,
+    AttnDecoder, AttnPlan, DynamicShortConv, DynConvPlan, QKVAttention, RopePlan, dynamic_conv_attention,
+    dynamic_short_conv, qkv_attention, rope_table,
 )

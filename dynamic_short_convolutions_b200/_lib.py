@@ -32,7 +32,7 @@ EXPORTS = ("dynconv_workspace_bytes", "dynconv_fwd", "dynconv_fwd_varlen", "dync
            "dynconv_profile_enable", "dynconv_profile_read", "dynconv_selftest_umma", "dynconv_fwd_noalloc",
            "dynconv_decode_step", "dynconv_noalloc_status", "dynconv_query_family", "dynconv_selftest_wait",
            "dynconv_rope", "dynconv_attn_workspace_bytes", "dynconv_attn_query_family", "dynconv_attn_fwd",
-           "dynconv_attn_bwd")
+           "dynconv_attn_bwd", "dynconv_attn_decode_workspace_bytes", "dynconv_attn_decode")
 
 
 class DynConvError(RuntimeError):
@@ -68,6 +68,15 @@ class dynconv_attn_desc(ctypes.Structure):
                 ("head_dim", ctypes.c_int64), ("q_row_stride", ctypes.c_int64), ("k_row_stride", ctypes.c_int64),
                 ("v_row_stride", ctypes.c_int64), ("o_row_stride", ctypes.c_int64), ("do_row_stride", ctypes.c_int64),
                 ("dq_row_stride", ctypes.c_int64), ("dk_row_stride", ctypes.c_int64), ("dv_row_stride", ctypes.c_int64),
+                ("scale", ctypes.c_float)]
+
+
+class dynconv_attn_decode_desc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("rope_layout", ctypes.c_int32), ("batch", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("heads", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("max_len", ctypes.c_int64), ("q_row_stride", ctypes.c_int64),
+                ("k_row_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64), ("o_row_stride", ctypes.c_int64),
+                ("rope_dim", ctypes.c_int64), ("rope_max_pos", ctypes.c_int64), ("rope_cos_sin", ctypes.c_void_p),
                 ("scale", ctypes.c_float)]
 
 
@@ -121,7 +130,12 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.dynconv_attn_query_family.argtypes = [AD, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
     lib.dynconv_attn_fwd.argtypes = [AD, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.dynconv_attn_bwd.argtypes = [AD, vp, i64] + [vp] * 10 + [sz, vp]
-    for f in (lib.dynconv_rope, lib.dynconv_attn_query_family, lib.dynconv_attn_fwd, lib.dynconv_attn_bwd):
+    DD = ctypes.POINTER(dynconv_attn_decode_desc)
+    lib.dynconv_attn_decode_workspace_bytes.argtypes = [DD]
+    lib.dynconv_attn_decode_workspace_bytes.restype = sz
+    lib.dynconv_attn_decode.argtypes = [DD] + [vp] * 9 + [sz, vp]
+    for f in (lib.dynconv_rope, lib.dynconv_attn_query_family, lib.dynconv_attn_fwd, lib.dynconv_attn_bwd,
+              lib.dynconv_attn_decode):
         f.restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -171,6 +185,17 @@ def make_attn_desc(dtype: int, batch: int, seqlen: int, heads: int, kv_heads: in
     return dynconv_attn_desc(dtype, algo, batch, seqlen, heads, kv_heads, head_dim, q_row_stride, k_row_stride,
                              v_row_stride, o_row_stride, do_row_stride, dq_row_stride, dk_row_stride, dv_row_stride,
                              scale)
+
+
+def make_attn_decode_desc(dtype: int, batch: int, tokens: int, heads: int, kv_heads: int, head_dim: int, max_len: int,
+                          scale: float = 0.0, rope_table: Optional[torch.Tensor] = None,
+                          rope_layout: int = ROPE_INTERLEAVED, q_row_stride: int = 0, k_row_stride: int = 0,
+                          v_row_stride: int = 0, o_row_stride: int = 0) -> dynconv_attn_decode_desc:
+    """rope_table: device fp32 [max_pos, rotated channels], kept alive by the caller; None: no rotation."""
+    rot, top, at = (0, 0, None) if rope_table is None else (
+        int(rope_table.shape[1]), int(rope_table.shape[0]), ctypes.c_void_p(rope_table.data_ptr()))
+    return dynconv_attn_decode_desc(dtype, rope_layout, batch, tokens, heads, kv_heads, head_dim, max_len, q_row_stride,
+                                    k_row_stride, v_row_stride, o_row_stride, rot, top, at, scale)
 
 
 def dynconv_workspace_bytes(desc: dynconv_desc) -> int:
@@ -240,6 +265,16 @@ def dynconv_attn_bwd(desc, cu_seqlens, d_o, q, k, v, o, lse, dq, dk, dv, ws, str
     _check(load().dynconv_attn_bwd(ctypes.byref(desc), _ptr(cu_seqlens), _docs(cu_seqlens), _ptr(d_o), _ptr(q),
                                    _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws),
                                    ws.numel() * ws.element_size(), _stream(stream, q)))
+
+
+def dynconv_attn_decode_workspace_bytes(desc: dynconv_attn_decode_desc) -> int:
+    return int(load().dynconv_attn_decode_workspace_bytes(ctypes.byref(desc)))
+
+
+def dynconv_attn_decode(desc, q, k, v, k_cache, v_cache, lens, ancestors, o, ws, stream=None):
+    _check(load().dynconv_attn_decode(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
+                                      _ptr(lens), _ptr(ancestors), _ptr(o), _ptr(ws), ws.numel() * ws.element_size(),
+                                      _stream(stream, q)))
 
 
 def dynconv_attn_query_family(desc: dynconv_attn_desc):

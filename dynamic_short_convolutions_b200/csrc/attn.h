@@ -52,4 +52,22 @@ cudaError_t attn_tc_bwd(const AttnProb& p, const void* d_o, const void* q, const
 // D[h][n] = d_o[n, h] . o[n, h], fp32.
 cudaError_t attn_delta(const AttnProb& p, const void* d_o, const void* o, float* delta, cudaStream_t st);
 
+// A validated step of new or drafted tokens over a cache.
+struct DecodeProb {
+    int dtype;
+    int64_t batch, max_len;
+    int M, heads, kvh, group, hd;                 // M tokens per sequence
+    int64_t qs, ks, vs, os;
+    int rot, half;                                // rotated channels (0: none), pair layout
+    int64_t max_pos;
+    const float* cs;
+    float scale;
+};
+int64_t attn_decode_groups(const DecodeProb& p);  // blocks before the cache is split into runs: one counter each
+int attn_decode_splits(const DecodeProb& p);
+size_t attn_decode_part_bytes(const DecodeProb& p);
+cudaError_t attn_decode(const DecodeProb& p, const void* q, const void* k, const void* v, void* k_cache, void* v_cache,
+                        const int32_t* lens, const uint64_t* tree, void* o, uint32_t* err, uint32_t* count, float* part,
+                        cudaStream_t st);
+
 }  // namespace dynconv

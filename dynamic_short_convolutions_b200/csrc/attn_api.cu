@@ -101,6 +101,69 @@ dynconv_status make_attn(const dynconv_attn_desc* d, AttnProb* p) {
     return DYNCONV_OK;
 }
 
+dynconv_status make_decode(const dynconv_attn_decode_desc* d, DecodeProb* p) {
+    *p = DecodeProb{};
+    if (!d) return invalid("desc is NULL");
+    if (d->dtype != DYNCONV_F32 && d->dtype != DYNCONV_BF16) { set_error("bad dtype %d", d->dtype); return DYNCONV_ERR_INVALID; }
+    if (d->batch < 0) return invalid("negative batch");
+    if (d->tokens < 1) return invalid("tokens must be >= 1");
+    if (d->tokens > 64) { set_error("%lld tokens > 64 are not supported", (long long)d->tokens); return DYNCONV_ERR_UNSUPPORTED; }
+    if (d->heads < 1 || d->kv_heads < 1 || d->heads % d->kv_heads) return invalid("kv_heads must divide heads");
+    if (d->heads > 65535) { set_error("heads above 65535 are not supported"); return DYNCONV_ERR_UNSUPPORTED; }
+    const int64_t es = d->dtype == DYNCONV_BF16 ? 2 : 4, vec = 16 / es;
+    if (d->head_dim < 1) return invalid("head_dim must be >= 1");
+    if (d->head_dim > 128 || d->head_dim % vec) {
+        set_error("head_dim %lld: a multiple of 16 bytes up to 128 channels is supported", (long long)d->head_dim);
+        return DYNCONV_ERR_UNSUPPORTED;
+    }
+    if (d->max_len < d->tokens) return invalid("max_len must hold the new tokens");
+    if (d->max_len > INT32_MAX) { set_error("max_len must be below 2^31"); return DYNCONV_ERR_UNSUPPORTED; }
+    if (!fits(std::max<int64_t>(d->batch, 1), d->kv_heads * d->head_dim * es, d->max_len)) return invalid("a cache passes 2^56 bytes");
+    if (!(d->scale >= 0.f) || std::isinf(d->scale)) return invalid("scale must be positive and finite (0: 1 / sqrt(head_dim))");
+    const int64_t wq = d->heads * d->head_dim, wk = d->kv_heads * d->head_dim;
+    int64_t N;
+    if (__builtin_mul_overflow(d->batch, d->tokens, &N) || !stride_of(d->q_row_stride, wq, N, es, &p->qs) ||
+        !stride_of(d->k_row_stride, wk, N, es, &p->ks) || !stride_of(d->v_row_stride, wk, N, es, &p->vs) ||
+        !stride_of(d->o_row_stride, wq, N, es, &p->os))
+        return invalid("a row stride is below its row's width, or an operand passes 2^56 bytes");
+    if (p->qs % vec || p->ks % vec || p->vs % vec || p->os % vec) return invalid("row strides must be multiples of 16 bytes");
+    if (d->rope_dim < 0 || d->rope_dim % 2 || d->rope_dim > d->head_dim) return invalid("rope_dim must be even, 0 to head_dim");
+    if (d->rope_dim > 0) {
+        if (d->rope_layout != DYNCONV_ROPE_INTERLEAVED && d->rope_layout != DYNCONV_ROPE_HALF) { set_error("bad layout %d", d->rope_layout); return DYNCONV_ERR_INVALID; }
+        if (d->rope_max_pos < 1 || !fits(d->rope_max_pos, d->rope_dim, 4)) return invalid("rope_max_pos must be >= 1 and the table below 2^56 bytes");
+    }
+    p->dtype = d->dtype;
+    p->batch = d->batch;
+    p->max_len = d->max_len;
+    p->M = (int)d->tokens;
+    p->heads = (int)d->heads;
+    p->kvh = (int)d->kv_heads;
+    p->group = p->heads / p->kvh;
+    p->hd = (int)d->head_dim;
+    p->rot = (int)d->rope_dim;
+    p->half = d->rope_layout == DYNCONV_ROPE_HALF;
+    p->max_pos = d->rope_max_pos;
+    p->cs = d->rope_cos_sin;
+    p->scale = d->scale > 0.f ? d->scale : (float)(1.0 / std::sqrt((double)d->head_dim));
+    if (!fits(std::max<int64_t>(d->batch, 1), d->heads * d->tokens, 64) || attn_decode_groups(*p) > (int64_t(1) << 24)) {
+        set_error("batch * kv_heads beyond the grid are not supported");
+        return DYNCONV_ERR_UNSUPPORTED;
+    }
+    return DYNCONV_OK;
+}
+
+// Workspace of a step: the error word, a counter per group of runs, the runs' parts.
+struct DecodeWs {
+    size_t count, part, total;
+};
+DecodeWs decode_ws(const DecodeProb& p) {
+    DecodeWs w{};
+    w.count = 256;
+    w.part = w.count + ((size_t)attn_decode_groups(p) * sizeof(uint32_t) + 255) / 256 * 256;
+    w.total = w.part + attn_decode_part_bytes(p);
+    return w;
+}
+
 bool attn_tc(const AttnProb& p) { return p.algo != DYNCONV_ALGO_SIMT && attn_tc_refusal(p) == nullptr; }
 
 uint32_t* err_of(void* ws) { return static_cast<uint32_t*>(ws); }
@@ -239,6 +302,35 @@ dynconv_status dynconv_attn_bwd(const dynconv_attn_desc* desc, const int32_t* cu
     return cuda_status(attn_tc(p) ? attn_tc_bwd(p, d_o, q, k, v, lse, delta, dq, dk, dv, err_of(ws), st)
                                   : attn_simt_bwd(p, d_o, q, k, v, lse, delta, dq, dk, dv, st),
                        "attention backward launch");
+}
+
+size_t dynconv_attn_decode_workspace_bytes(const dynconv_attn_decode_desc* desc) {
+    set_error("%s", "");
+    DecodeProb p;
+    if (make_decode(desc, &p) != DYNCONV_OK) return 0;
+    return decode_ws(p).total;
+}
+
+dynconv_status dynconv_attn_decode(const dynconv_attn_decode_desc* desc, const void* q, const void* k, const void* v,
+                                   void* k_cache, void* v_cache, const int32_t* lens, const uint64_t* ancestors,
+                                   void* o, void* ws, size_t ws_bytes, void* stream) {
+    set_error("%s", "");
+    DecodeProb p;
+    dynconv_status s = make_decode(desc, &p);
+    if (s != DYNCONV_OK) return s;
+    if (p.batch == 0) return DYNCONV_OK;
+    const DecodeWs w = decode_ws(p);
+    if ((s = validate_ptr(q, "q", true)) || (s = validate_ptr(k, "k", true)) || (s = validate_ptr(v, "v", true)) ||
+        (s = validate_ptr(k_cache, "k_cache", true)) || (s = validate_ptr(v_cache, "v_cache", true)) ||
+        (s = validate_ptr(lens, "lens", true)) || (s = validate_ptr(ancestors, "ancestors", false)) ||
+        (s = validate_ptr(p.cs, "rope_cos_sin", p.rot > 0)) || (s = validate_ptr(o, "o", true)) ||
+        (s = check_ws(ws, ws_bytes, w.total)))
+        return s;
+    char* base = static_cast<char*>(ws);
+    return cuda_status(attn_decode(p, q, k, v, k_cache, v_cache, lens, ancestors, o, err_of(ws),
+                                   reinterpret_cast<uint32_t*>(base + w.count), reinterpret_cast<float*>(base + w.part),
+                                   static_cast<cudaStream_t>(stream)),
+                       "attention decode launch");
 }
 
 }  // extern "C"

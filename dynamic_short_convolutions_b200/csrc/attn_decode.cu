@@ -1,0 +1,690 @@
+// attn_decode.cu -- attention of new or drafted tokens over a key/value cache, one launch per step:
+// rotation of q and k at their positions, appending to the caches, and
+//   o_m = softmax(scale q_m . k_j) v_j   over the cached rows j < L and the drafted rows m may see.
+//
+// Memory-bound for single tokens: the cache is read once.  A block takes one key/value head of one
+// sequence, so all heads of the group and all its tokens (rows r = m * group + g) share each key and value
+// read, and one of n_split runs of the cached rows, because batch x kv_heads alone would not fill the GPU;
+// runs follow the sequence's own length.  Tiles of K and V come through a ring of 16-byte asynchronous
+// copies (rows beyond L are zero-filled, never read).  The drafted rows are a last tile that the block
+// of the last run fills from k and v (rotated, rounded to the storage type as the cache holds them) and also
+// writes to the cache.  Partial results of the runs are joined in their order by the block that finishes
+// last (a counter per head and sequence, reset by it), so results repeat bitwise.
+//
+// bf16: mma.sync m16n8k16 (the rows are few: a tcgen05 tile of 128 would be mostly empty); P is rounded to
+// bf16 because the tensor cores take it so, its sum is taken before; the rotated q is kept as two bf16
+// (value and remainder), since nothing else rounds it.  fp32: FMAs, a warp per four rows.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/dynconv_attn.h"
+#include "attn.h"
+#include "common.cuh"
+#include "prof.h"
+
+namespace dynconv {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct DecArgs {
+    int M, heads, kvh, group, hd, rows, n_split;     // rows = M * group
+    int64_t max_len, qs, ks, vs, os;
+    int rot, half;
+    int64_t max_pos;
+    const float* cs;
+    const int32_t* lens;
+    const uint64_t* tree;
+    float scale;
+    float* part;                                     // [batch, kvh, row tiles][n_split][rows of a tile][HD + 2]
+    uint32_t* count;                                 // [batch, kvh, row tiles]
+    uint32_t* err;
+};
+
+__device__ __forceinline__ uint32_t smem_at(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// 16 bytes to shared memory; zeros where !real (the address is not read then)
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Which drafted tokens token m sees, as bits, and its depth below the cached tokens.
+__device__ __forceinline__ uint64_t seen_by(const DecArgs& a, int64_t b, int m) {
+    if (a.tree != nullptr) {
+        const uint64_t t = __ldg(reinterpret_cast<const unsigned long long*>(a.tree) + b * a.M + m);
+        return a.M < 64 ? t & ((uint64_t(1) << a.M) - 1) : t;
+    }
+    return m == 63 ? ~uint64_t(0) : (uint64_t(2) << m) - 1;
+}
+__device__ __forceinline__ int depth_of(uint64_t seen, int m) { return __popcll(seen & ~(uint64_t(1) << m)); }
+
+// Channel c of a head's row x, rotated by the table row f (nullptr: as it is).
+template <typename T>
+__device__ __forceinline__ float turned(const T* x, int c, const float* f, int rot, int half) {
+    const float v = to_f32(x[c]);
+    if (f == nullptr || c >= rot) return v;
+    const int hr = rot / 2;
+    const int pair = half ? (c < hr ? c : c - hr) : c / 2;
+    const bool first = half ? c < hr : (c & 1) == 0;
+    const float w = to_f32(x[half ? (first ? c + hr : c - hr) : (c ^ 1)]);
+    const float2 z = __ldg(reinterpret_cast<const float2*>(f) + pair);
+    return first ? v * z.x - w * z.y : w * z.y + v * z.x;
+}
+
+// What a block works on.
+struct Place {
+    int64_t b;
+    int kv, tile, split;           // row tile, run of the cache
+    int64_t len;                   // cached tokens
+    int64_t from, to;              // this run: cached rows from .. to - 1
+    bool tail, idle;
+};
+template <int ROWS>
+__device__ __forceinline__ Place place_of(const DecArgs& a, int tokens_per_tile) {
+    Place p;
+    const int tiles = (a.rows + ROWS - 1) / ROWS;
+    int64_t x = blockIdx.x;
+    p.split = (int)(x % a.n_split);
+    x /= a.n_split;
+    p.tile = (int)(x % tiles);
+    x /= tiles;
+    p.kv = (int)(x % a.kvh);
+    p.b = x / a.kvh;
+    p.len = __ldg(a.lens + p.b);
+    p.idle = p.len < 0;
+    if (p.len + a.M > a.max_len) {
+        p.idle = true;
+        if (threadIdx.x == 0) atomicOr(a.err, kErrCacheLen);
+    }
+    // positions go up to len + the largest depth; checked per token where the table is read
+    const int64_t n = p.idle ? 0 : p.len;
+    const int64_t chunk = (n + (int64_t)a.n_split * tokens_per_tile - 1) / ((int64_t)a.n_split * tokens_per_tile) * tokens_per_tile;
+    p.from = min(n, chunk * p.split);
+    p.to = min(n, p.from + chunk);
+    p.tail = p.split == a.n_split - 1;
+    return p;
+}
+// Whether every token's position lies inside the table.
+__device__ __forceinline__ bool positions_ok(const DecArgs& a, const Place& p) {
+    if (a.rot == 0) return true;
+    bool ok = true;
+    for (int m = threadIdx.x; m < a.M; m += kThreads) ok = ok && p.len + depth_of(seen_by(a, p.b, m), m) < a.max_pos;
+    return __syncthreads_and(ok) != 0;
+}
+
+// Joins NP partial results of ROWS rows in shared memory (o [NP][ROWS][HD] not yet divided by l, m and l [NP][ROWS])
+// and either writes o or leaves this run's part and, as the last block of its rows, joins the runs.
+template <typename T, int HD, int ROWS, int NP>
+__device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const float* so, const float* smax,
+                                       const float* ssum, T* __restrict__ o) {
+    __shared__ int last;
+    constexpr int kLd = HD + 2;
+    const int tiles = (a.rows + ROWS - 1) / ROWS;
+    const int64_t group = (p.b * a.kvh + p.kv) * tiles + p.tile;
+    const int rows = min(ROWS, a.rows - p.tile * ROWS);
+    float* mine = a.part + (group * a.n_split + p.split) * (ROWS * kLd);
+    auto out_at = [&](int r) {
+        const int row = p.tile * ROWS + r, m = row / a.group, g = row - m * a.group;
+        return o + (p.b * a.M + m) * a.os + ((int64_t)p.kv * a.group + g) * a.hd;
+    };
+    for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {
+        const int r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+        float mx = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) mx = fmaxf(mx, smax[n * ROWS + r]);
+        const float use = mx == -INFINITY ? 0.f : mx;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            const float w = exp2f(smax[n * ROWS + r] - use);
+            const float4 x = *reinterpret_cast<const float4*>(so + (n * ROWS + r) * HD + c);
+            // a part without keys holds zeros; others may hold what a NaN made of them
+            s.x += w * x.x; s.y += w * x.y; s.z += w * x.z; s.w += w * x.w;
+            l += w * ssum[n * ROWS + r];
+        }
+        if (a.n_split == 1) {
+            const float inv = l > 0.f ? 1.f / l : l;
+            if (c < a.hd) {
+                T* to = out_at(r) + c;
+                to[0] = from_f32<T>(s.x * inv); to[1] = from_f32<T>(s.y * inv);
+                to[2] = from_f32<T>(s.z * inv); to[3] = from_f32<T>(s.w * inv);
+            }
+        } else {
+            float* to = mine + r * kLd;
+            to[c] = s.x; to[c + 1] = s.y; to[c + 2] = s.z; to[c + 3] = s.w;
+            if (c == 0) { to[HD] = mx; to[HD + 1] = l; }
+        }
+    }
+    if (a.n_split == 1) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t done = atomicAdd(a.count + group, 1u);
+        last = done == (uint32_t)a.n_split - 1;
+        if (last) a.count[group] = 0;            // ready for the next call
+        __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+    const float* all = a.part + group * a.n_split * (int64_t)(ROWS * kLd);
+    for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {
+        const int r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+        if (c >= a.hd) continue;
+        float mx = -INFINITY, l = 0.f;
+        for (int n = 0; n < a.n_split; ++n) mx = fmaxf(mx, __ldcg(all + n * (ROWS * kLd) + r * kLd + HD));
+        const float use = mx == -INFINITY ? 0.f : mx;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < a.n_split; ++n) {
+            const float* x = all + n * (ROWS * kLd) + r * kLd;
+            const float w = exp2f(__ldcg(x + HD) - use);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += w * __ldcg(x + c + e);
+            l += w * __ldcg(x + HD + 1);
+        }
+        const float inv = l > 0.f ? 1.f / l : l;
+        T* to = out_at(r) + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e] = from_f32<T>(s[e] * inv);
+    }
+}
+
+// The rows of an idle slot.
+template <typename T, int ROWS>
+__device__ __forceinline__ void zero_rows(const DecArgs& a, const Place& p, T* o) {
+    if (!p.tail) return;
+    const int rows = min(ROWS, a.rows - p.tile * ROWS);
+    for (int i = threadIdx.x; i < rows * a.hd; i += kThreads) {
+        const int row = p.tile * ROWS + i / a.hd, m = row / a.group, g = row - m * a.group;
+        o[(p.b * a.M + m) * a.os + ((int64_t)p.kv * a.group + g) * a.hd + i % a.hd] = from_f32<T>(0.f);
+    }
+}
+
+// ---------------------------------------------------------------- bf16
+constexpr int kTok = 64;                             // tokens per tile
+constexpr int kStages = 3;
+
+// Byte offset of 16-byte chunk c of row r in a tile of HD bf16 per row: chunks permuted within a row's
+// 128-byte half so that the eight rows of an ldmatrix fall in different banks.
+template <int HD>
+__device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * HD * 2 + ((c ^ (r & 7)) << 4)); }
+
+template <int HD, int RW>
+struct DecSmem {
+    static constexpr int rows = 16 * RW;
+    static constexpr uint32_t half = kTok * HD * 2;              // K or V of a tile
+    static constexpr uint32_t bytes = kStages * 2 * half;        // the parts and q use the ring's memory
+};
+
+template <int HD, int RW>
+__global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat16* __restrict__ q,
+                                                               const __nv_bfloat16* __restrict__ k,
+                                                               const __nv_bfloat16* __restrict__ v,
+                                                               __nv_bfloat16* k_cache, __nv_bfloat16* v_cache,
+                                                               __nv_bfloat16* __restrict__ o, const DecArgs a) {
+    using S = DecSmem<HD, RW>;
+    constexpr int ROWS = 16 * RW, TW = 4 / RW, GROUPS = RW;      // a warp: 16 rows, GROUPS x 16 tokens of each tile
+    constexpr int C = HD / 8;                                    // 16-byte chunks per row
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ float smax[TW * ROWS], ssum[TW * ROWS];
+    __shared__ uint64_t seen[64];
+    __shared__ float scratch[4][16][17];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rw = warp % RW, tw = warp / RW;
+    Place p = place_of<ROWS>(a, kTok);
+    const int64_t slot = (p.b * a.kvh + p.kv) * a.max_len;
+    const uint32_t ring = smem_at(sm);
+    const int tiles = (int)((p.to - p.from + kTok - 1) / kTok);
+
+    auto fetch = [&](int t) {                                    // cached tile t of this run
+        if (t < tiles) {
+            const int64_t r0 = p.from + (int64_t)t * kTok;
+            const uint32_t at = ring + (t % kStages) * 2 * S::half;
+            for (int i = threadIdx.x; i < kTok * C; i += kThreads) {
+                const int r = i / C, c = i % C;
+                const bool real = r0 + r < p.to && c * 8 < a.hd;
+                const int64_t src = (slot + (real ? r0 + r : 0)) * a.hd + (real ? c * 8 : 0);
+                copy16(at + swz<HD>(r, c), k_cache + src, real);
+                copy16(at + S::half + swz<HD>(r, c), v_cache + src, real);
+            }
+        }
+        copies_close();
+    };
+#pragma unroll
+    for (int t = 0; t < kStages - 1; ++t) fetch(t);
+    if (!p.idle && !positions_ok(a, p)) {
+        p.idle = true;
+        if (threadIdx.x == 0) atomicOr(a.err, kErrRopePos);
+    }
+    if (p.idle) {
+        copies_wait<0>();
+        zero_rows<__nv_bfloat16, ROWS>(a, p, o);
+        return;
+    }
+    for (int m = threadIdx.x; m < a.M; m += kThreads) seen[m] = seen_by(a, p.b, m);
+    // q, rotated, as value and remainder, through the last stage of the ring
+    uint8_t* sq = sm + (kStages - 1) * 2 * S::half;
+    for (int i = threadIdx.x; i < ROWS * HD; i += kThreads) {
+        const int r = i / HD, c = i % HD, row = p.tile * ROWS + r;
+        float x = 0.f;
+        if (row < a.rows && c < a.hd) {
+            const int m = row / a.group, g = row - m * a.group;
+            const float* f = a.rot ? a.cs + (p.len + depth_of(seen_by(a, p.b, m), m)) * a.rot : nullptr;
+            x = turned(q + (p.b * a.M + m) * a.qs + ((int64_t)p.kv * a.group + g) * a.hd, c, f, a.rot, a.half);
+        }
+        const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+        const uint32_t at = swz<HD>(r, c / 8) + (c % 8) * 2;
+        *reinterpret_cast<__nv_bfloat16*>(sq + at) = hi;
+        *reinterpret_cast<__nv_bfloat16*>(sq + ROWS * HD * 2 + at) = __float2bfloat16_rn(x - __bfloat162float(hi));
+    }
+    __syncthreads();
+    uint32_t qh[HD / 16][4], ql[HD / 16][4];
+#pragma unroll
+    for (int c = 0; c < HD / 16; ++c) {
+        const uint32_t at = smem_at(sq) + swz<HD>(16 * rw + (lane & 15), 2 * c + (lane >> 4));
+        ldsm4(qh[c], at);
+        ldsm4(ql[c], at + ROWS * HD * 2);
+    }
+    __syncthreads();
+
+    float acc[HD / 8][4], mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < HD / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+    const float cs = a.scale * kLog2e;
+    const int total = tiles + (p.tail ? 1 : 0);
+    for (int t = 0; t < total; ++t) {
+        const bool draft = t == tiles;
+        uint8_t* tile = sm + (t % kStages) * 2 * S::half;
+        bool poison = false;                                     // infinities or NaN among the drafted values
+        if (!draft) {
+            fetch(t + kStages - 1);
+            copies_wait<kStages - 1>();
+            __syncthreads();
+        } else {
+            copies_wait<0>();
+            __syncthreads();
+            bool bad = false;
+            const bool write = p.tile == 0;
+            for (int i = threadIdx.x; i < kTok * HD; i += kThreads) {
+                const int r = i / HD, c = i % HD;
+                __nv_bfloat16 x = __float2bfloat16_rn(0.f), y = x;
+                if (r < a.M && c < a.hd) {
+                    const float* f = a.rot ? a.cs + (p.len + depth_of(seen[r], r)) * a.rot : nullptr;
+                    x = __float2bfloat16_rn(turned(k + (p.b * a.M + r) * a.ks + (int64_t)p.kv * a.hd, c, f, a.rot, a.half));
+                    y = v[(p.b * a.M + r) * a.vs + (int64_t)p.kv * a.hd + c];
+                    bad = bad || !(fabsf(__bfloat162float(y)) < INFINITY);
+                    if (write) {
+                        k_cache[(slot + p.len + r) * a.hd + c] = x;
+                        v_cache[(slot + p.len + r) * a.hd + c] = y;
+                    }
+                }
+                const uint32_t at = swz<HD>(r, c / 8) + (c % 8) * 2;
+                *reinterpret_cast<__nv_bfloat16*>(tile + at) = x;
+                *reinterpret_cast<__nv_bfloat16*>(tile + S::half + at) = y;
+            }
+            poison = __syncthreads_or(bad) != 0;
+        }
+        const uint32_t kt = smem_at(tile), vt = kt + S::half;
+        const int64_t left = draft ? a.M : p.to - p.from - (int64_t)t * kTok;     // real rows of the tile
+#pragma unroll
+        for (int gi = 0; gi < GROUPS; ++gi) {
+            const int c0 = 16 * (GROUPS * tw + gi);              // first of 16 tokens
+            if (c0 >= left) continue;
+            float s[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < HD / 16; ++c) {
+                uint32_t b[4];
+                ldsm4(b, kt + swz<HD>(c0 + (lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1)));
+                mma16816(s[0], qh[c], b[0], b[1]);
+                mma16816(s[1], qh[c], b[2], b[3]);
+                if (a.rot) {
+                    mma16816(s[0], ql[c], b[0], b[1]);
+                    mma16816(s[1], ql[c], b[2], b[3]);
+                }
+            }
+            // rows 16 rw + lane / 4 (e 0, 1) and + 8 (e 2, 3), tokens c0 + 8 n + 2 (lane % 4) + (e & 1)
+            uint32_t hidden = 0;
+            if (draft || left < kTok) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int tok = c0 + 8 * n + 2 * (lane & 3) + (e & 1);
+                        const int row = p.tile * ROWS + 16 * rw + (lane >> 2) + 8 * (e >> 1);
+                        const bool see = tok < left && (!draft || (row < a.rows && (seen[row / a.group] >> tok & 1)));
+                        if (!see) {
+                            s[n][e] = -INFINITY;
+                            hidden |= 1u << (4 * n + e);
+                        }
+                    }
+            }
+            uint32_t pa[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                const float now = fmaxf(mx[h], top * cs), use = now == -INFINITY ? 0.f : now;
+                const float corr = exp2f(mx[h] - use);
+                mx[h] = now;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) s[n][2 * h + e] = exp2f(fmaf(s[n][2 * h + e], cs, -use));
+                sum[h] = sum[h] * corr + ((s[0][2 * h] + s[0][2 * h + 1]) + (s[1][2 * h] + s[1][2 * h + 1]));
+                pa[h] = pack2(s[0][2 * h], s[0][2 * h + 1]);
+                pa[2 + h] = pack2(s[1][2 * h], s[1][2 * h + 1]);
+                if (corr != 1.f) {
+#pragma unroll
+                    for (int n = 0; n < HD / 8; ++n) {
+                        acc[n][2 * h] *= corr;
+                        acc[n][2 * h + 1] *= corr;
+                    }
+                }
+            }
+            if (!poison) {
+#pragma unroll
+                for (int n = 0; n < HD / 16; ++n) {
+                    uint32_t b[4];
+                    ldsm4t(b, vt + swz<HD>(c0 + (lane & 15), 2 * n + (lane >> 4)));
+                    mma16816(acc[2 * n], pa, b[0], b[1]);
+                    mma16816(acc[2 * n + 1], pa, b[2], b[3]);
+                }
+            } else {
+                // term by term, without the masked ones (0 x NaN would be NaN); a masked place is marked by -1
+                __syncwarp();
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        scratch[warp][(lane >> 2) + 8 * (e >> 1)][8 * n + 2 * (lane & 3) + (e & 1)] =
+                            hidden >> (4 * n + e) & 1 ? -1.f : s[n][e];
+                __syncwarp();
+                for (int c = 0; c < 16; ++c)
+#pragma unroll
+                    for (int n = 0; n < HD / 8; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float w = scratch[warp][(lane >> 2) + 8 * (e >> 1)][c];
+                            const int d = 2 * (lane & 3) + (e & 1);
+                            if (w != -1.f)
+                                acc[n][e] = fmaf(w, __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+                                                        tile + S::half + swz<HD>(c0 + c, n) + 2 * d)), acc[n][e]);
+                        }
+            }
+        }
+        __syncthreads();                                         // the tile's stage is filled again
+    }
+    copies_wait<0>();
+    __syncthreads();
+    // parts of the TW token groups, in the ring's memory
+    float* so = reinterpret_cast<float*>(sm);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        sum[h] += __shfl_xor_sync(0xFFFFFFFFu, sum[h], 1);
+        sum[h] += __shfl_xor_sync(0xFFFFFFFFu, sum[h], 2);
+        const int r = tw * ROWS + 16 * rw + (lane >> 2) + 8 * h;
+        if ((lane & 3) == 0) {
+            smax[r] = mx[h];
+            ssum[r] = sum[h];
+        }
+#pragma unroll
+        for (int n = 0; n < HD / 8; ++n)
+            *reinterpret_cast<float2*>(so + r * HD + 8 * n + 2 * (lane & 3)) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
+    }
+    __syncthreads();
+    finish<__nv_bfloat16, HD, ROWS, TW>(a, p, so, smax, ssum, o);
+}
+
+// ---------------------------------------------------------------- fp32
+constexpr int kTokF = 32;
+constexpr int kRowsF = 16;                           // four rows per warp
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* __restrict__ q,
+                                                                   const float* __restrict__ k,
+                                                                   const float* __restrict__ v, float* k_cache,
+                                                                   float* v_cache, float* __restrict__ o,
+                                                                   const DecArgs a) {
+    constexpr int C = HD / 4, E = HD / 32;                       // 16-byte chunks per row; channels per lane
+    constexpr uint32_t kHalf = kTokF * HD * 4;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ __align__(16) float sq[kRowsF][HD];
+    __shared__ float smax[kRowsF], ssum[kRowsF];
+    __shared__ uint64_t seen[64];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Place p = place_of<kRowsF>(a, kTokF);
+    const int64_t slot = (p.b * a.kvh + p.kv) * a.max_len;
+    const uint32_t ring = smem_at(sm);
+    const int tiles = (int)((p.to - p.from + kTokF - 1) / kTokF);
+    auto place = [](int r, int c) { return (uint32_t)(r * HD * 4 + ((c ^ (r & 7)) << 4)); };
+    auto fetch = [&](int t) {
+        if (t < tiles) {
+            const int64_t r0 = p.from + (int64_t)t * kTokF;
+            const uint32_t at = ring + (t % kStages) * 2 * kHalf;
+            for (int i = threadIdx.x; i < kTokF * C; i += kThreads) {
+                const int r = i / C, c = i % C;
+                const bool real = r0 + r < p.to && c * 4 < a.hd;
+                const int64_t src = (slot + (real ? r0 + r : 0)) * a.hd + (real ? c * 4 : 0);
+                copy16(at + place(r, c), k_cache + src, real);
+                copy16(at + kHalf + place(r, c), v_cache + src, real);
+            }
+        }
+        copies_close();
+    };
+#pragma unroll
+    for (int t = 0; t < kStages - 1; ++t) fetch(t);
+    if (!p.idle && !positions_ok(a, p)) {
+        p.idle = true;
+        if (threadIdx.x == 0) atomicOr(a.err, kErrRopePos);
+    }
+    if (p.idle) {
+        copies_wait<0>();
+        zero_rows<float, kRowsF>(a, p, o);
+        return;
+    }
+    for (int m = threadIdx.x; m < a.M; m += kThreads) seen[m] = seen_by(a, p.b, m);
+    for (int i = threadIdx.x; i < kRowsF * HD; i += kThreads) {
+        const int r = i / HD, c = i % HD, row = p.tile * kRowsF + r;
+        float x = 0.f;
+        if (row < a.rows && c < a.hd) {
+            const int m = row / a.group, g = row - m * a.group;
+            const float* f = a.rot ? a.cs + (p.len + depth_of(seen_by(a, p.b, m), m)) * a.rot : nullptr;
+            x = turned(q + (p.b * a.M + m) * a.qs + ((int64_t)p.kv * a.group + g) * a.hd, c, f, a.rot, a.half);
+        }
+        sq[r][c] = x;
+    }
+    __syncthreads();
+    float acc[4][E], mx[4], sum[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        mx[r] = -INFINITY;
+        sum[r] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
+    }
+    const float cs = a.scale * kLog2e;
+    const int rows_left = a.rows - p.tile * kRowsF - 4 * warp;   // real rows of this warp
+    const int drafts = p.tail ? (a.M + kTokF - 1) / kTokF : 0;
+    for (int t = 0; t < tiles + drafts; ++t) {
+        const bool draft = t >= tiles;
+        const int d0 = draft ? (t - tiles) * kTokF : 0;          // first drafted token of the tile
+        uint8_t* tile = sm + (t % kStages) * 2 * kHalf;
+        if (!draft) {
+            fetch(t + kStages - 1);
+            copies_wait<kStages - 1>();
+            __syncthreads();
+        } else {
+            copies_wait<0>();
+            __syncthreads();
+            const bool write = p.tile == 0;
+            for (int i = threadIdx.x; i < kTokF * HD; i += kThreads) {
+                const int r = i / HD, c = i % HD, m = d0 + r;
+                float x = 0.f, y = 0.f;
+                if (m < a.M && c < a.hd) {
+                    const float* f = a.rot ? a.cs + (p.len + depth_of(seen[m], m)) * a.rot : nullptr;
+                    x = turned(k + (p.b * a.M + m) * a.ks + (int64_t)p.kv * a.hd, c, f, a.rot, a.half);
+                    y = v[(p.b * a.M + m) * a.vs + (int64_t)p.kv * a.hd + c];
+                    if (write) {
+                        k_cache[(slot + p.len + m) * a.hd + c] = x;
+                        v_cache[(slot + p.len + m) * a.hd + c] = y;
+                    }
+                }
+                const uint32_t at = place(r, c / 4) + (c % 4) * 4;
+                *reinterpret_cast<float*>(tile + at) = x;
+                *reinterpret_cast<float*>(tile + kHalf + at) = y;
+            }
+            __syncthreads();
+        }
+        const int left = (int)min((int64_t)kTokF, draft ? (int64_t)(a.M - d0) : p.to - p.from - (int64_t)t * kTokF);
+        if (rows_left > 0) {
+            // scores: a lane per token, four rows
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+            for (int c = 0; c < C; ++c) {
+                const float4 x = *reinterpret_cast<const float4*>(tile + place(lane, c));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float4 y = *reinterpret_cast<const float4*>(&sq[4 * warp + r][4 * c]);
+                    s[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[r]))));
+                }
+            }
+            uint32_t see[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = min(p.tile * kRowsF + 4 * warp + r, a.rows - 1);
+                const bool mine = lane < left && (!draft || (seen[row / a.group] >> (d0 + lane) & 1));
+                see[r] = __ballot_sync(0xFFFFFFFFu, mine);
+                float top = mine ? s[r] * cs : -INFINITY;
+#pragma unroll
+                for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+                const float now = fmaxf(mx[r], top), use = now == -INFINITY ? 0.f : now;
+                const float corr = exp2f(mx[r] - use);
+                mx[r] = now;
+                s[r] = mine ? exp2f(fmaf(s[r], cs, -use)) : 0.f;
+                sum[r] = sum[r] * corr + s[r];
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[r][e] *= corr;
+            }
+            // values: a lane per E channels; a masked token's value is not touched
+            for (int n = 0; n < left; ++n) {
+                float x[E];
+                const int c = lane * E;
+                const float* row = reinterpret_cast<const float*>(tile + kHalf + place(n, c / 4)) + c % 4;
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] = row[e];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float w = __shfl_sync(0xFFFFFFFFu, s[r], n);
+                    if (see[r] >> n & 1)
+#pragma unroll
+                        for (int e = 0; e < E; ++e) acc[r][e] = fmaf(w, x[e], acc[r][e]);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    copies_wait<0>();
+    __syncthreads();
+    float* so = reinterpret_cast<float*>(sm);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+#pragma unroll
+        for (int x = 16; x; x >>= 1) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], x);
+        if (lane == 0) {
+            smax[4 * warp + r] = mx[r];
+            ssum[4 * warp + r] = sum[r];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) so[(4 * warp + r) * HD + lane * E + e] = acc[r][e];
+    }
+    __syncthreads();
+    finish<float, HD, kRowsF, 1>(a, p, so, smax, ssum, o);
+}
+
+// Rows a block takes: 16 or 32 where they are all there are (its warps then share out the tokens), else 64.
+int tile_rows(const DecodeProb& p) {
+    if (p.dtype == 0) return kRowsF;
+    const int64_t rows = (int64_t)p.M * p.group;
+    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+template <typename F, typename T>
+cudaError_t launch(F* f, size_t smem, unsigned grid, const T* q, const T* k, const T* v, T* kc, T* vc, T* o,
+                   const DecArgs& a, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    DC_LAUNCH(kAttnDecode, st, f<<<grid, kThreads, smem, st>>>(q, k, v, kc, vc, o, a));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t attn_decode_groups(const DecodeProb& p) {
+    const int rows = tile_rows(p);
+    return p.batch * p.kvh * (((int64_t)p.M * p.group + rows - 1) / rows);
+}
+
+// Runs the cache is split into: enough blocks for four per SM, but no run of a full cache below 128 tokens (two tiles).
+int attn_decode_splits(const DecodeProb& p) {
+    const int64_t groups = std::max<int64_t>(1, attn_decode_groups(p));
+    const int64_t want = (4 * 148 + groups - 1) / groups;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({want, (p.max_len + 127) / 128, 64}));
+}
+
+size_t attn_decode_part_bytes(const DecodeProb& p) {
+    const int n = attn_decode_splits(p), hd = p.hd <= 64 ? 64 : 128;
+    return n == 1 ? 0 : (size_t)attn_decode_groups(p) * n * tile_rows(p) * (hd + 2) * sizeof(float);
+}
+
+cudaError_t attn_decode(const DecodeProb& p, const void* q, const void* k, const void* v, void* kc, void* vc,
+                        const int32_t* lens, const uint64_t* tree, void* o, uint32_t* err, uint32_t* count, float* part,
+                        cudaStream_t st) {
+    DecArgs a{p.M, p.heads, p.kvh, p.group, p.hd, p.M * p.group, attn_decode_splits(p), p.max_len, p.qs, p.ks, p.vs, p.os,
+              p.rot, p.half, p.max_pos, p.cs, lens, tree, p.scale, part, count, err};
+    const unsigned grid = (unsigned)(attn_decode_groups(p) * a.n_split);
+    if (p.dtype == 0) {
+        const float *qf = static_cast<const float*>(q), *kf = static_cast<const float*>(k), *vf = static_cast<const float*>(v);
+        float *kcf = static_cast<float*>(kc), *vcf = static_cast<float*>(vc), *of = static_cast<float*>(o);
+        return p.hd <= 64 ? launch(attn_decode_f32_kernel<64>, kStages * 2 * kTokF * 64 * 4, grid, qf, kf, vf, kcf, vcf, of, a, st)
+                          : launch(attn_decode_f32_kernel<128>, kStages * 2 * kTokF * 128 * 4, grid, qf, kf, vf, kcf, vcf, of, a, st);
+    }
+    using B = __nv_bfloat16;
+    const B *qb = static_cast<const B*>(q), *kb = static_cast<const B*>(k), *vb = static_cast<const B*>(v);
+    B *kcb = static_cast<B*>(kc), *vcb = static_cast<B*>(vc), *ob = static_cast<B*>(o);
+    const int rows = tile_rows(p);
+    if (p.hd <= 64)
+        return rows == 16   ? launch(attn_decode_kernel<64, 1>, DecSmem<64, 1>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st)
+               : rows == 32 ? launch(attn_decode_kernel<64, 2>, DecSmem<64, 2>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st)
+                            : launch(attn_decode_kernel<64, 4>, DecSmem<64, 4>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st);
+    return rows == 16   ? launch(attn_decode_kernel<128, 1>, DecSmem<128, 1>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st)
+           : rows == 32 ? launch(attn_decode_kernel<128, 2>, DecSmem<128, 2>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st)
+                        : launch(attn_decode_kernel<128, 4>, DecSmem<128, 4>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st);
+}
+
+}  // namespace dynconv

@@ -343,6 +343,72 @@ class AttnPlan:
         return out
 
 
+class AttnDecoder:
+    """Serving steps of ``batch`` sequences over a key/value cache: each step takes ``tokens`` new or drafted
+    tokens per sequence, rotates their q and k (``rope_table``, see :func:`rope_table`), appends k and v to the
+    caches and returns their attention.
+
+    ``k_cache``, ``v_cache`` [batch, kv_heads, max_len, head_dim] and ``lens`` (int32 [batch]: tokens cached, a
+    negative entry for an idle slot) are made here, empty, or taken from the caller.  A step reads ``lens`` and
+    leaves it: :meth:`advance` adds the tokens that are kept."""
+
+    def __init__(self, dtype: torch.dtype, batch: int, heads: int, kv_heads: int, head_dim: int, max_len: int,
+                 tokens: int = 1, scale: float = 0.0, rope_table: Optional[torch.Tensor] = None,
+                 rope_layout: int = L.ROPE_INTERLEAVED, q_row_stride: int = 0, k_row_stride: int = 0,
+                 v_row_stride: int = 0, k_cache=None, v_cache=None, lens=None, device=None):
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"storage dtype must be bf16 or fp32, got {dtype}")
+        if rope_table is not None and (rope_table.dtype != torch.float32 or rope_table.dim() != 2
+                                       or not rope_table.is_contiguous()):
+            raise ValueError("rope_table must be a contiguous fp32 [max_pos, rotated channels] tensor")
+        self.table = rope_table                 # kept alive: the descriptor holds its address
+        self.desc = L.make_attn_decode_desc(L.BF16 if dtype == torch.bfloat16 else L.F32, batch, tokens, heads, kv_heads,
+                                            head_dim, max_len, scale, rope_table, rope_layout, q_row_stride,
+                                            k_row_stride, v_row_stride)
+        nbytes = L.dynconv_attn_decode_workspace_bytes(self.desc)
+        if nbytes == 0:
+            raise L.DynConvError(1, L.dynconv_last_error() or "invalid descriptor")
+        self.device = k_cache.device if device is None and k_cache is not None else _device(device)
+        shape = (batch, kv_heads, max_len, head_dim)
+        self.k_cache = torch.zeros(shape, dtype=dtype, device=self.device) if k_cache is None else k_cache
+        self.v_cache = torch.zeros(shape, dtype=dtype, device=self.device) if v_cache is None else v_cache
+        self.lens = torch.zeros(batch, dtype=torch.int32, device=self.device) if lens is None else lens
+        _ints(self.k_cache, "k_cache", dtype, shape)
+        _ints(self.v_cache, "v_cache", dtype, shape)
+        _ints(self.lens, "lens", torch.int32, (batch,))
+        _one_device(self.device, self.k_cache, self.v_cache, self.lens, rope_table)
+        self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self.dtype, self.batch, self.tokens = dtype, batch, tokens
+        self.wq, self.wk = heads * head_dim, kv_heads * head_dim
+        self.strides = (q_row_stride, k_row_stride, v_row_stride)
+
+    def step(self, q, k, v, ancestors=None, o=None, stream=None):
+        """o [batch * tokens, heads * head_dim] of q [batch * tokens, heads * head_dim], k and v
+        [batch * tokens, kv_heads * head_dim] (rows by sequence, then token).  ``ancestors`` (int64
+        [batch, tokens]): bit j of an entry set where that token sees drafted token j, its own bit included;
+        None: a chain."""
+        rows = self.batch * self.tokens
+        if o is None:
+            o = torch.empty((rows, self.wq), dtype=self.dtype, device=self.device)
+        _rows(q, "q", rows, self.wq, self.dtype, self.strides[0])
+        _rows(k, "k", rows, self.wk, self.dtype, self.strides[1])
+        _rows(v, "v", rows, self.wk, self.dtype, self.strides[2])
+        _rows(o, "o", rows, self.wq, self.dtype, 0)
+        _ints(ancestors, "ancestors", torch.int64, (self.batch, self.tokens))
+        _one_device(self.device, q, k, v, o, ancestors)
+        with _On(self.device):
+            L.dynconv_attn_decode(self.desc, q, k, v, self.k_cache, self.v_cache, self.lens, ancestors, o, self.ws, stream)
+        return o
+
+    def advance(self, kept=None):
+        """Adds the tokens kept of the last step to ``lens``: all of them, or ``kept`` (int32 [batch]).  Idle
+        slots stay idle.  Kept tokens of a tree have to lie in the cache in order (tokens 0 .. kept - 1)."""
+        self.lens.add_(torch.where(self.lens < 0, 0, self.tokens if kept is None else kept).to(torch.int32))
+
+    def reset(self):
+        self.lens.zero_()
+
+
 class QKVAttention(torch.autograd.Function):
     """Causal attention of a fused QKV buffer, with the rotation of Q and K where a table is given.
 

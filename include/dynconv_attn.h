@@ -1,6 +1,7 @@
 /*
  * dynconv_attn.h -- C ABI of the operators that follow the Q/K/V convolution: rotary
- * positions and causal attention over packed prompts (forward and backward).
+ * positions, causal attention over packed prompts (forward and backward) and attention of
+ * new or drafted tokens over a key/value cache.
  *
  * They take what dynconv_fwd / dynconv_fwd_varlen leave: token-major rows whose heads are
  * runs of head_dim channels, so that Q, K and V may be column slices of one [N, C] buffer
@@ -107,6 +108,49 @@ DYNCONV_API dynconv_status dynconv_attn_bwd(const dynconv_attn_desc *desc, const
                                             const void *d_o, const void *q, const void *k, const void *v,
                                             const void *o, const float *lse, void *dq, void *dk, void *dv,
                                             void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ attention over a cache */
+typedef struct {
+    int32_t dtype;          /* dynconv_dtype of every tensor and of the caches */
+    int32_t rope_layout;    /* dynconv_rope_layout (rope_dim > 0) */
+    int64_t batch;          /* sequences */
+    int64_t tokens;         /* new or drafted tokens per sequence: 1..64 */
+    int64_t heads, kv_heads, head_dim;   /* as dynconv_attn_desc; head_dim a multiple of 16 bytes */
+    int64_t max_len;        /* tokens each sequence's cache holds */
+    int64_t q_row_stride, k_row_stride, v_row_stride, o_row_stride;   /* multiples of 16 bytes; 0 = dense */
+    int64_t rope_dim;       /* rotated channels of each q and k head: 0 (none) or even, up to head_dim */
+    int64_t rope_max_pos;   /* rows of rope_cos_sin */
+    const float *rope_cos_sin;   /* as dynconv_rope_desc.cos_sin, [rope_max_pos, rope_dim] */
+    float scale;            /* positive and finite; 0 = 1 / sqrt(head_dim) */
+} dynconv_attn_decode_desc;
+
+DYNCONV_API size_t dynconv_attn_decode_workspace_bytes(const dynconv_attn_decode_desc *desc);
+
+/* One serving step: the `tokens` new tokens of each sequence are rotated, appended to the
+ * caches and attend to them.  With L = lens[b] tokens already cached,
+ *   - token m stands at position L + depth(m), depth(m) = the number of its ancestors; q and k
+ *     are rotated there (rope_dim > 0);
+ *   - k (rotated, rounded to the storage dtype) and v go to rows L + m of the caches;
+ *   - o[b, m] = softmax attention of q[b, m] over rows 0 .. L - 1 and the rows L + j of its
+ *     ancestors j and of itself.
+ * lens is read, not advanced: the caller adds the tokens it keeps.
+ *   q [batch * tokens, heads * head_dim], k and v [batch * tokens, kv_heads * head_dim],
+ *   o like q; rows ordered by sequence, then token
+ *   k_cache, v_cache [batch, kv_heads, max_len, head_dim], updated in place
+ *   lens       DEVICE int32 [batch].  A negative entry marks an idle slot: its o rows are
+ *              zero and its caches are left as they are.
+ *   ancestors  nullable DEVICE uint64 [batch, tokens]: bit j of entry m set where token m sees
+ *              drafted token j (its own bit included; an entry may be 0: it then sees the cached
+ *              rows only, and its o is zero where there are none).  depth(m) counts the bits
+ *              other than m.  NULL: token m sees tokens 0 .. m (a chain).
+ * Rows of the cache at L + tokens and beyond are neither read nor written, and what a masked
+ * row holds (infinities and NaN among it) does not reach o.
+ * Errors: DYNCONV_ERR_INVALID, _UNSUPPORTED, _WORKSPACE, _CUDA; L + tokens above max_len, or a
+ * position at or beyond rope_max_pos, raises the device check and the sequence is treated as idle. */
+DYNCONV_API dynconv_status dynconv_attn_decode(const dynconv_attn_decode_desc *desc, const void *q, const void *k,
+                                               const void *v, void *k_cache, void *v_cache, const int32_t *lens,
+                                               const uint64_t *ancestors, void *o, void *ws, size_t ws_bytes,
+                                               void *stream);
 
 #ifdef __cplusplus
 }

@@ -26,9 +26,10 @@ def doc_ranges(cu):
     return [(int(a), int(b)) for a, b in zip(cu[:-1], cu[1:]) if b > a]
 
 
-def attention(q, k, v, cu, heads, kv_heads, hd, d_o=None, scale=0.0, eps=0.0):
+def attention(q, k, v, cu, heads, kv_heads, hd, d_o=None, scale=0.0, eps=0.0, q_err=0.0):
     """values and bounds ({name: (value, bound)}) of o, lse and, with d_o, dq, dk, dv.
-    q, k, v, d_o: [N, heads * hd] tensors of any float type on any device."""
+    q, k, v, d_o: [N, heads * hd] tensors of any float type on any device; q_err: relative error of q as
+    the kernel holds it."""
     dev = q.device
     N, G = q.shape[0], heads // kv_heads
     scale = scale or 1.0 / math.sqrt(hd)
@@ -50,7 +51,7 @@ def attention(q, k, v, cu, heads, kv_heads, hd, d_o=None, scale=0.0, eps=0.0):
         p = (s - ls).exp()
         # the largest score as the exponent's argument sees it, and the size of its terms
         big = scale * float((qd.abs() @ kd.abs().transpose(-1, -2)).max())
-        r = (hd + n + 32) * 2.0 ** -24 * (2 + big)
+        r = (hd + n + 32) * 2.0 ** -24 * (2 + big) + 2 * q_err * big
         back = lambda t: t.reshape(-1, n, hd).permute(1, 0, 2)
         o = p @ vd
         size = p @ vd.abs()
@@ -79,6 +80,33 @@ def attention(q, k, v, cu, heads, kv_heads, hd, d_o=None, scale=0.0, eps=0.0):
     out = {n: (flat(val[n]), flat(bnd[n])) for n in (val if d_o is not None else ("o",))}
     out["lse"] = (lse, lse_bound)
     return out
+
+
+def decode(q, k_cache, v_cache, lens, trees, heads, kv_heads, hd, tokens, scale=0.0, eps=0.0, q_err=0.0):
+    """(value, bound) of o for rotated q [batch * tokens, heads * hd] (64 bits) over caches that already hold
+    the new rows; trees[b][m]: bitmask of the drafted tokens that token m sees; lens < 0: zero rows.
+    q_err: relative error of q as the kernel holds it."""
+    scale = scale or 1.0 / math.sqrt(hd)
+    G = heads // kv_heads
+    q = q.double().reshape(len(lens), tokens, kv_heads, G, hd)
+    val, bnd = torch.zeros_like(q), torch.zeros_like(q)
+    for b, n in enumerate(lens):
+        if n < 0:
+            continue
+        k, v = (t[b, :, :n + tokens].double() for t in (k_cache, v_cache))     # [kv, rows, hd]
+        for m in range(tokens):
+            at = list(range(n)) + [n + j for j in range(tokens) if trees[b][m] >> j & 1]
+            if not at:
+                continue
+            ks, vs = k[:, at], v[:, at]
+            s = scale * torch.einsum("kgd,kjd->kgj", q[b, m], ks)
+            p = torch.softmax(s, -1)
+            size = torch.einsum("kgj,kjd->kgd", p, vs.abs())
+            big = scale * float(torch.einsum("kgd,kjd->kgj", q[b, m].abs(), ks.abs()).max())
+            r = (hd + len(at) + 32) * 2.0 ** -24 * (2 + big) + 2 * q_err * big
+            o = torch.einsum("kgj,kjd->kgd", p, vs)
+            val[b, m], bnd[b, m] = o, eps / 2 * (o.abs() + size) + r * size
+    return val.reshape(-1, heads * hd), bnd.reshape(-1, heads * hd)
 
 
 def rope(x, table, pos, heads, hd, half, inverse=False, eps=0.0):
