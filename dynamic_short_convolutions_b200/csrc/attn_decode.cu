@@ -78,17 +78,48 @@ __device__ __forceinline__ uint64_t seen_by(const DecArgs& a, int64_t b, int m) 
 }
 __device__ __forceinline__ int depth_of(uint64_t seen, int m) { return __popcll(seen & ~(uint64_t(1) << m)); }
 
-// Channel c of a head's row x, rotated by the table row f (nullptr: as it is).
+// The 16 bytes of channels from c on of a head's row x, rotated by the table row f (nullptr: as they are).
 template <typename T>
-__device__ __forceinline__ float turned(const T* x, int c, const float* f, int rot, int half) {
-    const float v = to_f32(x[c]);
-    if (f == nullptr || c >= rot) return v;
+__device__ __forceinline__ void turned(const T* x, int c, const float* f, int rot, int half, float (&out)[16 / sizeof(T)]) {
+    constexpr int V = 16 / sizeof(T);
+    T own[V];
+    *reinterpret_cast<uint4*>(own) = __ldg(reinterpret_cast<const uint4*>(x + c));
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] = to_f32(own[e]);
+    if (f == nullptr || c >= rot) return;
+    if (!half) {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            if (c + e >= rot) break;
+            const float2 z = __ldg(reinterpret_cast<const float2*>(f + c + e));
+            const float u = out[e], w = out[e + 1];
+            out[e] = u * z.x - w * z.y;
+            out[e + 1] = u * z.y + w * z.x;
+        }
+        return;
+    }
     const int hr = rot / 2;
-    const int pair = half ? (c < hr ? c : c - hr) : c / 2;
-    const bool first = half ? c < hr : (c & 1) == 0;
-    const float w = to_f32(x[half ? (first ? c + hr : c - hr) : (c ^ 1)]);
-    const float2 z = __ldg(reinterpret_cast<const float2*>(f) + pair);
-    return first ? v * z.x - w * z.y : w * z.y + v * z.x;
+    if (hr % V == 0) {
+        const bool first = c < hr;
+        T other[V];
+        *reinterpret_cast<uint4*>(other) = __ldg(reinterpret_cast<const uint4*>(x + (first ? c + hr : c - hr)));
+        const float2* z = reinterpret_cast<const float2*>(f) + (first ? c : c - hr);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float2 y = __ldg(z + e);
+            const float w = to_f32(other[e]);
+            out[e] = first ? out[e] * y.x - w * y.y : w * y.y + out[e] * y.x;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (c + e >= rot) break;
+            const bool first = c + e < hr;
+            const float2 y = __ldg(reinterpret_cast<const float2*>(f) + (first ? c + e : c + e - hr));
+            const float w = to_f32(x[first ? c + e + hr : c + e - hr]);
+            out[e] = first ? out[e] * y.x - w * y.y : w * y.y + out[e] * y.x;
+        }
+    }
 }
 
 // What a block works on.
@@ -116,7 +147,6 @@ __device__ __forceinline__ Place place_of(const DecArgs& a, int tokens_per_tile)
         p.idle = true;
         if (threadIdx.x == 0) atomicOr(a.err, kErrCacheLen);
     }
-    // positions go up to len + the largest depth; checked per token where the table is read
     const int64_t n = p.idle ? 0 : p.len;
     const int64_t chunk = (n + (int64_t)a.n_split * tokens_per_tile - 1) / ((int64_t)a.n_split * tokens_per_tile) * tokens_per_tile;
     p.from = min(n, chunk * p.split);
@@ -124,11 +154,16 @@ __device__ __forceinline__ Place place_of(const DecArgs& a, int tokens_per_tile)
     p.tail = p.split == a.n_split - 1;
     return p;
 }
-// Whether every token's position lies inside the table.
-__device__ __forceinline__ bool positions_ok(const DecArgs& a, const Place& p) {
-    if (a.rot == 0) return true;
+// What each drafted token sees and the table row of its position; false where a position is outside the table.
+__device__ __forceinline__ bool look_up(const DecArgs& a, const Place& p, uint64_t* seen, const float** turn) {
     bool ok = true;
-    for (int m = threadIdx.x; m < a.M; m += kThreads) ok = ok && p.len + depth_of(seen_by(a, p.b, m), m) < a.max_pos;
+    for (int m = threadIdx.x; m < a.M; m += kThreads) {
+        const uint64_t s = seen_by(a, p.b, m);
+        const int64_t pos = p.len + depth_of(s, m);
+        ok = ok && (a.rot == 0 || pos < a.max_pos);
+        seen[m] = s;
+        turn[m] = a.rot ? a.cs + pos * a.rot : nullptr;
+    }
     return __syncthreads_and(ok) != 0;
 }
 
@@ -242,12 +277,14 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
                                                                __nv_bfloat16* k_cache, __nv_bfloat16* v_cache,
                                                                __nv_bfloat16* __restrict__ o, const DecArgs a) {
     using S = DecSmem<HD, RW>;
-    constexpr int ROWS = 16 * RW, TW = 4 / RW, GROUPS = RW;      // a warp: 16 rows, GROUPS x 16 tokens of each tile
+    constexpr int ROWS = 16 * RW, TW = 4 / RW;                   // a warp: 16 rows, 64 / TW tokens of each tile,
+    constexpr int NT = RW == 1 ? 16 : 32, GROUPS = kTok / TW / NT;   // in groups of NT
     constexpr int C = HD / 8;                                    // 16-byte chunks per row
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ float smax[TW * ROWS], ssum[TW * ROWS];
     __shared__ uint64_t seen[64];
-    __shared__ float scratch[4][16][17];
+    __shared__ const float* turn[64];
+    __shared__ float scratch[4][16][NT + 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rw = warp % RW, tw = warp / RW;
     Place p = place_of<ROWS>(a, kTok);
@@ -271,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
     };
 #pragma unroll
     for (int t = 0; t < kStages - 1; ++t) fetch(t);
-    if (!p.idle && !positions_ok(a, p)) {
+    if (!p.idle && !look_up(a, p, seen, turn)) {
         p.idle = true;
         if (threadIdx.x == 0) atomicOr(a.err, kErrRopePos);
     }
@@ -280,21 +317,24 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
         zero_rows<__nv_bfloat16, ROWS>(a, p, o);
         return;
     }
-    for (int m = threadIdx.x; m < a.M; m += kThreads) seen[m] = seen_by(a, p.b, m);
     // q, rotated, as value and remainder, through the last stage of the ring
     uint8_t* sq = sm + (kStages - 1) * 2 * S::half;
-    for (int i = threadIdx.x; i < ROWS * HD; i += kThreads) {
-        const int r = i / HD, c = i % HD, row = p.tile * ROWS + r;
-        float x = 0.f;
-        if (row < a.rows && c < a.hd) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < ROWS * C; i += kThreads) {
+        const int r = i / C, c = i % C, row = p.tile * ROWS + r;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (row < a.rows && c * 8 < a.hd) {
             const int m = row / a.group, g = row - m * a.group;
-            const float* f = a.rot ? a.cs + (p.len + depth_of(seen_by(a, p.b, m), m)) * a.rot : nullptr;
-            x = turned(q + (p.b * a.M + m) * a.qs + ((int64_t)p.kv * a.group + g) * a.hd, c, f, a.rot, a.half);
+            turned(q + (p.b * a.M + m) * a.qs + ((int64_t)p.kv * a.group + g) * a.hd, c * 8, turn[m], a.rot, a.half, x);
         }
-        const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-        const uint32_t at = swz<HD>(r, c / 8) + (c % 8) * 2;
-        *reinterpret_cast<__nv_bfloat16*>(sq + at) = hi;
-        *reinterpret_cast<__nv_bfloat16*>(sq + ROWS * HD * 2 + at) = __float2bfloat16_rn(x - __bfloat162float(hi));
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = pack2(x[2 * e], x[2 * e + 1]);
+            lo[e] = pack2(x[2 * e] - __uint_as_float(hi[e] << 16), x[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+        }
+        *reinterpret_cast<uint4*>(sq + swz<HD>(r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(sq + ROWS * HD * 2 + swz<HD>(r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     __syncthreads();
     uint32_t qh[HD / 16][4], ql[HD / 16][4];
@@ -326,22 +366,25 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
             __syncthreads();
             bool bad = false;
             const bool write = p.tile == 0;
-            for (int i = threadIdx.x; i < kTok * HD; i += kThreads) {
-                const int r = i / HD, c = i % HD;
-                __nv_bfloat16 x = __float2bfloat16_rn(0.f), y = x;
-                if (r < a.M && c < a.hd) {
-                    const float* f = a.rot ? a.cs + (p.len + depth_of(seen[r], r)) * a.rot : nullptr;
-                    x = __float2bfloat16_rn(turned(k + (p.b * a.M + r) * a.ks + (int64_t)p.kv * a.hd, c, f, a.rot, a.half));
-                    y = v[(p.b * a.M + r) * a.vs + (int64_t)p.kv * a.hd + c];
-                    bad = bad || !(fabsf(__bfloat162float(y)) < INFINITY);
+#pragma unroll 4
+            for (int i = threadIdx.x; i < kTok * C; i += kThreads) {
+                const int r = i / C, c = i % C;
+                uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                if (r < a.M && c * 8 < a.hd) {
+                    float f[8];
+                    turned(k + (p.b * a.M + r) * a.ks + (int64_t)p.kv * a.hd, c * 8, turn[r], a.rot, a.half, f);
+                    x = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+                    y = __ldg(reinterpret_cast<const uint4*>(v + (p.b * a.M + r) * a.vs + (int64_t)p.kv * a.hd + c * 8));
+                    // an exponent of ones in either half of a word
+                    auto odd = [](uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
+                    bad = bad || (odd(y.x) | odd(y.y) | odd(y.z) | odd(y.w));
                     if (write) {
-                        k_cache[(slot + p.len + r) * a.hd + c] = x;
-                        v_cache[(slot + p.len + r) * a.hd + c] = y;
+                        *reinterpret_cast<uint4*>(k_cache + (slot + p.len + r) * a.hd + c * 8) = x;
+                        *reinterpret_cast<uint4*>(v_cache + (slot + p.len + r) * a.hd + c * 8) = y;
                     }
                 }
-                const uint32_t at = swz<HD>(r, c / 8) + (c % 8) * 2;
-                *reinterpret_cast<__nv_bfloat16*>(tile + at) = x;
-                *reinterpret_cast<__nv_bfloat16*>(tile + S::half + at) = y;
+                *reinterpret_cast<uint4*>(tile + swz<HD>(r, c)) = x;
+                *reinterpret_cast<uint4*>(tile + S::half + swz<HD>(r, c)) = y;
             }
             poison = __syncthreads_or(bad) != 0;
         }
@@ -349,29 +392,32 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
         const int64_t left = draft ? a.M : p.to - p.from - (int64_t)t * kTok;     // real rows of the tile
 #pragma unroll
         for (int gi = 0; gi < GROUPS; ++gi) {
-            const int c0 = 16 * (GROUPS * tw + gi);              // first of 16 tokens
-            if (c0 >= left) continue;
-            float s[2][4];
+            const int c0 = NT * (GROUPS * tw + gi);              // first of NT tokens
+            if (c0 >= left || p.tile * ROWS + 16 * rw >= a.rows) continue;
+            float s[NT / 8][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NT / 8; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < HD / 16; ++c) {
-                uint32_t b[4];
-                ldsm4(b, kt + swz<HD>(c0 + (lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1)));
-                mma16816(s[0], qh[c], b[0], b[1]);
-                mma16816(s[1], qh[c], b[2], b[3]);
-                if (a.rot) {
-                    mma16816(s[0], ql[c], b[0], b[1]);
-                    mma16816(s[1], ql[c], b[2], b[3]);
+#pragma unroll
+                for (int n = 0; n < NT / 16; ++n) {
+                    uint32_t b[4];
+                    ldsm4(b, kt + swz<HD>(c0 + 16 * n + (lane & 7) + ((lane >> 4) << 3), 2 * c + ((lane >> 3) & 1)));
+                    mma16816(s[2 * n], qh[c], b[0], b[1]);
+                    mma16816(s[2 * n + 1], qh[c], b[2], b[3]);
+                    if (a.rot) {
+                        mma16816(s[2 * n], ql[c], b[0], b[1]);
+                        mma16816(s[2 * n + 1], ql[c], b[2], b[3]);
+                    }
                 }
             }
             // rows 16 rw + lane / 4 (e 0, 1) and + 8 (e 2, 3), tokens c0 + 8 n + 2 (lane % 4) + (e & 1)
             uint32_t hidden = 0;
             if (draft || left < kTok) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NT / 8; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int tok = c0 + 8 * n + 2 * (lane & 3) + (e & 1);
@@ -383,22 +429,26 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
                         }
                     }
             }
-            uint32_t pa[4];
+            uint32_t pa[NT / 16][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float top = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+                float top = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < NT / 8; ++n) top = fmaxf(top, fmaxf(s[n][2 * h], s[n][2 * h + 1]));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
                 const float now = fmaxf(mx[h], top * cs), use = now == -INFINITY ? 0.f : now;
                 const float corr = exp2f(mx[h] - use);
                 mx[h] = now;
+                float add = 0.f;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) s[n][2 * h + e] = exp2f(fmaf(s[n][2 * h + e], cs, -use));
-                sum[h] = sum[h] * corr + ((s[0][2 * h] + s[0][2 * h + 1]) + (s[1][2 * h] + s[1][2 * h + 1]));
-                pa[h] = pack2(s[0][2 * h], s[0][2 * h + 1]);
-                pa[2 + h] = pack2(s[1][2 * h], s[1][2 * h + 1]);
+                for (int n = 0; n < NT / 8; ++n) {
+                    s[n][2 * h] = exp2f(fmaf(s[n][2 * h], cs, -use));
+                    s[n][2 * h + 1] = exp2f(fmaf(s[n][2 * h + 1], cs, -use));
+                    add += s[n][2 * h] + s[n][2 * h + 1];
+                    pa[n / 2][2 * (n & 1) + h] = pack2(s[n][2 * h], s[n][2 * h + 1]);
+                }
+                sum[h] = sum[h] * corr + add;
                 if (corr != 1.f) {
 #pragma unroll
                     for (int n = 0; n < HD / 8; ++n) {
@@ -409,23 +459,25 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
             }
             if (!poison) {
 #pragma unroll
-                for (int n = 0; n < HD / 16; ++n) {
-                    uint32_t b[4];
-                    ldsm4t(b, vt + swz<HD>(c0 + (lane & 15), 2 * n + (lane >> 4)));
-                    mma16816(acc[2 * n], pa, b[0], b[1]);
-                    mma16816(acc[2 * n + 1], pa, b[2], b[3]);
-                }
+                for (int n = 0; n < HD / 16; ++n)
+#pragma unroll
+                    for (int x = 0; x < NT / 16; ++x) {
+                        uint32_t b[4];
+                        ldsm4t(b, vt + swz<HD>(c0 + 16 * x + (lane & 15), 2 * n + (lane >> 4)));
+                        mma16816(acc[2 * n], pa[x], b[0], b[1]);
+                        mma16816(acc[2 * n + 1], pa[x], b[2], b[3]);
+                    }
             } else {
                 // term by term, without the masked ones (0 x NaN would be NaN); a masked place is marked by -1
                 __syncwarp();
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NT / 8; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         scratch[warp][(lane >> 2) + 8 * (e >> 1)][8 * n + 2 * (lane & 3) + (e & 1)] =
                             hidden >> (4 * n + e) & 1 ? -1.f : s[n][e];
                 __syncwarp();
-                for (int c = 0; c < 16; ++c)
+                for (int c = 0; c < NT; ++c)
 #pragma unroll
                     for (int n = 0; n < HD / 8; ++n)
 #pragma unroll
@@ -477,6 +529,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
     __shared__ __align__(16) float sq[kRowsF][HD];
     __shared__ float smax[kRowsF], ssum[kRowsF];
     __shared__ uint64_t seen[64];
+    __shared__ const float* turn[64];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Place p = place_of<kRowsF>(a, kTokF);
     const int64_t slot = (p.b * a.kvh + p.kv) * a.max_len;
@@ -499,7 +552,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
     };
 #pragma unroll
     for (int t = 0; t < kStages - 1; ++t) fetch(t);
-    if (!p.idle && !positions_ok(a, p)) {
+    if (!p.idle && !look_up(a, p, seen, turn)) {
         p.idle = true;
         if (threadIdx.x == 0) atomicOr(a.err, kErrRopePos);
     }
@@ -508,16 +561,15 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
         zero_rows<float, kRowsF>(a, p, o);
         return;
     }
-    for (int m = threadIdx.x; m < a.M; m += kThreads) seen[m] = seen_by(a, p.b, m);
-    for (int i = threadIdx.x; i < kRowsF * HD; i += kThreads) {
-        const int r = i / HD, c = i % HD, row = p.tile * kRowsF + r;
-        float x = 0.f;
-        if (row < a.rows && c < a.hd) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kRowsF * C; i += kThreads) {
+        const int r = i / C, c = i % C, row = p.tile * kRowsF + r;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (row < a.rows && c * 4 < a.hd) {
             const int m = row / a.group, g = row - m * a.group;
-            const float* f = a.rot ? a.cs + (p.len + depth_of(seen_by(a, p.b, m), m)) * a.rot : nullptr;
-            x = turned(q + (p.b * a.M + m) * a.qs + ((int64_t)p.kv * a.group + g) * a.hd, c, f, a.rot, a.half);
+            turned(q + (p.b * a.M + m) * a.qs + ((int64_t)p.kv * a.group + g) * a.hd, c * 4, turn[m], a.rot, a.half, x);
         }
-        sq[r][c] = x;
+        *reinterpret_cast<float4*>(&sq[r][c * 4]) = make_float4(x[0], x[1], x[2], x[3]);
     }
     __syncthreads();
     float acc[4][E], mx[4], sum[4];
@@ -543,21 +595,21 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
             copies_wait<0>();
             __syncthreads();
             const bool write = p.tile == 0;
-            for (int i = threadIdx.x; i < kTokF * HD; i += kThreads) {
-                const int r = i / HD, c = i % HD, m = d0 + r;
-                float x = 0.f, y = 0.f;
-                if (m < a.M && c < a.hd) {
-                    const float* f = a.rot ? a.cs + (p.len + depth_of(seen[m], m)) * a.rot : nullptr;
-                    x = turned(k + (p.b * a.M + m) * a.ks + (int64_t)p.kv * a.hd, c, f, a.rot, a.half);
-                    y = v[(p.b * a.M + m) * a.vs + (int64_t)p.kv * a.hd + c];
+#pragma unroll 4
+            for (int i = threadIdx.x; i < kTokF * C; i += kThreads) {
+                const int r = i / C, c = i % C, m = d0 + r;
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (m < a.M && c * 4 < a.hd) {
+                    turned(k + (p.b * a.M + m) * a.ks + (int64_t)p.kv * a.hd, c * 4, turn[m], a.rot, a.half, x);
+                    y = __ldg(reinterpret_cast<const float4*>(v + (p.b * a.M + m) * a.vs + (int64_t)p.kv * a.hd + c * 4));
                     if (write) {
-                        k_cache[(slot + p.len + m) * a.hd + c] = x;
-                        v_cache[(slot + p.len + m) * a.hd + c] = y;
+                        *reinterpret_cast<float4*>(k_cache + (slot + p.len + m) * a.hd + c * 4) = make_float4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<float4*>(v_cache + (slot + p.len + m) * a.hd + c * 4) = y;
                     }
                 }
-                const uint32_t at = place(r, c / 4) + (c % 4) * 4;
-                *reinterpret_cast<float*>(tile + at) = x;
-                *reinterpret_cast<float*>(tile + kHalf + at) = y;
+                *reinterpret_cast<float4*>(tile + place(r, c)) = make_float4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<float4*>(tile + kHalf + place(r, c)) = y;
             }
             __syncthreads();
         }
