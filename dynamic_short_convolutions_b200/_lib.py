@@ -143,14 +143,21 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The handle of a device's current stream without building a torch.cuda.Stream around it (a microsecond of
+# every call) where this torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, ref: torch.Tensor):
     if stream is not None:
-        return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    dev = ref.device if ref is not None and ref.device.type == "cuda" else None
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    dev = ref.device if ref is not None and ref.is_cuda else None
+    if dev is not None and dev.index is not None and _raw_stream is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _check(status: int):

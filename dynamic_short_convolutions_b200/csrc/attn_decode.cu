@@ -21,6 +21,7 @@
 #include "attn.h"
 #include "common.cuh"
 #include "prof.h"
+#include "smem_limit.h"
 
 namespace dynconv {
 namespace {
@@ -37,7 +38,8 @@ struct DecArgs {
     const int32_t* lens;
     const uint64_t* tree;
     float scale;
-    float* part;                                     // [batch, kvh, row tiles][n_split][rows of a tile][HD + 2]
+    float* part;                                     // per [batch, kvh, row tile]: o [n_split][rows][HD], then maximum and
+                                                     // sum [n_split][rows][2]
     uint32_t* count;                                 // [batch, kvh, row tiles]
     uint32_t* err;
 };
@@ -167,23 +169,35 @@ __device__ __forceinline__ bool look_up(const DecArgs& a, const Place& p, uint64
     return __syncthreads_and(ok) != 0;
 }
 
-// Joins NP partial results of ROWS rows in shared memory (o [NP][ROWS][HD] not yet divided by l, m and l [NP][ROWS])
-// and either writes o or leaves this run's part and, as the last block of its rows, joins the runs.
+// Joins NP partial results of ROWS rows in shared memory (so [NP][ROWS][HD] not yet divided by the sum, smax and
+// ssum [NP][ROWS]) and either writes o or leaves this run's part and, as the last block of its rows, joins the
+// runs.  The loads of a join are independent of one another (weights first, then 16 values in flight per
+// thread and more): a load and its use in turn, run by run, took longer than the attention itself.
+// `weights`: shared memory for ROWS x n_split floats (n_split <= 64).
 template <typename T, int HD, int ROWS, int NP>
 __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const float* so, const float* smax,
-                                       const float* ssum, T* __restrict__ o) {
+                                       const float* ssum, float* weights, T* __restrict__ o) {
     __shared__ int last;
-    constexpr int kLd = HD + 2;
+    __shared__ float inverse[ROWS];
+    constexpr int kItems = ROWS * HD / 4 / kThreads;             // runs of four channels per thread
     const int tiles = (a.rows + ROWS - 1) / ROWS;
     const int64_t group = (p.b * a.kvh + p.kv) * tiles + p.tile;
     const int rows = min(ROWS, a.rows - p.tile * ROWS);
-    float* mine = a.part + (group * a.n_split + p.split) * (ROWS * kLd);
-    auto out_at = [&](int r) {
+    float* parts = a.part + group * a.n_split * (int64_t)(ROWS * (HD + 2));
+    float* stats = parts + (int64_t)a.n_split * ROWS * HD;       // [n_split][ROWS][2]: maximum, sum
+    auto put = [&](int r, int c, float4 s, float inv) {
         const int row = p.tile * ROWS + r, m = row / a.group, g = row - m * a.group;
-        return o + (p.b * a.M + m) * a.os + ((int64_t)p.kv * a.group + g) * a.hd;
+        T* to = o + (p.b * a.M + m) * a.os + ((int64_t)p.kv * a.group + g) * a.hd + c;
+        if (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(to) = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+        } else {
+            *reinterpret_cast<uint2*>(to) = make_uint2(pack2(s.x * inv, s.y * inv), pack2(s.z * inv, s.w * inv));
+        }
     };
-    for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {
-        const int r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+#pragma unroll
+    for (int it = 0; it < kItems; ++it) {
+        const int i = threadIdx.x + it * kThreads, r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+        if (r >= rows) break;
         float mx = -INFINITY, l = 0.f;
 #pragma unroll
         for (int n = 0; n < NP; ++n) mx = fmaxf(mx, smax[n * ROWS + r]);
@@ -193,21 +207,14 @@ __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const f
         for (int n = 0; n < NP; ++n) {
             const float w = exp2f(smax[n * ROWS + r] - use);
             const float4 x = *reinterpret_cast<const float4*>(so + (n * ROWS + r) * HD + c);
-            // a part without keys holds zeros; others may hold what a NaN made of them
             s.x += w * x.x; s.y += w * x.y; s.z += w * x.z; s.w += w * x.w;
             l += w * ssum[n * ROWS + r];
         }
         if (a.n_split == 1) {
-            const float inv = l > 0.f ? 1.f / l : l;
-            if (c < a.hd) {
-                T* to = out_at(r) + c;
-                to[0] = from_f32<T>(s.x * inv); to[1] = from_f32<T>(s.y * inv);
-                to[2] = from_f32<T>(s.z * inv); to[3] = from_f32<T>(s.w * inv);
-            }
+            if (c < a.hd) put(r, c, s, l > 0.f ? 1.f / l : l);
         } else {
-            float* to = mine + r * kLd;
-            to[c] = s.x; to[c + 1] = s.y; to[c + 2] = s.z; to[c + 3] = s.w;
-            if (c == 0) { to[HD] = mx; to[HD + 1] = l; }
+            *reinterpret_cast<float4*>(parts + ((int64_t)p.split * ROWS + r) * HD + c) = s;
+            if (c == 0) *reinterpret_cast<float2*>(stats + (p.split * ROWS + r) * 2) = make_float2(mx, l);
         }
     }
     if (a.n_split == 1) return;
@@ -221,25 +228,50 @@ __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const f
     }
     __syncthreads();
     if (!last) return;
-    const float* all = a.part + group * a.n_split * (int64_t)(ROWS * kLd);
-    for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {
-        const int r = i / (HD / 4), c = (i % (HD / 4)) * 4;
-        if (c >= a.hd) continue;
-        float mx = -INFINITY, l = 0.f;
-        for (int n = 0; n < a.n_split; ++n) mx = fmaxf(mx, __ldcg(all + n * (ROWS * kLd) + r * kLd + HD));
+    float* sums = weights + ROWS * a.n_split;
+    for (int i = threadIdx.x; i < a.n_split * rows; i += kThreads) {
+        const int n = i / rows, r = i - n * rows;
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(stats + (n * ROWS + r) * 2));
+        weights[r * a.n_split + n] = x.x;
+        sums[r * a.n_split + n] = x.y;
+    }
+    __syncthreads();
+    if (threadIdx.x < rows) {
+        float* w = weights + threadIdx.x * a.n_split;
+        const float* l = sums + threadIdx.x * a.n_split;
+        float mx = -INFINITY, sum = 0.f;
+        for (int n = 0; n < a.n_split; ++n) mx = fmaxf(mx, w[n]);
         const float use = mx == -INFINITY ? 0.f : mx;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
         for (int n = 0; n < a.n_split; ++n) {
-            const float* x = all + n * (ROWS * kLd) + r * kLd;
-            const float w = exp2f(__ldcg(x + HD) - use);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] += w * __ldcg(x + c + e);
-            l += w * __ldcg(x + HD + 1);
+            w[n] = exp2f(w[n] - use);
+            sum += w[n] * l[n];
         }
-        const float inv = l > 0.f ? 1.f / l : l;
-        T* to = out_at(r) + c;
+        inverse[threadIdx.x] = sum > 0.f ? 1.f / sum : sum;
+    }
+    __syncthreads();
+    float4 s[kItems];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) to[e] = from_f32<T>(s[e] * inv);
+    for (int it = 0; it < kItems; ++it) s[it] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll (kItems >= 8 ? 1 : 16 / kItems)
+    for (int n = 0; n < a.n_split; ++n) {
+        float4 x[kItems];
+#pragma unroll
+        for (int it = 0; it < kItems; ++it) {
+            const int i = threadIdx.x + it * kThreads, r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+            x[it] = r < rows ? __ldcg(reinterpret_cast<const float4*>(parts + ((int64_t)n * ROWS + r) * HD + c))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int it = 0; it < kItems; ++it) {
+            const int r = (threadIdx.x + it * kThreads) / (HD / 4);
+            const float w = r < rows ? weights[r * a.n_split + n] : 0.f;
+            s[it].x += w * x[it].x; s[it].y += w * x[it].y; s[it].z += w * x[it].z; s[it].w += w * x[it].w;
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < kItems; ++it) {
+        const int i = threadIdx.x + it * kThreads, r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+        if (r < rows && c < a.hd) put(r, c, s[it], inverse[r]);
     }
 }
 
@@ -366,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
             __syncthreads();
             bool bad = false;
             const bool write = p.tile == 0;
-#pragma unroll 4
+#pragma unroll 2
             for (int i = threadIdx.x; i < kTok * C; i += kThreads) {
                 const int r = i / C, c = i % C;
                 uint4 x = make_uint4(0, 0, 0, 0), y = x;
@@ -390,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
         }
         const uint32_t kt = smem_at(tile), vt = kt + S::half;
         const int64_t left = draft ? a.M : p.to - p.from - (int64_t)t * kTok;     // real rows of the tile
-#pragma unroll
+#pragma unroll 1
         for (int gi = 0; gi < GROUPS; ++gi) {
             const int c0 = NT * (GROUPS * tw + gi);              // first of NT tokens
             if (c0 >= left || p.tile * ROWS + 16 * rw >= a.rows) continue;
@@ -477,6 +509,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
                         scratch[warp][(lane >> 2) + 8 * (e >> 1)][8 * n + 2 * (lane & 3) + (e & 1)] =
                             hidden >> (4 * n + e) & 1 ? -1.f : s[n][e];
                 __syncwarp();
+#pragma unroll 1
                 for (int c = 0; c < NT; ++c)
 #pragma unroll
                     for (int n = 0; n < HD / 8; ++n)
@@ -510,7 +543,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
             *reinterpret_cast<float2*>(so + r * HD + 8 * n + 2 * (lane & 3)) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
     }
     __syncthreads();
-    finish<__nv_bfloat16, HD, ROWS, TW>(a, p, so, smax, ssum, o);
+    finish<__nv_bfloat16, HD, ROWS, TW>(a, p, so, smax, ssum, so + TW * ROWS * HD, o);
 }
 
 // ---------------------------------------------------------------- fp32
@@ -676,7 +709,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
         for (int e = 0; e < E; ++e) so[(4 * warp + r) * HD + lane * E + e] = acc[r][e];
     }
     __syncthreads();
-    finish<float, HD, kRowsF, 1>(a, p, so, smax, ssum, o);
+    finish<float, HD, kRowsF, 1>(a, p, so, smax, ssum, so + kRowsF * HD, o);
 }
 
 // Rows a block takes: 16 or 32 where they are all there are (its warps then share out the tokens), else 64.
@@ -686,13 +719,27 @@ int tile_rows(const DecodeProb& p) {
     return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-template <typename F, typename T>
-cudaError_t launch(F* f, size_t smem, unsigned grid, const T* q, const T* k, const T* v, T* kc, T* vc, T* o,
-                   const DecArgs& a, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <typename T, typename F>
+cudaError_t launch(std::atomic<uint64_t>& limit, F* f, size_t smem, unsigned grid, const void* q, const void* k,
+                   const void* v, void* kc, void* vc, void* o, const DecArgs& a, cudaStream_t st) {
+    cudaError_t e = smem_limit(limit, reinterpret_cast<const void*>(f), smem);
     if (e != cudaSuccess) return e;
-    DC_LAUNCH(kAttnDecode, st, f<<<grid, kThreads, smem, st>>>(q, k, v, kc, vc, o, a));
+    DC_LAUNCH(kAttnDecode, st, f<<<grid, kThreads, smem, st>>>(static_cast<const T*>(q), static_cast<const T*>(k),
+                                                               static_cast<const T*>(v), static_cast<T*>(kc),
+                                                               static_cast<T*>(vc), static_cast<T*>(o), a));
     return cudaGetLastError();
+}
+template <int HD>
+cudaError_t launch_f32(unsigned grid, const void* q, const void* k, const void* v, void* kc, void* vc, void* o,
+                       const DecArgs& a, cudaStream_t st) {
+    static std::atomic<uint64_t> limit{0};
+    return launch<float>(limit, attn_decode_f32_kernel<HD>, kStages * 2 * kTokF * HD * 4, grid, q, k, v, kc, vc, o, a, st);
+}
+template <int HD, int RW>
+cudaError_t launch_bf16(unsigned grid, const void* q, const void* k, const void* v, void* kc, void* vc, void* o,
+                        const DecArgs& a, cudaStream_t st) {
+    static std::atomic<uint64_t> limit{0};
+    return launch<__nv_bfloat16>(limit, attn_decode_kernel<HD, RW>, DecSmem<HD, RW>::bytes, grid, q, k, v, kc, vc, o, a, st);
 }
 
 }  // namespace
@@ -702,11 +749,14 @@ int64_t attn_decode_groups(const DecodeProb& p) {
     return p.batch * p.kvh * (((int64_t)p.M * p.group + rows - 1) / rows);
 }
 
-// Runs the cache is split into: enough blocks for four per SM, but no run of a full cache below 128 tokens (two tiles).
+// Runs the cache is split into: as many as keep all blocks on the GPU at once (two per SM), but no run of a
+// full cache below four tiles.  Measured: 8 sequences x 24 tokens over ~2600 cached rows take 62 us with 4 runs,
+// 72 with 6, 84 with 2; one sequence of 12 heads over ~1200 rows 8.7 us with runs of at least 256 rows, 9.3 with
+// 128; 64 sequences do not care (88 us with 1 to 3 runs).
 int attn_decode_splits(const DecodeProb& p) {
     const int64_t groups = std::max<int64_t>(1, attn_decode_groups(p));
-    const int64_t want = (4 * 148 + groups - 1) / groups;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({want, (p.max_len + 127) / 128, 64}));
+    const int64_t shortest = 4 * (p.dtype == 0 ? kTokF : kTok);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * 148 / groups, (p.max_len + shortest - 1) / shortest, 64}));
 }
 
 size_t attn_decode_part_bytes(const DecodeProb& p) {
@@ -720,23 +770,16 @@ cudaError_t attn_decode(const DecodeProb& p, const void* q, const void* k, const
     DecArgs a{p.M, p.heads, p.kvh, p.group, p.hd, p.M * p.group, attn_decode_splits(p), p.max_len, p.qs, p.ks, p.vs, p.os,
               p.rot, p.half, p.max_pos, p.cs, lens, tree, p.scale, part, count, err};
     const unsigned grid = (unsigned)(attn_decode_groups(p) * a.n_split);
-    if (p.dtype == 0) {
-        const float *qf = static_cast<const float*>(q), *kf = static_cast<const float*>(k), *vf = static_cast<const float*>(v);
-        float *kcf = static_cast<float*>(kc), *vcf = static_cast<float*>(vc), *of = static_cast<float*>(o);
-        return p.hd <= 64 ? launch(attn_decode_f32_kernel<64>, kStages * 2 * kTokF * 64 * 4, grid, qf, kf, vf, kcf, vcf, of, a, st)
-                          : launch(attn_decode_f32_kernel<128>, kStages * 2 * kTokF * 128 * 4, grid, qf, kf, vf, kcf, vcf, of, a, st);
-    }
-    using B = __nv_bfloat16;
-    const B *qb = static_cast<const B*>(q), *kb = static_cast<const B*>(k), *vb = static_cast<const B*>(v);
-    B *kcb = static_cast<B*>(kc), *vcb = static_cast<B*>(vc), *ob = static_cast<B*>(o);
+    if (p.dtype == 0)
+        return p.hd <= 64 ? launch_f32<64>(grid, q, k, v, kc, vc, o, a, st) : launch_f32<128>(grid, q, k, v, kc, vc, o, a, st);
     const int rows = tile_rows(p);
     if (p.hd <= 64)
-        return rows == 16   ? launch(attn_decode_kernel<64, 1>, DecSmem<64, 1>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st)
-               : rows == 32 ? launch(attn_decode_kernel<64, 2>, DecSmem<64, 2>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st)
-                            : launch(attn_decode_kernel<64, 4>, DecSmem<64, 4>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st);
-    return rows == 16   ? launch(attn_decode_kernel<128, 1>, DecSmem<128, 1>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st)
-           : rows == 32 ? launch(attn_decode_kernel<128, 2>, DecSmem<128, 2>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st)
-                        : launch(attn_decode_kernel<128, 4>, DecSmem<128, 4>::bytes, grid, qb, kb, vb, kcb, vcb, ob, a, st);
+        return rows == 16   ? launch_bf16<64, 1>(grid, q, k, v, kc, vc, o, a, st)
+               : rows == 32 ? launch_bf16<64, 2>(grid, q, k, v, kc, vc, o, a, st)
+                            : launch_bf16<64, 4>(grid, q, k, v, kc, vc, o, a, st);
+    return rows == 16   ? launch_bf16<128, 1>(grid, q, k, v, kc, vc, o, a, st)
+           : rows == 32 ? launch_bf16<128, 2>(grid, q, k, v, kc, vc, o, a, st)
+                        : launch_bf16<128, 4>(grid, q, k, v, kc, vc, o, a, st);
 }
 
 }  // namespace dynconv

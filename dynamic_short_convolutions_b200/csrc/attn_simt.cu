@@ -21,6 +21,7 @@
 #include "attn.h"
 #include "common.cuh"
 #include "prof.h"
+#include "smem_limit.h"
 
 namespace dynconv {
 namespace {
@@ -424,16 +425,11 @@ int vec_ok(const AttnProb& p, bool bwd) {
     return p.hd % 4 == 0 && p.qs % 4 == 0 && p.ks % 4 == 0 && p.vs % 4 == 0 && (!bwd || p.dos % 4 == 0);
 }
 
-template <typename F>
-cudaError_t big_smem(F* f, size_t bytes) {
-    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 template <typename T, int HD>
 cudaError_t fwd_t(const AttnProb& p, const void* q, const void* k, const void* v, void* o, float* lse,
                   cudaStream_t st) {
     constexpr size_t smem = sizeof(float) * 3 * kTile * ld_of<HD>();
-    cudaError_t e = big_smem(attn_fwd_simt_kernel<T, HD>, smem);
+    cudaError_t e = DC_SMEM_LIMIT((attn_fwd_simt_kernel<T, HD>), smem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((p.N + kTile - 1) / kTile * p.heads);
     DC_LAUNCH(kAttnSimtFwd, st, attn_fwd_simt_kernel<T, HD><<<grid, kThreads, smem, st>>>(
@@ -447,8 +443,8 @@ cudaError_t bwd_t(const AttnProb& p, const void* d_o, const void* q, const void*
                   const float* delta, void* dq, void* dk, void* dv, cudaStream_t st) {
     constexpr size_t smem_q = sizeof(float) * 4 * kTile * ld_of<HD>();
     constexpr size_t smem_kv = smem_q + sizeof(float) * 2 * kTile * kLdP;
-    cudaError_t e = big_smem(attn_dq_simt_kernel<T, HD>, smem_q);
-    if (e == cudaSuccess) e = big_smem(attn_dkv_simt_kernel<T, HD>, smem_kv);
+    cudaError_t e = DC_SMEM_LIMIT((attn_dq_simt_kernel<T, HD>), smem_q);
+    if (e == cudaSuccess) e = DC_SMEM_LIMIT((attn_dkv_simt_kernel<T, HD>), smem_kv);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kTile - 1) / kTile;
     DC_LAUNCH(kAttnSimtDkv, st, attn_dkv_simt_kernel<T, HD><<<(unsigned)(tiles * p.kvh), kThreads, smem_kv, st>>>(

@@ -26,6 +26,7 @@
 
 #include "attn_tc.cuh"
 #include "prof.h"
+#include "smem_limit.h"
 
 namespace dynconv {
 namespace attn_tc {
@@ -597,8 +598,8 @@ template <int HD>
 cudaError_t bwd_hd(const AttnProb& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const CUtensorMap& td, const AttnTcArgs& a, cudaStream_t st) {
     constexpr uint32_t smem = BwdSmem<HD>::bytes;
-    cudaError_t e = cudaFuncSetAttribute(attn_dkv_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(attn_dq_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = DC_SMEM_LIMIT(attn_dkv_kernel<HD>, smem);
+    if (e == cudaSuccess) e = DC_SMEM_LIMIT(attn_dq_kernel<HD>, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kRows - 1) / kRows;
     DC_LAUNCH(kAttnTcDkv, st, attn_dkv_kernel<HD><<<(unsigned)(tiles * p.kvh), kBwdThreads, smem, st>>>(tq, tk, tv, td, a));

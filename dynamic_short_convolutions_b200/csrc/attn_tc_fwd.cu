@@ -23,6 +23,7 @@
 
 #include "attn_tc.cuh"
 #include "prof.h"
+#include "smem_limit.h"
 
 namespace dynconv {
 namespace attn_tc {
@@ -376,7 +377,7 @@ template <int HD>
 cudaError_t fwd_hd(const AttnProb& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const AttnTcArgs& a, cudaStream_t st) {
     constexpr uint32_t smem = FwdSmem<HD>::bytes;
-    cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = DC_SMEM_LIMIT(attn_fwd_kernel<HD>, smem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((p.N + 2 * kRows - 1) / (2 * kRows) * p.heads);
     DC_LAUNCH(kAttnTcFwd, st, attn_fwd_kernel<HD><<<grid, kFwdThreads, smem, st>>>(tq, tk, tv, a));

@@ -59,35 +59,43 @@ def rope_table(max_pos: int, head_dim: int, base: float = 10000.0, device=None, 
     return (table if scale == 1.0 else scale * table).float().to(device or "cuda")
 
 
-def _rows(t: torch.Tensor, name: str, rows: int, width: int, dtype: torch.dtype, stride: int) -> None:
-    """A tensor of `rows` rows of `width` contiguous elements, `stride` (0: width) elements apart."""
-    if t.dtype != dtype:
+def _rows(t: torch.Tensor, name: str, rows: int, width: int, dtype: torch.dtype, stride: int,
+          device: torch.device) -> None:
+    """A tensor of `rows` rows of `width` contiguous elements, `stride` (0: width) elements apart, on `device`."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+    if t.shape != (rows, width):
         raise ValueError(f"{name} must be [{rows}, {width}], got {list(t.shape)}")
-    if (width > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (stride or width)):
+    at = t.stride()
+    if (width > 1 and at[1] != 1) or (rows > 1 and at[0] != (stride or width)):
         raise ValueError(f"{name} must have contiguous channels and a row stride of {stride or width}, "
-                         f"got strides {t.stride()}")
+                         f"got strides {at}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}: a call's tensors must be on its plan's device, {device}")
 
 
-def _ints(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape=None) -> None:
+def _flat(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, device: torch.device, shape=None) -> None:
+    """A contiguous tensor (or None) on `device`."""
     if t is None:
         return
-    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor" + (f" of shape {list(shape)}" if shape else "")
                          + f", got {t.dtype} {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}: a call's tensors must be on its plan's device, {device}")
 
 
-def _cu(t: Optional[torch.Tensor]) -> None:
-    _ints(t, "cu_seqlens", torch.int32)
-    if t is not None and (t.dim() != 1 or t.numel() < 2):
+def _cu(t: Optional[torch.Tensor], device: torch.device) -> None:
+    if t is None:
+        return
+    _flat(t, "cu_seqlens", torch.int32, device)
+    if t.dim() != 1 or t.numel() < 2:
         raise ValueError(f"cu_seqlens must be [documents + 1], got {list(t.shape)}")
 
 
-def _one_device(device: torch.device, *tensors) -> None:
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {t.device} and {device}: a call's tensors must be on its plan's device")
+def _table(t: torch.Tensor, name: str) -> None:
+    if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 [max_pos, rotated channels] tensor")
 
 
 def _device(device) -> torch.device:
@@ -247,10 +255,9 @@ class RopePlan:
                  layout: int = L.ROPE_INTERLEAVED, x_row_stride: int = 0, y_row_stride: int = 0, device=None):
         if dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"storage dtype must be bf16 or fp32, got {dtype}")
-        if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
-            raise ValueError("table must be a contiguous fp32 [max_pos, rotated channels] tensor")
+        _table(table, "table")
         self.device = table.device if device is None else _device(device)
-        _one_device(self.device, table)
+        _flat(table, "table", torch.float32, self.device)
         self.table = table                      # kept alive: the descriptors hold its address
         code = L.BF16 if dtype == torch.bfloat16 else L.F32
         self.desc = [L.make_rope_desc(code, layout, batch, seqlen, heads, head_dim, table, inv, x_row_stride,
@@ -265,11 +272,11 @@ class RopePlan:
             if self.strides[1] not in (0, self.width):
                 raise ValueError("a plan with a strided y needs the y to write")
             y = torch.empty((self.N, self.width), dtype=self.dtype, device=self.device)
-        _rows(x, "x", self.N, self.width, self.dtype, self.strides[0])
-        _rows(y, "y", self.N, self.width, self.dtype, self.strides[1])
-        _ints(positions, "positions", torch.int32, (self.N,))
-        _cu(cu_seqlens)
-        _one_device(self.device, x, y, positions, cu_seqlens)
+        else:
+            _rows(y, "y", self.N, self.width, self.dtype, self.strides[1], self.device)
+        _rows(x, "x", self.N, self.width, self.dtype, self.strides[0], self.device)
+        _flat(positions, "positions", torch.int32, self.device, (self.N,))
+        _cu(cu_seqlens, self.device)
         with _On(self.device):
             L.dynconv_rope(self.desc[int(inverse)], cu_seqlens, positions, x, y, self.ws, stream)
         return y
@@ -301,19 +308,18 @@ class AttnPlan:
         self.grad_strides = (dq_row_stride, dk_row_stride, dv_row_stride)
 
     def _inputs(self, q, k, v, cu_seqlens):
-        _rows(q, "q", self.N, self.wq, self.dtype, self.strides[0])
-        _rows(k, "k", self.N, self.wk, self.dtype, self.strides[1])
-        _rows(v, "v", self.N, self.wk, self.dtype, self.strides[2])
-        _cu(cu_seqlens)
-        _one_device(self.device, q, k, v, cu_seqlens)
+        _rows(q, "q", self.N, self.wq, self.dtype, self.strides[0], self.device)
+        _rows(k, "k", self.N, self.wk, self.dtype, self.strides[1], self.device)
+        _rows(v, "v", self.N, self.wk, self.dtype, self.strides[2], self.device)
+        _cu(cu_seqlens, self.device)
 
     def forward(self, q, k, v, cu_seqlens=None, o=None, want_lse: bool = False, stream=None):
         """o [N, heads * head_dim]; with ``want_lse`` (o, lse), lse fp32 [heads, N] for :meth:`backward`."""
         self._inputs(q, k, v, cu_seqlens)
         if o is None:
             o = torch.empty((self.N, self.wq), dtype=self.dtype, device=self.device)
-        _rows(o, "o", self.N, self.wq, self.dtype, 0)
-        _one_device(self.device, o)
+        else:
+            _rows(o, "o", self.N, self.wq, self.dtype, 0, self.device)
         lse = torch.empty((self.heads, self.N), dtype=torch.float32, device=self.device) if want_lse else None
         with _On(self.device):
             L.dynconv_attn_fwd(self.desc, cu_seqlens, q, k, v, o, lse, self.ws, stream)
@@ -333,10 +339,10 @@ class AttnPlan:
                                        ("dq", out["dq"], self.wq, self.grad_strides[0]),
                                        ("dk", out["dk"], self.wk, self.grad_strides[1]),
                                        ("dv", out["dv"], self.wk, self.grad_strides[2])):
-            _rows(t, name, self.N, width, self.dtype, stride)
-            _one_device(self.device, t)
-        _ints(lse, "lse", torch.float32, (self.heads, self.N))
-        _one_device(self.device, lse)
+            _rows(t, name, self.N, width, self.dtype, stride, self.device)
+        if lse is None:
+            raise ValueError("the backward needs the forward's lse (want_lse=True)")
+        _flat(lse, "lse", torch.float32, self.device, (self.heads, self.N))
         with _On(self.device):
             L.dynconv_attn_bwd(self.desc, cu_seqlens, d_o, q, k, v, o, lse, out["dq"], out["dk"], out["dv"], self.ws,
                                stream)
@@ -358,9 +364,8 @@ class AttnDecoder:
                  v_row_stride: int = 0, k_cache=None, v_cache=None, lens=None, device=None):
         if dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"storage dtype must be bf16 or fp32, got {dtype}")
-        if rope_table is not None and (rope_table.dtype != torch.float32 or rope_table.dim() != 2
-                                       or not rope_table.is_contiguous()):
-            raise ValueError("rope_table must be a contiguous fp32 [max_pos, rotated channels] tensor")
+        if rope_table is not None:
+            _table(rope_table, "rope_table")
         self.table = rope_table                 # kept alive: the descriptor holds its address
         self.desc = L.make_attn_decode_desc(L.BF16 if dtype == torch.bfloat16 else L.F32, batch, tokens, heads, kv_heads,
                                             head_dim, max_len, scale, rope_table, rope_layout, q_row_stride,
@@ -373,10 +378,10 @@ class AttnDecoder:
         self.k_cache = torch.zeros(shape, dtype=dtype, device=self.device) if k_cache is None else k_cache
         self.v_cache = torch.zeros(shape, dtype=dtype, device=self.device) if v_cache is None else v_cache
         self.lens = torch.zeros(batch, dtype=torch.int32, device=self.device) if lens is None else lens
-        _ints(self.k_cache, "k_cache", dtype, shape)
-        _ints(self.v_cache, "v_cache", dtype, shape)
-        _ints(self.lens, "lens", torch.int32, (batch,))
-        _one_device(self.device, self.k_cache, self.v_cache, self.lens, rope_table)
+        _flat(self.k_cache, "k_cache", dtype, self.device, shape)
+        _flat(self.v_cache, "v_cache", dtype, self.device, shape)
+        _flat(self.lens, "lens", torch.int32, self.device, (batch,))
+        _flat(rope_table, "rope_table", torch.float32, self.device)
         self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.dtype, self.batch, self.tokens = dtype, batch, tokens
         self.wq, self.wk = heads * head_dim, kv_heads * head_dim
@@ -390,12 +395,12 @@ class AttnDecoder:
         rows = self.batch * self.tokens
         if o is None:
             o = torch.empty((rows, self.wq), dtype=self.dtype, device=self.device)
-        _rows(q, "q", rows, self.wq, self.dtype, self.strides[0])
-        _rows(k, "k", rows, self.wk, self.dtype, self.strides[1])
-        _rows(v, "v", rows, self.wk, self.dtype, self.strides[2])
-        _rows(o, "o", rows, self.wq, self.dtype, 0)
-        _ints(ancestors, "ancestors", torch.int64, (self.batch, self.tokens))
-        _one_device(self.device, q, k, v, o, ancestors)
+        else:
+            _rows(o, "o", rows, self.wq, self.dtype, 0, self.device)
+        _rows(q, "q", rows, self.wq, self.dtype, self.strides[0], self.device)
+        _rows(k, "k", rows, self.wk, self.dtype, self.strides[1], self.device)
+        _rows(v, "v", rows, self.wk, self.dtype, self.strides[2], self.device)
+        _flat(ancestors, "ancestors", torch.int64, self.device, (self.batch, self.tokens))
         with _On(self.device):
             L.dynconv_attn_decode(self.desc, q, k, v, self.k_cache, self.v_cache, self.lens, ancestors, o, self.ws, stream)
         return o
