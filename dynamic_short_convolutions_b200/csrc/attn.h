@@ -47,7 +47,7 @@ cudaError_t attn_simt_bwd(const AttnProb& p, const void* d_o, const void* q, con
 cudaError_t attn_tc_fwd(const AttnProb& p, const void* q, const void* k, const void* v, void* o, float* lse,
                         uint32_t* err, cudaStream_t st);
 cudaError_t attn_tc_bwd(const AttnProb& p, const void* d_o, const void* q, const void* k, const void* v,
-                        const float* lse, const float* delta, void* dq, void* dk, void* dv, uint32_t* err,
+                        const void* o, const float* lse, float* delta, void* dq, void* dk, void* dv, uint32_t* err,
                         cudaStream_t st);
 // D[h][n] = d_o[n, h] . o[n, h], fp32.
 cudaError_t attn_delta(const AttnProb& p, const void* d_o, const void* o, float* delta, cudaStream_t st);

@@ -298,10 +298,11 @@ dynconv_status dynconv_attn_bwd(const dynconv_attn_desc* desc, const int32_t* cu
         (s = cuda_status(launch_check_seqlens(cu_seqlens, n_docs, p.N, err_of(ws), st), "cu_seqlens check")))
         return s;
     float* delta = reinterpret_cast<float*>(static_cast<char*>(ws) + attn_ws(p).delta);
+    if (attn_tc(p))
+        return cuda_status(attn_tc_bwd(p, d_o, q, k, v, o, lse, delta, dq, dk, dv, err_of(ws), st),
+                           "attention backward launch");
     if ((s = cuda_status(attn_delta(p, d_o, o, delta, st), "attention row products"))) return s;
-    return cuda_status(attn_tc(p) ? attn_tc_bwd(p, d_o, q, k, v, lse, delta, dq, dk, dv, err_of(ws), st)
-                                  : attn_simt_bwd(p, d_o, q, k, v, lse, delta, dq, dk, dv, st),
-                       "attention backward launch");
+    return cuda_status(attn_simt_bwd(p, d_o, q, k, v, lse, delta, dq, dk, dv, st), "attention backward launch");
 }
 
 size_t dynconv_attn_decode_workspace_bytes(const dynconv_attn_decode_desc* desc) {

@@ -190,7 +190,7 @@ struct AttnTcArgs {
     const __nv_bfloat16 *q, *k, *v, *d_o;
     __nv_bfloat16 *o, *dq, *dk, *dv;
     float* lse;
-    const float* delta;
+    float* delta;                                // D [heads][N], written by the dq kernel, read by the other
     int64_t qs, ks, vs, os, dos, dqs, dks, dvs;
 };
 

@@ -14,14 +14,29 @@
 // No operand passes through shared memory by hand: the transposed scores S^T = K Q^T put keys on the TMEM
 // lanes, P^T and dS^T are written back to TMEM as bf16 and are the A operands of dV and dK; in attn_dq_kernel
 // dS is the A operand of dQ.  P and dS are rounded to bf16 because the tensor cores take them so; dS is
-// computed from the fp32 P.
+// computed from the fp32 P.  In the diagonal tile, where the rows of few keys are whose gradients are the
+// largest, dS goes in as two bf16 (value and remainder).
+//
+// attn_dq_kernel runs first and leaves D for the other.  D = dO . O takes the O that the forward rounded; for
+// rows that see no key outside the diagonal tile it is taken as sum_j P dP instead, which is the same without
+// that rounding (dP - D cancels most where a row sees few keys).
+//
+// With few key tiles and large groups the heads of a group are shared out over a cluster of blocks, whose partial
+// dK and dV are added through distributed shared memory in the order of their ranks.
 //
 // Warps: 0-7 the element work (a lane is a row; warps 0-3 take columns 0-63, 4-7 columns 64-127, each
-// writing its bf16 results over scores that it alone has read), 8 MMA issue, 9 TMA, 10 infinities and NaN in
-// masked tiles (see attn_tc_fwd.cu), 11 (dkv) the rows' lse and D.  MMAs run in issue order, and the order
-// is chosen so that the tensor cores have the other half of the work while the element warps do theirs:
-//   dkv: dV(i) S(i+1) | dK(i) dP(i+1)    while the element warps compute dS(i) | P(i+1)
-//   dq:  S(i+1) dP(i+1) dQ(i)            while they compute P(i), dS(i), from registers
+// writing its bf16 results over columns that it alone has read), 8 MMA issue, 9 TMA, 10 infinities and NaN in
+// masked tiles (see attn_tc_fwd.cu), 11 (dkv) the rows' lse and D.
+//
+// What bounds them is the chain from one item (tile pair) to the next, so every wait on it is moved off:
+// the next scores are computed into S as soon as the element warps hold this item's in registers, the
+// exponentials run before the wait for dP, and the two halves of an item have ring places of their own,
+// given back as soon as their last product is done (both loads of an item together, released together, left the
+// tensor cores waiting for L2: 4250 cycles per item instead of ~2500 at HD = 128).
+//   dkv: S(i+1) | dV(i) | dK(i) dP(i+1)    P and dS lie in the columns of dP, read into registers before
+//   dq:  S(i+1) | dP(i+1) | dQ(i)          dS has two buffers of its own
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "attn_tc.cuh"
@@ -32,21 +47,106 @@ namespace dynconv {
 namespace attn_tc {
 namespace {
 
-constexpr int kBwdThreads = 384;
+namespace cg = cooperative_groups;
 
+constexpr int kBwdThreads = 384;
+// The element warps' barrier (256 threads).
+__device__ __forceinline__ void element_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// Shared memory: two resident tiles, a ring of tiles, the statistics of two items, the barriers.  No slack for
+// alignment: the dynamic part starts on a 1024-byte boundary, since these kernels have no static part (checked).
 template <int HD>
 struct BwdSmem {
     static constexpr uint32_t tile = kAtom * (HD / 64);
-    static constexpr int stages = HD == 128 ? 2 : 4;
-    static constexpr uint32_t stats = stages * 2 * kRows * sizeof(float);       // lse and D of a stage's queries
-    static constexpr uint32_t bytes = 1024 + tile * (2 + 2 * stages) + stats;
+    static constexpr int slots = HD == 128 ? 5 : 10;
+    static constexpr uint32_t ring = 2 * tile, stats = ring + slots * tile, shared = stats + 2 * 2 * kRows * sizeof(float);
+    // a block's partial dV and dK for its cluster, in the memory of the tiles: rows padded by 16 bytes, so that
+    // a lane per row writes without bank conflicts
+    static constexpr int part_ld = HD + 4;
+    static_assert(2 * kRows * part_ld * sizeof(float) <= stats, "partial gradients fit the tiles");
+    struct Shared {
+        uint64_t resident, full[slots], empty[slots], stat_full[2], stat_free[2];
+        uint64_t s_full, s_free, dp_full, dp_free, p_ready, ds_ready, done, scanned;
+        uint32_t tmem_base;
+        int abort_flag, again;
+    };
+    static constexpr uint32_t bytes = shared + sizeof(Shared);
+    static_assert(bytes <= 232448, "fits an SM");
 };
+// The tiles' swizzle needs 1024-byte alignment: true for the whole grid alike, and reported, where it does not hold.
+__device__ __forceinline__ bool misplaced(const void* sm, uint32_t* err) {
+    if ((smem_u32(sm) & 1023u) == 0) return false;
+    if (threadIdx.x == 0) atomicOr(err, kErrWaitTimeout);
+    return true;
+}
+// Barriers of either kernel; thread 0.
+template <int HD>
+__device__ __forceinline__ void bwd_init(typename BwdSmem<HD>::Shared& x) {
+    mbar_init(&x.resident, 1);
+    for (int s = 0; s < BwdSmem<HD>::slots; ++s) {
+        mbar_init(&x.full[s], 1);
+        mbar_init(&x.empty[s], 2);                           // the last product, the look for infinities
+    }
+    for (int s = 0; s < 2; ++s) {
+        mbar_init(&x.stat_full[s], 1);
+        mbar_init(&x.stat_free[s], 8);
+    }
+    mbar_init(&x.s_full, 1);
+    mbar_init(&x.s_free, 8);
+    mbar_init(&x.dp_full, 1);
+    mbar_init(&x.dp_free, 8);
+    mbar_init(&x.p_ready, 8);
+    mbar_init(&x.ds_ready, 8);
+    mbar_init(&x.done, 1);
+    mbar_init(&x.scanned, 1);
+    x.abort_flag = 0;
+    x.again = 0;
+    fence_mbar_init();
+}
+// Place n of the ring: its slot, and the parity of its use of that slot.
+template <int HD>
+struct Spot {
+    int slot;
+    uint32_t parity;
+    __device__ __forceinline__ explicit Spot(uint32_t n)
+        : slot((int)(n % BwdSmem<HD>::slots)), parity((n / BwdSmem<HD>::slots) & 1) {}
+};
+// TMA of the ring's places 0 .. count - 1 by one thread: load(place, destination, barrier).  After an abort no
+// copy may land once the block has gone.
+template <int HD, typename Load>
+__device__ __forceinline__ void feed_ring(uint8_t* ring, typename BwdSmem<HD>::Shared& x, uint32_t count, uint32_t* err,
+                                          Load load) {
+    using S = BwdSmem<HD>;
+    uint32_t n = 0;
+    for (; n < count; ++n) {
+        const Spot<HD> at(n);
+        if (n >= S::slots && !mbar_wait(&x.empty[at.slot], at.parity ^ 1, &x.abort_flag, err)) break;
+        mbar_arrive_expect_tx(&x.full[at.slot], S::tile);
+        load(n, ring + at.slot * S::tile, &x.full[at.slot]);
+    }
+    if (*(volatile int*)&x.abort_flag) {
+        mbar_wait_drain(&x.resident, 0);
+        for (uint32_t m = n > S::slots ? n - S::slots : 0; m < n; ++m) {
+            const Spot<HD> at(m);
+            mbar_wait_drain(&x.full[at.slot], at.parity);
+        }
+    }
+}
 
 // p (columns base .. base + 31 of a row) = 2^(s f - lse2), 0 outside columns from .. to where masked
 __device__ __forceinline__ void hide32z(float (&s)[32], int base, int from, int to) {
 #pragma unroll
     for (int e = 0; e < 32; ++e)
         if (base + e < from || base + e > to) s[e] = 0.f;
+}
+// What bf16 rounding leaves of 32 values.
+__device__ __forceinline__ void remainder32(float (&f)[32]) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        const uint32_t w = pack_bf16(f[e], f[e + 1]);
+        f[e] -= bf16_lo(w);
+        f[e + 1] -= bf16_hi(w);
+    }
 }
 __device__ __forceinline__ void store32(uint32_t to, const float (&f)[32]) {
     uint32_t w[16];
@@ -99,7 +199,9 @@ __device__ __noinline__ void dq_rows_again(const AttnTcArgs& a, int head, int32_
         const int32_t n = row0 + r;
         const float4 q = row4(a.q + (int64_t)n * a.qs + (int64_t)head * a.hd, lane, a.hd);
         const float4 d = row4(a.d_o + (int64_t)n * a.dos + (int64_t)head * a.hd, lane, a.hd);
-        const float ls = a.lse[(int64_t)head * a.N + n] * kLog2e, dl = a.delta[(int64_t)head * a.N + n];
+        const float ls = a.lse[(int64_t)head * a.N + n] * kLog2e;
+        const float dl = warp_dot(d, row4(a.o + (int64_t)n * a.os + (int64_t)head * a.hd, lane, a.hd));
+        if (lane == 0) a.delta[(int64_t)head * a.N + n] = dl;
         float4 dq = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int32_t j = seg_start32(n, a.cu, a.n_docs, a.seqlen); j <= n; ++j) {
             const float4 k = row4(a.k + (int64_t)j * a.ks + (int64_t)kv * a.hd, lane, a.hd);
@@ -120,76 +222,52 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                                                                   const __grid_constant__ CUtensorMap td,
                                                                   const AttnTcArgs a) {
     using S = BwdSmem<HD>;
-    extern __shared__ uint8_t raw[];
-    uint8_t* sm = align1024(raw);
+    extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t* sK = sm;
     uint8_t* sV = sm + S::tile;
-    uint8_t* sQ = sm + 2 * S::tile;                          // stage s: Q at sQ + 2 s tile, dO behind it
-    float* sStat = reinterpret_cast<float*>(sm + (2 + 2 * S::stages) * S::tile);
-    __shared__ uint64_t kv_full, full[S::stages], empty[S::stages], s_full, dp_full, p_ready, ds_ready, done, scanned;
-    __shared__ uint32_t tmem_base;
-    __shared__ int abort_flag, again;
+    uint8_t* ring = sm + S::ring;                            // place 2 i: Q of item i, 2 i + 1: its dO
+    float* stats = reinterpret_cast<float*>(sm + S::stats);
+    typename S::Shared& x = *reinterpret_cast<typename S::Shared*>(sm + S::shared);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kv = blockIdx.x % a.kvh;
-    const int32_t key0 = (int32_t)(blockIdx.x / a.kvh) * kRows;          // early keys have the most queries
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int kv = (int)(blockIdx.x / ranks) % a.kvh;
+    const int32_t key0 = (int32_t)(blockIdx.x / ranks / a.kvh) * kRows;  // early keys have the most queries
+    const int head0 = kv * a.group + rank * a.group / ranks;             // this block's heads
+    const int heads = kv * a.group + (rank + 1) * a.group / ranks - head0;
     int32_t s0, full_to, e_last;
     seg_bounds32(key0, a.cu, a.n_docs, a.seqlen, a.N, s0, full_to);      // queries below it see every key of the tile
     seg_bounds32(min(key0 + kRows, a.N) - 1, a.cu, a.n_docs, a.seqlen, a.N, s0, e_last);
     const int32_t t0 = key0 / kRows, per_head = (e_last - 1) / kRows - t0 + 1;
-    const int64_t items = (int64_t)per_head * a.group;
-    if (threadIdx.x == 0) {
-        mbar_init(&kv_full, 1);
-        for (int s = 0; s < S::stages; ++s) {
-            mbar_init(&full[s], 2);
-            mbar_init(&empty[s], 2);
-        }
-        mbar_init(&s_full, 1);
-        mbar_init(&dp_full, 1);
-        mbar_init(&p_ready, 8);
-        mbar_init(&ds_ready, 8);
-        mbar_init(&done, 1);
-        mbar_init(&scanned, 1);
-        abort_flag = 0;
-        again = 0;
-        fence_mbar_init();
-    }
+    const uint32_t items = (uint32_t)per_head * heads;
+    if (misplaced(sm, a.err)) return;
+    if (threadIdx.x == 0) bwd_init<HD>(x);
     if (warp == 8) {
-        tmem_alloc(&tmem_base, 512);
+        tmem_alloc(&x.tmem_base, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tb = tmem_base;
+    const uint32_t tb = x.tmem_base;
     constexpr uint32_t kDP = 128, kDV = 256, kDK = 256 + HD;
 
     if (warp == 9) {
         if (lane == 0) {
-            mbar_arrive_expect_tx(&kv_full, 2 * S::tile);
-            load_head_tile<HD>(sK, &tk, &kv_full, kv, key0);
-            load_head_tile<HD>(sV, &tv, &kv_full, kv, key0);
-            int64_t issued = 0;
+            mbar_arrive_expect_tx(&x.resident, 2 * S::tile);
+            load_head_tile<HD>(sK, &tk, &x.resident, kv, key0);
+            load_head_tile<HD>(sV, &tv, &x.resident, kv, key0);
             int32_t g = 0, t = 0;
-            for (; issued < items; ++issued) {
-                const int s = (int)(issued % S::stages);
-                const int64_t use = issued / S::stages;
-                if (use > 0 && !mbar_wait(&empty[s], (uint32_t)(use - 1) & 1, &abort_flag, a.err)) break;
-                mbar_arrive_expect_tx(&full[s], 2 * S::tile);
-                load_head_tile<HD>(sQ + 2 * s * S::tile, &tq, &full[s], kv * a.group + g, (t0 + t) * kRows);
-                load_head_tile<HD>(sQ + (2 * s + 1) * S::tile, &td, &full[s], kv * a.group + g, (t0 + t) * kRows);
-                if (++t == per_head) { t = 0; ++g; }
-            }
-            if (abort_flag) {
-                mbar_wait_drain(&kv_full, 0);
-                for (int s = 0; s < S::stages && s < issued; ++s)
-                    mbar_wait_drain(&full[s], (uint32_t)((issued - 1 - s) / S::stages) & 1);
-            }
+            feed_ring<HD>(ring, x, 2 * items, a.err, [&](uint32_t n, uint8_t* to, uint64_t* bar) {
+                load_head_tile<HD>(to, n & 1 ? &td : &tq, bar, head0 + g, (t0 + t) * kRows);
+                if ((n & 1) && ++t == per_head) { t = 0; ++g; }
+            });
         }
         __syncwarp();
     } else if (warp == 8) {
         constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
         constexpr uint32_t kIdG = idesc_bf16(128, HD, false, true);
-        const uint32_t k_at = smem_u32(sK), v_at = smem_u32(sV), q_at = smem_u32(sQ);
+        const uint32_t k_at = smem_u32(sK), v_at = smem_u32(sV), r_at = smem_u32(ring);
         const bool lead = elect_one();
         // D (128 columns at `to`) = A B^T of two K-major tiles
         auto nt = [&](uint32_t to, uint32_t A, uint32_t B, uint64_t* bar) {
@@ -210,75 +288,85 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                                  kIdG, add || c > 0);
             }
         };
-        bool ok = mbar_wait(&kv_full, 0, &abort_flag, a.err) && mbar_wait(&full[0], 0, &abort_flag, a.err);
-        tc_fence_after();
-        if (ok) {
-            nt(0, k_at, q_at, &s_full);
-            nt(kDP, v_at, q_at + S::tile, &dp_full);
-        }
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool got = mbar_wait(bar, parity, &x.abort_flag, a.err);
+            tc_fence_after();
+            return got;
+        };
+        bool ok = wait(&x.resident, 0) && wait(&x.full[0], 0);
+        if (ok) nt(0, k_at, r_at, &x.s_full);
+        ok = ok && wait(&x.full[1], 0);
+        if (ok) nt(kDP, v_at, r_at + S::tile, &x.dp_full);
         uint32_t phase = 0;
-        for (int64_t i = 0; ok && i < items; ++i, phase ^= 1) {
-            const uint32_t at = q_at + 2 * (uint32_t)(i % S::stages) * S::tile;
-            const int ns = (int)((i + 1) % S::stages);
-            const uint32_t next = q_at + 2 * ns * S::tile;
-            ok = mbar_wait(&p_ready, phase, &abort_flag, a.err);
-            tc_fence_after();
-            if (ok) grad(kDV, 0, at + S::tile, i > 0);
-            if (ok && i + 1 < items) {
-                ok = mbar_wait(&full[ns], (uint32_t)((i + 1) / S::stages) & 1, &abort_flag, a.err);
-                tc_fence_after();
-                if (ok) nt(0, k_at, next, &s_full);
-            }
-            ok = ok && mbar_wait(&ds_ready, phase, &abort_flag, a.err);
-            tc_fence_after();
+        int32_t t = 0;
+        for (uint32_t i = 0; ok && i < items; ++i, phase ^= 1) {
+            const Spot<HD> q(2 * i), d(2 * i + 1), q1(2 * i + 2), d1(2 * i + 3);
+            const bool more = i + 1 < items;
+            auto next_scores = [&]() {
+                ok = ok && wait(&x.full[q1.slot], q1.parity) && wait(&x.s_free, phase);
+                if (ok) nt(0, k_at, r_at + q1.slot * S::tile, &x.s_full);
+            };
+            if (more && t > 0) next_scores();
+            ok = ok && wait(&x.p_ready, phase);
             if (ok) {
-                grad(kDK, kDP, at, i > 0);
-                if (lead) umma_commit(&empty[i % S::stages]);
-                if (i + 1 < items) nt(kDP, v_at, next + S::tile, &dp_full);
+                grad(kDV, kDP, r_at + d.slot * S::tile, i > 0);
+                if (lead) umma_commit(&x.empty[d.slot]);
             }
+            ok = ok && wait(&x.ds_ready, phase);
+            if (ok) {
+                grad(kDK, kDP + 32, r_at + q.slot * S::tile, i > 0);
+                // the diagonal tile's remainders lie in the columns of S: the next scores come after them
+                if (t == 0) grad(kDK, 0, r_at + q.slot * S::tile, true);
+                if (lead) umma_commit(&x.empty[q.slot]);
+            }
+            if (more && t == 0) next_scores();
+            if (more) {
+                ok = ok && wait(&x.full[d1.slot], d1.parity);
+                if (ok) nt(kDP, v_at, r_at + d1.slot * S::tile, &x.dp_full);
+            }
+            if (++t == per_head) t = 0;
             __syncwarp();
         }
-        if (lead) umma_commit(&done);                        // every MMA done
-        mbar_wait_drain(&done, 0);
+        if (lead) umma_commit(&x.done);                      // every MMA done
+        mbar_wait_drain(&x.done, 0);
     } else if (warp == 10) {
         bool ok = true;
         int32_t t = 0;
-        for (int64_t i = 0; ok && i < items; ++i) {
-            const int s = (int)(i % S::stages);
-            ok = mbar_wait(&full[s], (uint32_t)(i / S::stages) & 1, &abort_flag, a.err);
+        for (uint32_t n = 0; ok && n < 2 * items; ++n) {
+            const Spot<HD> at(n);
+            ok = mbar_wait(&x.full[at.slot], at.parity, &x.abort_flag, a.err);
             if (!ok) break;
-            if (t == 0 || (t0 + t + 1) * kRows > full_to) {
-                if (tile_nonfinite(sQ + 2 * s * S::tile, 2 * S::tile, lane) && lane == 0) again = 1;
-            }
+            if ((t == 0 || (t0 + t + 1) * kRows > full_to) && tile_nonfinite(ring + at.slot * S::tile, S::tile, lane) &&
+                lane == 0)
+                x.again = 1;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
-            if (++t == per_head) t = 0;
+            if (lane == 0) mbar_arrive(&x.empty[at.slot]);
+            if ((n & 1) && ++t == per_head) t = 0;
         }
-        if (lane == 0) mbar_arrive(&scanned);
+        if (lane == 0) mbar_arrive(&x.scanned);
     } else if (warp == 11) {
-        // lse (log2 units, negated) and D of each stage's queries: read ahead, four per lane
+        // lse (log2 units, negated) and D of each item's queries: read ahead, four per lane
         int32_t g = 0, t = 0;
         float ls[4], dl[4];
         auto fetch = [&]() {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int32_t n = (t0 + t) * kRows + 4 * lane + e;
-                const int64_t at = (int64_t)(kv * a.group + g) * a.N + n;
+                const int64_t at = (int64_t)(head0 + g) * a.N + n;
                 ls[e] = n < a.N ? -a.lse[at] * kLog2e : 0.f;
                 dl[e] = n < a.N ? a.delta[at] : 0.f;
             }
             if (++t == per_head) { t = 0; ++g; }
         };
         fetch();
-        for (int64_t i = 0; i < items; ++i) {
-            const int s = (int)(i % S::stages);
-            const int64_t use = i / S::stages;
-            if (use > 0 && !mbar_wait(&empty[s], (uint32_t)(use - 1) & 1, &abort_flag, a.err)) break;
-            float4* st = reinterpret_cast<float4*>(sStat + s * 2 * kRows);
+        for (uint32_t i = 0; i < items; ++i) {
+            const int b = i & 1;
+            if (i >= 2 && !mbar_wait(&x.stat_free[b], ((i >> 1) - 1) & 1, &x.abort_flag, a.err)) break;
+            float4* st = reinterpret_cast<float4*>(stats + b * 2 * kRows);
             st[lane] = make_float4(ls[0], ls[1], ls[2], ls[3]);
             st[32 + lane] = make_float4(dl[0], dl[1], dl[2], dl[3]);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
+            if (lane == 0) mbar_arrive(&x.stat_full[b]);
             if (i + 1 < items) fetch();
         }
     } else {
@@ -291,20 +379,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         bool ok = true;
         uint32_t phase = 0;
         int32_t t = 0;
-        for (int64_t i = 0; i < items; ++i, phase ^= 1) {
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = mbar_wait(bar, parity, &x.abort_flag, a.err);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc_fence_after();
+            return ok;
+        };
+        auto signal = [&](uint64_t* bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        for (uint32_t i = 0; i < items; ++i, phase ^= 1) {
             const int32_t q0 = (t0 + t) * kRows;
             const bool masked = t == 0 || q0 + kRows > full_to;
             const int from = j - q0 - 64 * w, to = end - 1 - q0 - 64 * w;
-            const float* st = sStat + (i % S::stages) * 2 * kRows + 64 * w;
-            ok = mbar_wait(&full[i % S::stages], (uint32_t)(i / S::stages) & 1, &abort_flag, a.err) &&
-                 mbar_wait(&s_full, phase, &abort_flag, a.err);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            float p[2][32], f[32];
+            const float* st = stats + (i & 1) * 2 * kRows + 64 * w;
+            float p[2][32], f[2][32];
+            if (!wait(&x.s_full, phase)) break;
             tmem_ld32(at, p[0]);
             tmem_ld32(at + 32, p[1]);
             tmem_wait_ld();
+            signal(&x.s_free);
+            if (!wait(&x.stat_full[i & 1], (i >> 1) & 1)) break;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
 #pragma unroll
@@ -316,44 +413,53 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
 #pragma unroll
                 for (int e = 0; e < 32; ++e) p[b][e] = ex2(p[b][e]);
                 if (masked) hide32z(p[b], 32 * b, from, to);
-                store32(at + 16 * b, p[b]);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready);
-            ok = mbar_wait(&dp_full, phase, &abort_flag, a.err);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            float f2[32];
-            tmem_ld32(at + kDP, f);
-            tmem_ld32(at + kDP + 32, f2);
+            if (!wait(&x.dp_full, phase)) break;
+            tmem_ld32(at + kDP, f[0]);
+            tmem_ld32(at + kDP + 32, f[1]);
             tmem_wait_ld();
+            store32(at + kDP, p[0]);
+            store32(at + kDP + 16, p[1]);
+            tmem_wait_st();
+            signal(&x.p_ready);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                float(&x)[32] = b ? f2 : f;
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                     const float4 d = *reinterpret_cast<const float4*>(st + kRows + 32 * b + e);
-                    add2(x[e], x[e + 1], -d.x, -d.y);
-                    add2(x[e + 2], x[e + 3], -d.z, -d.w);
-                    mul2v(x[e], x[e + 1], p[b][e], p[b][e + 1]);
-                    mul2v(x[e + 2], x[e + 3], p[b][e + 2], p[b][e + 3]);
+                    add2(f[b][e], f[b][e + 1], -d.x, -d.y);
+                    add2(f[b][e + 2], f[b][e + 3], -d.z, -d.w);
+                    mul2v(f[b][e], f[b][e + 1], p[b][e], p[b][e + 1]);
+                    mul2v(f[b][e + 2], f[b][e + 3], p[b][e + 2], p[b][e + 3]);
                 }
-                if (masked) hide32z(x, 32 * b, from, to);
-                store32(at + kDP + 16 * b, x);
+                if (masked) hide32z(f[b], 32 * b, from, to);
+                store32(at + kDP + 32 + 16 * b, f[b]);
+                if (t == 0) {
+                    remainder32(f[b]);
+                    store32(at + 16 * b, f[b]);
+                }
             }
             tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ds_ready);
+            signal(&x.ds_ready);
+            if (lane == 0) mbar_arrive(&x.stat_free[i & 1]);
             if (++t == per_head) t = 0;
         }
-        ok = ok && mbar_wait(&done, 0, &abort_flag, a.err) && mbar_wait(&scanned, 0, &abort_flag, a.err);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        tc_fence_after();
-        if (ok && !again) {
+        ok = ok && wait(&x.done, 0) && wait(&x.scanned, 0);
+        if (!ok) x.again = -1;                               // nothing is written then
+        if (ranks > 1) {
+            // this block's part, for the cluster: warps 0-3 dv, warps 4-7 dk
+            float* row = reinterpret_cast<float*>(sm) + (size_t)(w * kRows + (warp & 3) * 32 + lane) * S::part_ld;
+            const uint32_t src = tb + ((uint32_t)((warp & 3) * 32) << 16) + (w ? kDK : kDV);
+#pragma unroll
+            for (int b = 0; b < HD / 32; ++b) {
+                float f[32];
+                tmem_ld32(src + 32 * b, f);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4*>(row + 32 * b + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            }
+        } else if (ok && !x.again) {
             // warps 0-3 write dv, warps 4-7 dk
             __nv_bfloat16* row = w ? a.dk + (int64_t)j * a.dks : a.dv + (int64_t)j * a.dvs;
             row += (int64_t)kv * a.hd;
@@ -377,6 +483,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         tc_fence_after();
         tmem_dealloc(tb, 512);
     }
+    if (ranks == 1) return;
+    // Every thread of every block comes here, whatever became of its waits, so the cluster's barriers end.
+    cluster.sync();
+    int bad = 0;
+    for (int r = 0; r < ranks; ++r) {
+        const int f = *cluster.map_shared_rank(&x.again, r);
+        bad = f < 0 || bad < 0 ? -1 : bad | f;
+    }
+    const int per = kRows / ranks, r0 = rank * per;          // the rows this block adds up
+    if (bad == 0) {
+        const float* part = reinterpret_cast<const float*>(sm);
+        for (int i = threadIdx.x; i < 2 * per * (HD / 8); i += kBwdThreads) {
+            const int c = i % (HD / 8) * 8, r = i / (HD / 8) % per, w = i / (HD / 8) / per;
+            const int32_t j = key0 + r0 + r;
+            float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+            for (int n = 0; n < ranks; ++n) {
+                const float4* p = reinterpret_cast<const float4*>(
+                    cluster.map_shared_rank(part, n) + (size_t)(w * kRows + r0 + r) * S::part_ld + c);
+                const float4 u = p[0], v = p[1];
+                lo.x += u.x; lo.y += u.y; lo.z += u.z; lo.w += u.w;
+                hi.x += v.x; hi.y += v.y; hi.z += v.z; hi.w += v.w;
+            }
+            if (j >= a.N || c >= a.hd) continue;
+            const float m = w ? a.scale : 1.f;
+            __nv_bfloat16* to = (w ? a.dk + (int64_t)j * a.dks : a.dv + (int64_t)j * a.dvs) + (int64_t)kv * a.hd + c;
+            *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(lo.x * m, lo.y * m), pack_bf16(lo.z * m, lo.w * m),
+                                                       pack_bf16(hi.x * m, hi.y * m), pack_bf16(hi.z * m, hi.w * m));
+        }
+    } else if (bad > 0 && warp < 8) {
+        const int32_t n = (per + 7) / 8, r = key0 + r0 + warp * n;
+        dkv_rows_again(a, kv, r, min(min(n, per - warp * n), a.N - r), lane);
+    }
+    cluster.sync();                                          // no block leaves while its part is read
 }
 
 // ---------------------------------------------------------------- dq
@@ -387,72 +526,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                                                                  const __grid_constant__ CUtensorMap td,
                                                                  const AttnTcArgs a) {
     using S = BwdSmem<HD>;
-    extern __shared__ uint8_t raw[];
-    uint8_t* sm = align1024(raw);
+    extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t* sQ = sm;
     uint8_t* sO = sm + S::tile;
-    uint8_t* sK = sm + 2 * S::tile;                          // stage s: K at sK + 2 s tile, V behind it
-    __shared__ uint64_t q_full, full[S::stages], empty[S::stages], s_full, dp_full, s_free, dp_free, ds_ready, done, scanned;
-    __shared__ uint32_t tmem_base;
-    __shared__ int abort_flag, again;
+    uint8_t* ring = sm + S::ring;                            // place 2 i: K of item i, 2 i + 1: its V
+    float* sD = reinterpret_cast<float*>(sm + S::stats);     // [128] D, then [2][128] its halves over the last item
+    float* sX = sD + kRows;
+    typename S::Shared& x = *reinterpret_cast<typename S::Shared*>(sm + S::shared);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.heads, kv = head / a.group;
     const int32_t tiles = (a.N + kRows - 1) / kRows;
     const int32_t row0 = (tiles - 1 - (int32_t)(blockIdx.x / a.heads)) * kRows;           // long rows first
     const int32_t lo = seg_start32(row0, a.cu, a.n_docs, a.seqlen) / kRows, hi = row0 / kRows;
     const int32_t full_from = seg_start32(min(row0 + kRows, a.N) - 1, a.cu, a.n_docs, a.seqlen);
-    const int32_t items = hi - lo + 1;
-    if (threadIdx.x == 0) {
-        mbar_init(&q_full, 1);
-        for (int s = 0; s < S::stages; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 2);
-        }
-        mbar_init(&s_full, 1);
-        mbar_init(&dp_full, 1);
-        mbar_init(&s_free, 8);
-        mbar_init(&dp_free, 8);
-        mbar_init(&ds_ready, 8);
-        mbar_init(&done, 1);
-        mbar_init(&scanned, 1);
-        abort_flag = 0;
-        again = 0;
-        fence_mbar_init();
-    }
+    const uint32_t items = (uint32_t)(hi - lo + 1);
+    if (misplaced(sm, a.err)) return;
+    if (threadIdx.x == 0) bwd_init<HD>(x);
     if (warp == 8) {
-        tmem_alloc(&tmem_base, 512);
+        tmem_alloc(&x.tmem_base, 512);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tb = tmem_base;
+    const uint32_t tb = x.tmem_base;
     constexpr uint32_t kDP = 128, kDQ = 256, kDS = 384;      // dS: two buffers of 64 columns
 
     if (warp == 9) {
         if (lane == 0) {
-            mbar_arrive_expect_tx(&q_full, 2 * S::tile);
-            load_head_tile<HD>(sQ, &tq, &q_full, head, row0);
-            load_head_tile<HD>(sO, &td, &q_full, head, row0);
-            int32_t issued = 0;
-            for (; issued < items; ++issued) {
-                const int s = issued % S::stages, use = issued / S::stages;
-                if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, &abort_flag, a.err)) break;
-                mbar_arrive_expect_tx(&full[s], 2 * S::tile);
-                load_head_tile<HD>(sK + 2 * s * S::tile, &tk, &full[s], kv, (lo + issued) * kRows);
-                load_head_tile<HD>(sK + (2 * s + 1) * S::tile, &tv, &full[s], kv, (lo + issued) * kRows);
-            }
-            if (abort_flag) {
-                mbar_wait_drain(&q_full, 0);
-                for (int s = 0; s < S::stages && s < issued; ++s)
-                    mbar_wait_drain(&full[s], ((issued - 1 - s) / S::stages) & 1);
-            }
+            mbar_arrive_expect_tx(&x.resident, 2 * S::tile);
+            load_head_tile<HD>(sQ, &tq, &x.resident, head, row0);
+            load_head_tile<HD>(sO, &td, &x.resident, head, row0);
+            feed_ring<HD>(ring, x, 2 * items, a.err, [&](uint32_t n, uint8_t* to, uint64_t* bar) {
+                load_head_tile<HD>(to, n & 1 ? &tv : &tk, bar, kv, (lo + (int32_t)(n >> 1)) * kRows);
+            });
         }
         __syncwarp();
     } else if (warp == 8) {
         constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
         constexpr uint32_t kIdG = idesc_bf16(128, HD, false, true);
-        const uint32_t q_at = smem_u32(sQ), o_at = smem_u32(sO), k_at = smem_u32(sK);
+        const uint32_t q_at = smem_u32(sQ), o_at = smem_u32(sO), r_at = smem_u32(ring);
         const bool lead = elect_one();
         auto nt = [&](uint32_t to, uint32_t A, uint32_t B, uint64_t* bar) {
             if (lead) {
@@ -463,78 +576,125 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 umma_commit(bar);
             }
         };
-        bool ok = mbar_wait(&q_full, 0, &abort_flag, a.err) && mbar_wait(&full[0], 0, &abort_flag, a.err);
-        tc_fence_after();
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool got = mbar_wait(bar, parity, &x.abort_flag, a.err);
+            tc_fence_after();
+            return got;
+        };
+        bool ok = wait(&x.resident, 0) && wait(&x.full[0], 0);
+        if (ok) nt(0, q_at, r_at, &x.s_full);
+        ok = ok && wait(&x.full[1], 0);
         if (ok) {
-            nt(0, q_at, k_at, &s_full);
-            nt(kDP, o_at, k_at + S::tile, &dp_full);
+            nt(kDP, o_at, r_at + S::tile, &x.dp_full);
+            if (lead) umma_commit(&x.empty[1]);
         }
         uint32_t phase = 0;
-        for (int32_t i = 0; ok && i < items; ++i, phase ^= 1) {
-            const uint32_t at = k_at + 2 * (i % S::stages) * S::tile;
-            const int ns = (i + 1) % S::stages;
-            const uint32_t next = k_at + 2 * ns * S::tile;
+        for (uint32_t i = 0; ok && i < items; ++i, phase ^= 1) {
+            const Spot<HD> k(2 * i), k1(2 * i + 2), v1(2 * i + 3);
             if (i + 1 < items) {
-                ok = mbar_wait(&full[ns], ((i + 1) / S::stages) & 1, &abort_flag, a.err) &&
-                     mbar_wait(&s_free, phase, &abort_flag, a.err);
-                tc_fence_after();
-                if (ok) nt(0, q_at, next, &s_full);
-                ok = ok && mbar_wait(&dp_free, phase, &abort_flag, a.err);
-                tc_fence_after();
-                if (ok) nt(kDP, o_at, next + S::tile, &dp_full);
+                ok = wait(&x.full[k1.slot], k1.parity) && wait(&x.s_free, phase);
+                if (ok) nt(0, q_at, r_at + k1.slot * S::tile, &x.s_full);
+                ok = ok && wait(&x.full[v1.slot], v1.parity) && wait(&x.dp_free, phase);
+                if (ok) {
+                    nt(kDP, o_at, r_at + v1.slot * S::tile, &x.dp_full);
+                    if (lead) umma_commit(&x.empty[v1.slot]);
+                }
             }
-            ok = ok && mbar_wait(&ds_ready, phase, &abort_flag, a.err);
-            tc_fence_after();
+            ok = ok && wait(&x.ds_ready, phase);
             if (ok && lead) {
+                const uint32_t at = r_at + k.slot * S::tile;
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     umma_ts_bf16(tb + kDQ, tb + kDS + 64 * (i & 1) + 8 * c, mnmajor_desc(at, kAtom, 16 * c), kIdG,
                                  i > 0 || c > 0);
-                umma_commit(&empty[i % S::stages]);
+                if (i == items - 1) {
+                    // the remainders of the diagonal tile, over the last scores
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        umma_ts_bf16(tb + kDQ, tb + (c < 4 ? 8 * c : 64 + 8 * (c - 4)), mnmajor_desc(at, kAtom, 16 * c), kIdG, 1);
+                }
+                umma_commit(&x.empty[k.slot]);
             }
             __syncwarp();
         }
-        if (lead) umma_commit(&done);
-        mbar_wait_drain(&done, 0);
+        if (lead) umma_commit(&x.done);
+        mbar_wait_drain(&x.done, 0);
     } else if (warp == 10) {
         bool ok = true;
-        for (int32_t i = 0; ok && i < items; ++i) {
-            const int s = i % S::stages;
-            ok = mbar_wait(&full[s], (i / S::stages) & 1, &abort_flag, a.err);
+        for (uint32_t n = 0; ok && n < 2 * items; ++n) {
+            const Spot<HD> at(n);
+            const uint32_t i = n >> 1;
+            ok = mbar_wait(&x.full[at.slot], at.parity, &x.abort_flag, a.err);
             if (!ok) break;
-            if (i == items - 1 || (lo + i) * kRows < full_from) {
-                if (tile_nonfinite(sK + 2 * s * S::tile, S::tile, lane) && lane == 0) again = 1;
-            }
+            if (!(n & 1) && (i == items - 1 || (lo + (int32_t)i) * kRows < full_from) &&
+                tile_nonfinite(ring + at.slot * S::tile, S::tile, lane) && lane == 0)
+                x.again = 1;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[s]);
+            if (lane == 0) mbar_arrive(&x.empty[at.slot]);
         }
-        if (lane == 0) mbar_arrive(&scanned);
+        if (lane == 0) mbar_arrive(&x.scanned);
     } else if (warp < 8) {
-        const int w = warp >> 2;
-        const int32_t n = row0 + (warp & 3) * 32 + lane;
+        const int w = warp >> 2, row = (warp & 3) * 32 + lane;
+        const int32_t n = row0 + row;
         const uint32_t at = tb + ((uint32_t)((warp & 3) * 32) << 16) + 64 * w;
         const uint32_t ds_at = tb + ((uint32_t)((warp & 3) * 32) << 16) + kDS + 32 * w;
         const float cs = a.scale * kLog2e;
+        {
+            // D = dO . O: half a warp per row, 16 rows per warp, all loads in flight together
+            uint4 u[8], v[8];
+            const int c = 8 * (lane & 15);
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                const int64_t m = row0 + 16 * warp + 2 * it + (lane >> 4);
+                const bool real = m < a.N && c < a.hd;
+                u[it] = v[it] = make_uint4(0, 0, 0, 0);
+                if (real) {
+                    u[it] = __ldg(reinterpret_cast<const uint4*>(a.o + m * a.os + (int64_t)head * a.hd + c));
+                    v[it] = __ldg(reinterpret_cast<const uint4*>(a.d_o + m * a.dos + (int64_t)head * a.hd + c));
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                float d = bf16_lo(u[it].x) * bf16_lo(v[it].x);
+                d = fmaf(bf16_hi(u[it].x), bf16_hi(v[it].x), d);
+                d = fmaf(bf16_lo(u[it].y), bf16_lo(v[it].y), d);
+                d = fmaf(bf16_hi(u[it].y), bf16_hi(v[it].y), d);
+                d = fmaf(bf16_lo(u[it].z), bf16_lo(v[it].z), d);
+                d = fmaf(bf16_hi(u[it].z), bf16_hi(v[it].z), d);
+                d = fmaf(bf16_lo(u[it].w), bf16_lo(v[it].w), d);
+                d = fmaf(bf16_hi(u[it].w), bf16_hi(v[it].w), d);
+#pragma unroll
+                for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
+                if ((lane & 15) == 0) sD[16 * warp + 2 * it + (lane >> 4)] = d;
+            }
+        }
         const int32_t start = n < a.N ? seg_start32(n, a.cu, a.n_docs, a.seqlen) : INT32_MAX;
         const float ls = n < a.N ? -a.lse[(int64_t)head * a.N + n] * kLog2e : 0.f;
-        const float dl = n < a.N ? -a.delta[(int64_t)head * a.N + n] : 0.f;
-        bool ok = true;
+        element_sync();
+        float dl = -sD[row];
+        bool ok = true, met = false;
         uint32_t phase = 0;
-        for (int32_t i = 0; i < items; ++i, phase ^= 1) {
-            const int32_t c0 = (lo + i) * kRows;
-            const bool masked = i == items - 1 || c0 < full_from;
-            const int from = start - c0 - 64 * w, to = n - c0 - 64 * w;
-            ok = mbar_wait(&s_full, phase, &abort_flag, a.err);
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = mbar_wait(bar, parity, &x.abort_flag, a.err);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
             tc_fence_after();
+            return ok;
+        };
+        auto signal = [&](uint64_t* bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        for (uint32_t i = 0; i < items; ++i, phase ^= 1) {
+            const int32_t c0 = (lo + (int32_t)i) * kRows;
+            const bool final = i == items - 1, masked = final || c0 < full_from;
+            const int from = start - c0 - 64 * w, to = n - c0 - 64 * w;
             float p[2][32], f[2][32];
+            if (!wait(&x.s_full, phase)) break;
             tmem_ld32(at, p[0]);
             tmem_ld32(at + 32, p[1]);
             tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_free);
+            signal(&x.s_free);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -543,16 +703,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                     p[b][e] = ex2(p[b][e]);
                     p[b][e + 1] = ex2(p[b][e + 1]);
                 }
-            ok = mbar_wait(&dp_full, phase, &abort_flag, a.err);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            tc_fence_after();
+            if (!wait(&x.dp_full, phase)) break;
             tmem_ld32(at + kDP, f[0]);
             tmem_ld32(at + kDP + 32, f[1]);
             tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&dp_free);
+            signal(&x.dp_free);
+            if (masked) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    hide32z(p[b], 32 * b, from, to);
+                    hide32z(f[b], 32 * b, from, to);
+                }
+            }
+            if (final) {
+                // D of the rows that see no other tile
+                float y = 0.f, z = 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    y = fmaf(p[0][e], f[0][e], y);
+                    z = fmaf(p[1][e], f[1][e], z);
+                }
+                sX[w * kRows + row] = y + z;
+                element_sync();
+                met = true;
+                if (start >= c0) dl = -(sX[row] + sX[kRows + row]);
+                if (w == 0 && n < a.N) a.delta[(int64_t)head * a.N + n] = -dl;
+            }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
 #pragma unroll
@@ -560,26 +736,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                     add2(f[b][e], f[b][e + 1], dl, dl);
                     mul2v(f[b][e], f[b][e + 1], p[b][e], p[b][e + 1]);
                 }
-                if (masked) hide32z(f[b], 32 * b, from, to);
                 store32(ds_at + 64 * (i & 1) + 16 * b, f[b]);
+                if (final) {
+                    remainder32(f[b]);
+                    store32(at + 16 * b, f[b]);
+                }
             }
             tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ds_ready);
+            signal(&x.ds_ready);
         }
-        ok = ok && mbar_wait(&done, 0, &abort_flag, a.err) && mbar_wait(&scanned, 0, &abort_flag, a.err);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        tc_fence_after();
-        if (ok && !again) {
-            __nv_bfloat16* row = a.dq + (int64_t)n * a.dqs + (int64_t)head * a.hd;
+        if (!met) element_sync();                            // after an abort: the other warps may wait there
+        ok = ok && wait(&x.done, 0) && wait(&x.scanned, 0);
+        if (ok && !x.again) {
+            __nv_bfloat16* to = a.dq + (int64_t)n * a.dqs + (int64_t)head * a.hd;
 #pragma unroll
             for (int b = 0; b < HD / 64; ++b) {              // each half of the warps writes half of the channels
                 const int c = 32 * (b + w * (HD / 64));
                 float f[32];
                 tmem_ld32(tb + ((uint32_t)((warp & 3) * 32) << 16) + kDQ + c, f);
                 tmem_wait_ld();
-                if (n < a.N) put32(row, c, a.hd, f, a.scale);
+                if (n < a.N) put32(to, c, a.hd, f, a.scale);
             }
         } else if (ok) {
             const int32_t r = row0 + warp * 16;
@@ -594,6 +770,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     }
 }
 
+// Blocks that share the heads of a group (a power of two up to 8).
+int dkv_ranks(const AttnProb& p, int64_t blocks) {
+    static const int force = getenv("DKV_R") ? atoi(getenv("DKV_R")) : 0;
+    int ranks = 1;
+    while (ranks * 2 <= std::min(p.group, 8) && (force ? ranks < force : blocks * ranks < 4 * num_sms())) ranks *= 2;
+    return ranks;
+}
+
 template <int HD>
 cudaError_t bwd_hd(const AttnProb& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    const CUtensorMap& td, const AttnTcArgs& a, cudaStream_t st) {
@@ -602,17 +786,29 @@ cudaError_t bwd_hd(const AttnProb& p, const CUtensorMap& tq, const CUtensorMap& 
     if (e == cudaSuccess) e = DC_SMEM_LIMIT(attn_dq_kernel<HD>, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kRows - 1) / kRows;
-    DC_LAUNCH(kAttnTcDkv, st, attn_dkv_kernel<HD><<<(unsigned)(tiles * p.kvh), kBwdThreads, smem, st>>>(tq, tk, tv, td, a));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<HD><<<(unsigned)(tiles * p.heads), kBwdThreads, smem, st>>>(tq, tk, tv, td, a));
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int ranks = dkv_ranks(p, tiles * p.kvh);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * p.kvh * ranks));
+    cfg.blockDim = dim3(kBwdThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ranks > 1 ? 1 : 0;
+    DC_LAUNCH(kAttnTcDkv, st, e = cudaLaunchKernelEx(&cfg, attn_dkv_kernel<HD>, tq, tk, tv, td, a));
+    return e;
 }
 
 }  // namespace
 }  // namespace attn_tc
 
 cudaError_t attn_tc_bwd(const AttnProb& p, const void* d_o, const void* q, const void* k, const void* v,
-                        const float* lse, const float* delta, void* dq, void* dk, void* dv, uint32_t* err,
+                        const void* o, const float* lse, float* delta, void* dq, void* dk, void* dv, uint32_t* err,
                         cudaStream_t st) {
     using namespace attn_tc;
     CUtensorMap tq, tk, tv, td;
@@ -624,6 +820,7 @@ cudaError_t attn_tc_bwd(const AttnProb& p, const void* d_o, const void* q, const
     a.k = static_cast<const __nv_bfloat16*>(k);
     a.v = static_cast<const __nv_bfloat16*>(v);
     a.d_o = static_cast<const __nv_bfloat16*>(d_o);
+    a.o = const_cast<__nv_bfloat16*>(static_cast<const __nv_bfloat16*>(o));
     a.dq = static_cast<__nv_bfloat16*>(dq);
     a.dk = static_cast<__nv_bfloat16*>(dk);
     a.dv = static_cast<__nv_bfloat16*>(dv);

@@ -102,6 +102,26 @@ def test_packed(lens, dtype, shape):
     _check(got, q, k, v, do, cu, heads, kv, hd)
 
 
+@pytest.mark.parametrize("heads,kv", [(8, 1), (5, 1), (6, 2), (12, 4)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_groups(dtype, heads, kv):
+    """Group sizes that are and are not powers of two: the sums of dk and dv over the heads of a group."""
+    lens = [1, 200, 77, 150]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    q, k, v, do = _inputs(428, heads, kv, 64, dtype, seed=11)
+    _check(_run(q, k, v, do, 1, 428, heads, kv, 64, cu=cu), q, k, v, do, cu, heads, kv, 64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_documents(dtype):
+    """Enough key tiles to fill the GPU without sharing out a group's heads."""
+    lens = [61 + 37 * i % 90 for i in range(180)]
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    N, heads, kv = int(cu[-1]), 8, 4
+    q, k, v, do = _inputs(N, heads, kv, 64, dtype, seed=12)
+    _check(_run(q, k, v, do, 1, N, heads, kv, 64, cu=cu), q, k, v, do, cu, heads, kv, 64)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_large_scores_and_a_given_scale(dtype):
     """Rows that one key dominates, scores up to some hundreds: the running maximum moves a lot."""
