@@ -39,6 +39,11 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
         ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
 // One tile of HD channels (HD / 64 atoms) of a head, 128 tokens from `row` on.
 template <int HD>
 __device__ __forceinline__ void load_head_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int head,
@@ -139,6 +144,40 @@ __device__ __forceinline__ void add2(float& x, float& y, float a0, float a1) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(a0), "f"(a1));
     asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+}
+
+// 32 columns of an accumulator, times `mul`, to channels base .. base + 31 of a row (hd of them are real)
+__device__ __forceinline__ void put32(__nv_bfloat16* row, int base, int hd, const float (&f)[32], float mul) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+        if (base + e < hd)
+            *reinterpret_cast<uint4*>(row + base + e) =
+                make_uint4(pack_bf16(f[e] * mul, f[e + 1] * mul), pack_bf16(f[e + 2] * mul, f[e + 3] * mul),
+                           pack_bf16(f[e + 4] * mul, f[e + 5] * mul), pack_bf16(f[e + 6] * mul, f[e + 7] * mul));
+}
+
+// ---------------------------------------------------------------- masks
+// Columns from .. to of a tile are seen by a row.  What a warp's rows see of columns base .. base + 31: in the
+// diagonal tile most such runs are seen by all of its rows or by none, and only the rest is masked one by one.
+enum { kSeeNone = 0, kSeeSome = 1, kSeeAll = 2 };
+__device__ __forceinline__ int seen_run(int base, int from, int to) {
+    if (__all_sync(0xFFFFFFFFu, from <= base && to >= base + 31)) return kSeeAll;
+    return __any_sync(0xFFFFFFFFu, from <= base + 31 && to >= base && from <= to) ? kSeeSome : kSeeNone;
+}
+// A bit per column of the run that the row sees.
+__device__ __forceinline__ uint32_t seen_bits(int base, int from, int to) {
+    const int lo = from - base, hi = to - base;
+    const uint32_t upto = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1;
+    return lo <= 0 ? upto : lo > 31 ? 0u : upto & (~0u << lo);
+}
+__device__ __forceinline__ void fill32(float (&s)[32], float x) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) s[e] = x;
+}
+// Columns a row does not see become `x`.
+__device__ __forceinline__ void hide32(float (&s)[32], uint32_t bits, float x) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) s[e] = bits >> e & 1 ? s[e] : x;
 }
 
 // ---------------------------------------------------------------- infinities and NaN

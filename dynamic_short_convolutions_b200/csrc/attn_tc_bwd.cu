@@ -154,16 +154,6 @@ __device__ __forceinline__ void store32(uint32_t to, const float (&f)[32]) {
     for (int e = 0; e < 16; ++e) w[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
     tmem_st16(to, w);
 }
-// 32 columns of an accumulator, times `mul`, to channels base .. base + 31 of a row (hd of them are real)
-__device__ __forceinline__ void put32(__nv_bfloat16* row, int base, int hd, const float (&f)[32], float mul) {
-#pragma unroll
-    for (int e = 0; e < 32; e += 8)
-        if (base + e < hd)
-            *reinterpret_cast<uint4*>(row + base + e) =
-                make_uint4(pack_bf16(f[e] * mul, f[e + 1] * mul), pack_bf16(f[e + 2] * mul, f[e + 3] * mul),
-                           pack_bf16(f[e + 4] * mul, f[e + 5] * mul), pack_bf16(f[e + 6] * mul, f[e + 7] * mul));
-}
-
 // dk and dv of `count` keys from key0 on (all below N), key by key over the queries that see it.
 __device__ __noinline__ void dkv_rows_again(const AttnTcArgs& a, int kv, int32_t key0, int count, int lane) {
     const float cs = a.scale * kLog2e;

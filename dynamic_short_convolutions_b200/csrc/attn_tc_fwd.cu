@@ -1,25 +1,27 @@
 // attn_tc_fwd.cu -- causal attention forward on the tensor cores (bf16 storage).
 //
-// A CTA takes 256 consecutive tokens of one query head as two tiles of 128 rows and walks the
-// 128-token tiles of keys and values from the first row's document start to the diagonal:
+// A CTA takes 128 consecutive tokens of one query head and walks the 128-token tiles of keys and values from
+// the first row's document start to the diagonal:
 //   S = Q K^T (tcgen05, fp32 in TMEM) -> softmax warps: one row per thread, running maximum and sum in
-//   fp32 -> P rounded to bf16, written over S in TMEM -> O += P V (tcgen05, A operand from TMEM).
+//   fp32 -> P rounded to bf16 in TMEM -> O += P V (tcgen05, A operand from TMEM).
 // P is rounded to bf16 because the tensor cores take it so; its sum is taken before the rounding.
 //
-// Warps: 0-3 softmax of tile 0, 4-7 of tile 1, 8 issues the MMAs, 9 the TMA loads, 10 looks at the
-// values of masked tiles.  The two tiles alternate: while one's softmax runs, the tensor cores work for
-// the other.  TMEM: S0, S1 128 columns each, O0, O1 HD columns each.  tcgen05.mma of one thread run in
-// issue order, so S(i+1) may be issued over P(i) right behind the product that reads it, and S(i+1)
-// complete means O holds every product up to i: the softmax thread may then rescale its row of O without
-// another barrier.  It does so only where the running maximum has grown by more than 2^8 (a stale maximum
-// cancels in the division by the sum and costs no precision below that), which after the first tiles is
+// Two CTAs share an SM (half of its TMEM and shared memory each): one's softmax runs while the tensor cores
+// work for the other, and so do its prologue and epilogue, which a CTA of 256 rows per SM left bare.
+// Warps: 0-3 softmax, 4 issues the MMAs, 5 the TMA loads; 6 warps at 168 registers are what fits twice.
+// TMEM (256 columns): S 128, O HD; P lies over S at HD = 128 and beside it at HD = 64, where the next
+// scores can then be computed as soon as this tile's are read.
+//
+// The softmax thread rescales its row of O only where the running maximum has grown by more than 2^8 (a stale
+// maximum cancels in the division by the sum and costs no precision below that), which after the first tiles is
 // rare.
 //
 // Tiles follow the packed token index, so documents need no list of work.  Masked scores are replaced by
-// -inf before the maximum.  P = 0 there, but 0 x NaN is NaN, so warp 10 looks for infinities and NaN among
-// the values of tiles that are masked for some row; where it finds one, the rows of that tile are computed
+// -inf before the maximum.  P = 0 there, but 0 x NaN is NaN, so the softmax warps look for infinities and NaN
+// among the values of tiles that are masked for some row; where they find one, the rows of the CTA are computed
 // again one by one over the tokens they see.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_tc.cuh"
 #include "prof.h"
@@ -29,14 +31,17 @@ namespace dynconv {
 namespace attn_tc {
 namespace {
 
-constexpr int kFwdThreads = 352;
+constexpr int kFwdThreads = 192;
+// The softmax warps' barrier.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 constexpr float kGrow = 8.f;                     // log2 growth of the maximum that makes a row rescale
 
 template <int HD>
 struct FwdSmem {
     static constexpr uint32_t tile = kAtom * (HD / 64);
-    static constexpr int slots = HD == 128 ? 4 : 6;
-    static constexpr uint32_t bytes = 1024 + tile * (2 + slots);
+    static constexpr int slots = HD == 128 ? 2 : 5;          // K and V tiles in turn
+    static constexpr uint32_t bytes = 1024 + tile * (1 + slots);
+    static_assert(2 * (bytes + 2048) <= 233472, "two blocks per SM");
 };
 
 // o and lse of rows row0 .. row0 + count - 1 (one warp's, all below N), over the tokens each sees, row by row.
@@ -67,12 +72,6 @@ __device__ __noinline__ void fwd_rows_again(const AttnTcArgs& a, int head, int32
     }
 }
 
-// -inf outside columns from .. to of a row; s holds columns base .. base + 31
-__device__ __forceinline__ void hide32(float (&s)[32], int base, int from, int to) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-        if (base + e < from || base + e > to) s[e] = -INFINITY;
-}
 __device__ __forceinline__ float max32(const float (&s)[32]) {
     float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
 #pragma unroll
@@ -96,217 +95,190 @@ __device__ __forceinline__ void probs32(float (&s)[32], float f, float g, float&
     tmem_st16(to, w);
 }
 
+__device__ __forceinline__ void zeros16(uint32_t to) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = 0;
+    tmem_st16(to, w);
+}
+
 template <int HD>
-__global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_constant__ CUtensorMap tq,
+__global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_constant__ CUtensorMap tq,
                                                                   const __grid_constant__ CUtensorMap tk,
                                                                   const __grid_constant__ CUtensorMap tv,
+                                                                  const __grid_constant__ CUtensorMap to,
                                                                   const AttnTcArgs a) {
     using S = FwdSmem<HD>;
+    constexpr bool kBeside = HD == 64;                       // P beside S
+    constexpr uint32_t kP = kBeside ? 128 : 0, kO = kBeside ? 192 : 128;
     extern __shared__ uint8_t raw[];
-    uint8_t* sm = align1024(raw);
-    uint8_t* sQ = sm;
-    uint8_t* sKV = sm + 2 * S::tile;
-    __shared__ uint64_t q_full, kv_full[S::slots], kv_empty[S::slots], s_full[2], p_ready[2], o_full[2], scanned, drained;
+    uint8_t* sQ = align1024(raw);
+    uint8_t* ring = sQ + S::tile;                            // place 2 i: K of tile i, 2 i + 1: its V
+    __shared__ uint64_t q_full, full[S::slots], empty[S::slots], s_full, s_free, p_ready, pv_done, drained;
     __shared__ uint32_t tmem_base;
-    __shared__ int abort_flag, again[2];
+    __shared__ int abort_flag, again;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.heads, kv = head / a.group;
-    const int32_t blocks = (a.N + 2 * kRows - 1) / (2 * kRows);
-    const int32_t row0 = (blocks - 1 - (int32_t)(blockIdx.x / a.heads)) * 2 * kRows;      // long rows first
-    // tiles of keys that each row tile walks, lo[t] .. hi[t] (none: lo > hi), and the first key that every row sees
-    int32_t lo[2], hi[2], full_from[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int32_t r = row0 + t * kRows;
-        lo[t] = 0; hi[t] = -1; full_from[t] = 0;
-        if (r < a.N) {
-            lo[t] = seg_start32(r, a.cu, a.n_docs, a.seqlen) / kRows;
-            hi[t] = r / kRows;
-            full_from[t] = seg_start32(min(r + kRows, a.N) - 1, a.cu, a.n_docs, a.seqlen);
-        }
-    }
-    const int32_t first = lo[0], last = max(hi[0], hi[1]);
+    const int32_t tiles = (a.N + kRows - 1) / kRows;
+    const int32_t row0 = (tiles - 1 - (int32_t)(blockIdx.x / a.heads)) * kRows;           // long rows first
     if (threadIdx.x == 0) {
         mbar_init(&q_full, 1);
         for (int s = 0; s < S::slots; ++s) {
-            mbar_init(&kv_full[s], 1);
-            mbar_init(&kv_empty[s], 2);
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
         }
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&s_full[t], 1);
-            mbar_init(&p_ready[t], 4);
-            mbar_init(&o_full[t], 1);
-            again[t] = 0;
-        }
-        mbar_init(&scanned, 1);
+        mbar_init(&s_full, 1);
+        mbar_init(&s_free, 4);
+        mbar_init(&p_ready, 4);
+        mbar_init(&pv_done, 1);
         mbar_init(&drained, 1);
         abort_flag = 0;
+        again = 0;
         fence_mbar_init();
     }
-    if (warp == 8) {
-        tmem_alloc(&tmem_base, 512);
+    if (warp == 4) {
+        tmem_alloc(&tmem_base, 256);
         tmem_relinquish();
     }
+    const int32_t lo = seg_start32(row0, a.cu, a.n_docs, a.seqlen) / kRows;
+    const int32_t items = row0 / kRows - lo + 1;             // tiles of keys
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = tmem_base;
 
-    if (warp == 9) {
-        // ---- TMA: Q once, then K(i), V(i) in turn through the ring
+    if (warp == 5) {
         if (lane == 0) {
-            tma_prefetch(&tk);
-            tma_prefetch(&tv);
-            mbar_arrive_expect_tx(&q_full, 2 * S::tile);
+            mbar_arrive_expect_tx(&q_full, S::tile);
             load_head_tile<HD>(sQ, &tq, &q_full, head, row0);
-            load_head_tile<HD>(sQ + S::tile, &tq, &q_full, head, row0 + kRows);
-            int issued = 0;
-            for (int32_t i = first; i <= last; ++i) {
-                bool ok = true;
-#pragma unroll
-                for (int w = 0; w < 2 && ok; ++w, ++issued) {
-                    const int s = issued % S::slots, use = issued / S::slots;
-                    if (use > 0 && !mbar_wait(&kv_empty[s], (use - 1) & 1, &abort_flag, a.err)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(&kv_full[s], S::tile);
-                    load_head_tile<HD>(sKV + s * S::tile, w ? &tv : &tk, &kv_full[s], kv, i * kRows);
-                }
-                if (!ok) break;
+            int n = 0;
+            for (; n < 2 * items; ++n) {
+                const int s = n % S::slots, use = n / S::slots;
+                if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, &abort_flag, a.err)) break;
+                mbar_arrive_expect_tx(&full[s], S::tile);
+                load_head_tile<HD>(ring + s * S::tile, n & 1 ? &tv : &tk, &full[s], kv, (lo + (n >> 1)) * kRows);
             }
-            if (abort_flag) {       // no copy may land after the CTA has gone
+            if (*(volatile int*)&abort_flag) {               // no copy may land after the CTA has gone
                 mbar_wait_drain(&q_full, 0);
-                for (int s = 0; s < S::slots && s < issued; ++s)
-                    mbar_wait_drain(&kv_full[s], ((issued - 1 - s) / S::slots) & 1);
+                for (int m = n > S::slots ? n - S::slots : 0; m < n; ++m)
+                    mbar_wait_drain(&full[m % S::slots], (m / S::slots) & 1);
             }
         }
         __syncwarp();
-    } else if (warp == 8) {
-        // ---- MMA
+    } else if (warp == 4) {
         constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
         constexpr uint32_t kIdO = idesc_bf16(128, HD, false, true);
-        const uint32_t q_at = smem_u32(sQ), kv_at = smem_u32(sKV);
+        const uint32_t q_at = smem_u32(sQ), r_at = smem_u32(ring);
         const bool lead = elect_one();
-        auto scores = [&](int t, int slot) {
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool got = mbar_wait(bar, parity, &abort_flag, a.err);
+            tc_fence_after();
+            return got;
+        };
+        auto scores = [&](int n) {                           // of the keys at place n
+            const int s = n % S::slots;
+            if (!wait(&full[s], (n / S::slots) & 1)) return false;
             if (lead) {
 #pragma unroll
                 for (int c = 0; c < HD / 16; ++c)
-                    umma_bf16(tb + 128 * t, kmajor_desc(q_at + t * S::tile + (c / 4) * kAtom, c % 4),
-                              kmajor_desc(kv_at + slot * S::tile + (c / 4) * kAtom, c % 4), kIdS, c != 0);
-                umma_commit(&s_full[t]);
+                    umma_bf16(tb, kmajor_desc(q_at + (c / 4) * kAtom, c % 4),
+                              kmajor_desc(r_at + s * S::tile + (c / 4) * kAtom, c % 4), kIdS, c != 0);
+                umma_commit(&s_full);
+                umma_commit(&empty[s]);
             }
+            return true;
         };
-        bool ok = mbar_wait(&q_full, 0, &abort_flag, a.err) && mbar_wait(&kv_full[0], 0, &abort_flag, a.err);
-        tc_fence_after();
-        if (ok) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (lo[t] <= first && first <= hi[t]) scores(t, 0);
-            if (lead) umma_commit(&kv_empty[0]);
-        }
-        int at = 1;                                          // ring place of V(i)
-        uint32_t phase[2] = {0, 0};
-        for (int32_t i = first; ok && i <= last; ++i, at += 2) {
-            const int vs = at % S::slots, ks = (at + 1) % S::slots;
-            ok = mbar_wait(&kv_full[vs], (at / S::slots) & 1, &abort_flag, a.err);
-            if (ok && i < last) ok = mbar_wait(&kv_full[ks], ((at + 1) / S::slots) & 1, &abort_flag, a.err);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (ok && lo[t] <= i && i <= hi[t]) {
-                    ok = mbar_wait(&p_ready[t], phase[t], &abort_flag, a.err);
-                    phase[t] ^= 1;
-                    tc_fence_after();
-                    if (ok && lead) {
-#pragma unroll
-                        for (int c = 0; c < 8; ++c)
-                            umma_ts_bf16(tb + 256 + HD * t, tb + 128 * t + 8 * c,
-                                         mnmajor_desc(kv_at + vs * S::tile, kAtom, 16 * c), kIdO, i > lo[t] || c > 0);
-                        if (i == hi[t]) umma_commit(&o_full[t]);
-                    }
-                }
-                if (ok && lo[t] <= i + 1 && i + 1 <= hi[t]) scores(t, ks);
-            }
+        bool ok = wait(&q_full, 0) && scores(0);
+        uint32_t phase = 0;
+        for (int32_t i = 0; ok && i < items; ++i, phase ^= 1) {
+            const int s = (2 * i + 1) % S::slots;
+            if (kBeside && i + 1 < items) ok = wait(&s_free, phase) && scores(2 * i + 2);
+            ok = ok && wait(&full[s], ((2 * i + 1) / S::slots) & 1) && wait(&p_ready, phase);
             if (ok && lead) {
-                umma_commit(&kv_empty[vs]);
-                if (i < last) umma_commit(&kv_empty[ks]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    umma_ts_bf16(tb + kO, tb + kP + 8 * c, mnmajor_desc(r_at + s * S::tile, kAtom, 16 * c), kIdO,
+                                 i > 0 || c > 0);
+                umma_commit(&pv_done);
+                umma_commit(&empty[s]);
             }
+            // P over S: these come behind the product that reads P
+            if (!kBeside && ok && i + 1 < items) ok = scores(2 * i + 2);
             __syncwarp();
         }
         if (lead) umma_commit(&drained);                     // every MMA done before TMEM is freed
         mbar_wait_drain(&drained, 0);
-    } else if (warp == 10) {
-        // ---- values of masked tiles: infinities and NaN
-        int at = 0;
-        bool ok = true;
-        for (int32_t i = first; ok && i <= last; ++i) {
-            for (int w = 0; w < 2 && ok; ++w, ++at) {
-                const int s = at % S::slots;
-                ok = mbar_wait(&kv_full[s], (at / S::slots) & 1, &abort_flag, a.err);
-                if (!ok) break;
-                if (w == 1) {
-                    bool masked[2];
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        masked[t] = lo[t] <= i && i <= hi[t] && (i == hi[t] || i * kRows < full_from[t]);
-                    if ((masked[0] || masked[1]) && tile_nonfinite(sKV + s * S::tile, S::tile, lane) && lane == 0) {
-                        if (masked[0]) again[0] = 1;
-                        if (masked[1]) again[1] = 1;
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&kv_empty[s]);
-            }
-        }
-        if (lane == 0) mbar_arrive(&scanned);
     } else {
         // ---- softmax: one row per thread
-        const int t = warp >> 2;
-        const int32_t tile0 = row0 + t * kRows, n = tile0 + (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tb + lanes + 128 * t, tO = tb + lanes + 256 + HD * t;
+        const int32_t n = row0 + warp * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const uint32_t tS = tb + lanes, tP = tS + kP, tO = tS + kO;
         const float cs = a.scale * kLog2e;
+        const int32_t full_from = seg_start32(min(row0 + kRows, a.N) - 1, a.cu, a.n_docs, a.seqlen);
         const int32_t start = n < a.N ? seg_start32(n, a.cu, a.n_docs, a.seqlen) : INT32_MAX;
         float m = -INFINITY, l0 = 0.f, l1 = 0.f;             // running maximum (log2 units), halves of the sum
         bool ok = true;
         uint32_t phase = 0;
-        for (int32_t i = lo[t]; i <= hi[t]; ++i) {
-            ok = mbar_wait(&s_full[t], phase, &abort_flag, a.err);
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = mbar_wait(bar, parity, &abort_flag, a.err);
             ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            phase ^= 1;
             tc_fence_after();
+            return ok;
+        };
+        auto signal = [&](uint64_t* bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        auto look = [&](int32_t i) {
+            const int v = 2 * i + 1;
+            if (!wait(&full[v % S::slots], (v / S::slots) & 1)) return false;
+            constexpr uint32_t part = S::tile / 4;
+            if (tile_nonfinite(ring + (v % S::slots) * S::tile + warp * part, part, lane) && lane == 0) again = 1;
+            return true;
+        };
+        // One tile; two copies of the code, so that the tiles every row sees whole pay nothing for masks.
+        auto tile = [&](auto with_mask, int32_t i) {
+            constexpr bool kMask = decltype(with_mask)::value;
+            const int32_t c0 = (lo + i) * kRows;
+            const int from = start - c0, to_col = n - c0;
+            if (!wait(&s_full, phase)) return false;
             // Maximum over columns 64-127, then 0-63; the latter stay in registers, the former are read again
             // below (a row of 128 scores next to its probabilities does not fit the registers).
-            const bool masked = i == hi[t] || i * kRows < full_from[t];
-            const int from = start - i * kRows, to = n - i * kRows;
             float s0[32], s1[32], mx[4];
+            int see[4] = {kSeeAll, kSeeAll, kSeeAll, kSeeAll};
+            if (kMask) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) see[b] = seen_run(32 * b, from, to_col);
+            }
+            auto mask = [&](float (&s)[32], int b) {
+                if (!kMask) return;
+                if (see[b] == kSeeSome) hide32(s, seen_bits(32 * b, from, to_col), -INFINITY);
+                else if (see[b] == kSeeNone) fill32(s, -INFINITY);
+            };
             tmem_ld32(tS + 64, s0);
             tmem_ld32(tS + 96, s1);
             tmem_wait_ld();
-            if (masked) {
-                hide32(s0, 64, from, to);
-                hide32(s1, 96, from, to);
-            }
+            mask(s0, 2);
+            mask(s1, 3);
             mx[0] = max32(s0);
             mx[1] = max32(s1);
             tmem_ld32(tS, s0);
             tmem_ld32(tS + 32, s1);
             tmem_wait_ld();
-            if (masked) {
-                hide32(s0, 0, from, to);
-                hide32(s1, 32, from, to);
-            }
+            mask(s0, 0);
+            mask(s1, 1);
             mx[2] = max32(s0);
             mx[3] = max32(s1);
             const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs);
+            // The last product is done where P lies over S, since these scores came behind it
+            if (kBeside && i > 0 && !wait(&pv_done, phase ^ 1)) return false;
             if (__any_sync(0xFFFFFFFFu, top - m > kGrow)) {
-                if (i > lo[t]) {
-                    // O is complete up to the previous tile: rescale this row of it
+                if (i > 0) {
                     const float c = top == -INFINITY ? 1.f : ex2(m - top);
                     l0 *= c;
                     l1 *= c;
-#pragma unroll
+#pragma unroll 1
                     for (int b = 0; b < HD / 32; ++b) {
                         float f[32];
                         tmem_ld32(tO + 32 * b, f);
@@ -319,68 +291,80 @@ __global__ void __launch_bounds__(kFwdThreads, 1) attn_fwd_kernel(const __grid_c
                 m = top;
             }
             const float neg = m == -INFINITY ? 0.f : -m;     // a row that has seen no key yet
-            probs32(s0, cs, neg, l0, l1, tS);
+            auto probs = [&](float (&s)[32], int b) {
+                if (kMask && see[b] == kSeeNone) zeros16(tP + 16 * b);
+                else probs32(s, cs, neg, l0, l1, tP + 16 * b);
+            };
+            probs(s0, 0);
             tmem_ld32(tS + 64, s0);
-            probs32(s1, cs, neg, l0, l1, tS + 16);
+            probs(s1, 1);
             tmem_ld32(tS + 96, s1);
             tmem_wait_ld();
-            if (masked) {
-                hide32(s0, 64, from, to);
-                hide32(s1, 96, from, to);
-            }
-            probs32(s0, cs, neg, l0, l1, tS + 32);
-            probs32(s1, cs, neg, l0, l1, tS + 48);
+            if (kBeside) signal(&s_free);
+            mask(s0, 2);
+            mask(s1, 3);
+            probs(s0, 2);
+            probs(s1, 3);
             tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[t]);
+            // Infinities and NaN among the values: before the product that gives the tile back waits for P, or
+            // behind it where no tile follows.
+            const bool final = i == items - 1;
+            if (kMask && !final && !look(i)) return false;
+            signal(&p_ready);
+            return !(kMask && final) || look(i);
+        };
+        for (int32_t i = 0; i < items; ++i, phase ^= 1) {
+            const bool masked = i == items - 1 || (lo + i) * kRows < full_from;
+            if (!(masked ? tile(std::true_type{}, i) : tile(std::false_type{}, i))) break;
         }
-        if (lo[t] <= hi[t]) {
-            ok = ok && mbar_wait(&o_full[t], 0, &abort_flag, a.err);
-            ok = ok && mbar_wait(&scanned, 0, &abort_flag, a.err);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            tc_fence_after();
-            const float l = l0 + l1;
-            const float inv = l > 0.f ? 1.f / l : l;
-            if (ok && !again[t]) {
-                __nv_bfloat16* row = a.o + (int64_t)n * a.os + (int64_t)head * a.hd;
+        ok = ok && wait(&pv_done, (items - 1) & 1);
+        ok = !named_bar_any<1, 128>(!ok);                    // every warp has looked; all go on, or none
+        const float l = l0 + l1;
+        const float inv = l > 0.f ? 1.f / l : l;
+        if (ok && !again) {
+            // O through Q's tile and TMA: rows from N on and channels from hd on are not written
 #pragma unroll
-                for (int b = 0; b < HD / 32; ++b) {
-                    float f[32];
-                    tmem_ld32(tO + 32 * b, f);
-                    tmem_wait_ld();
-                    if (n < a.N) {
+            for (int b = 0; b < HD / 32; ++b) {
+                float f[32];
+                tmem_ld32(tO + 32 * b, f);
+                tmem_wait_ld();
+                const uint32_t r = warp * 32 + lane;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            if (32 * b + e < a.hd)
-                                *reinterpret_cast<uint4*>(row + 32 * b + e) =
-                                    make_uint4(pack_bf16(f[e] * inv, f[e + 1] * inv), pack_bf16(f[e + 2] * inv, f[e + 3] * inv),
-                                               pack_bf16(f[e + 4] * inv, f[e + 5] * inv), pack_bf16(f[e + 6] * inv, f[e + 7] * inv));
-                    }
-                }
-                if (a.lse != nullptr && n < a.N) a.lse[(int64_t)head * a.N + n] = (m + __log2f(l)) * kLn2;
-            } else if (ok) {
-                const int32_t r = tile0 + (warp & 3) * 32;
-                fwd_rows_again(a, head, r, min(32, a.N - r), lane);
+                for (int e = 0; e < 32; e += 8)
+                    *reinterpret_cast<uint4*>(sQ + (b / 2) * kAtom + sw128_off(r, (b % 2) * 4 + e / 8)) =
+                        make_uint4(pack_bf16(f[e] * inv, f[e + 1] * inv), pack_bf16(f[e + 2] * inv, f[e + 3] * inv),
+                                   pack_bf16(f[e + 4] * inv, f[e + 5] * inv), pack_bf16(f[e + 6] * inv, f[e + 7] * inv));
             }
+            fence_async_smem();
+            softmax_sync();
+            if (threadIdx.x == 0) {
+#pragma unroll
+                for (int c = 0; c < HD / 64; ++c) tma_store_3d(&to, sQ + c * kAtom, 64 * c, head, row0);
+                tma_store_commit();
+            }
+            if (a.lse != nullptr && n < a.N) a.lse[(int64_t)head * a.N + n] = (m + __log2f(l)) * kLn2;
+        } else if (ok) {
+            const int32_t r = row0 + warp * 32;
+            fwd_rows_again(a, head, r, min(32, a.N - r), lane);
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == 4) {
         tc_fence_after();
-        tmem_dealloc(tb, 512);
+        tmem_dealloc(tb, 256);
     }
+    if (threadIdx.x == 0) tma_store_wait_all();              // O has left shared memory
 }
 
 template <int HD>
 cudaError_t fwd_hd(const AttnProb& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const AttnTcArgs& a, cudaStream_t st) {
+                   const CUtensorMap& to, const AttnTcArgs& a, cudaStream_t st) {
     constexpr uint32_t smem = FwdSmem<HD>::bytes;
     cudaError_t e = DC_SMEM_LIMIT(attn_fwd_kernel<HD>, smem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((p.N + 2 * kRows - 1) / (2 * kRows) * p.heads);
-    DC_LAUNCH(kAttnTcFwd, st, attn_fwd_kernel<HD><<<grid, kFwdThreads, smem, st>>>(tq, tk, tv, a));
+    const unsigned grid = (unsigned)((p.N + kRows - 1) / kRows * p.heads);
+    DC_LAUNCH(kAttnTcFwd, st, attn_fwd_kernel<HD><<<grid, kFwdThreads, smem, st>>>(tq, tk, tv, to, a));
     return cudaGetLastError();
 }
 
@@ -398,9 +382,9 @@ const char* attn_tc_refusal(const AttnProb& p) {
 cudaError_t attn_tc_fwd(const AttnProb& p, const void* q, const void* k, const void* v, void* o, float* lse,
                         uint32_t* err, cudaStream_t st) {
     using namespace attn_tc;
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, to;
     if (!make_head_map(&tq, q, p.N, p.heads, p.hd, p.qs) || !make_head_map(&tk, k, p.N, p.kvh, p.hd, p.ks) ||
-        !make_head_map(&tv, v, p.N, p.kvh, p.hd, p.vs))
+        !make_head_map(&tv, v, p.N, p.kvh, p.hd, p.vs) || !make_head_map(&to, o, p.N, p.heads, p.hd, p.os))
         return cudaErrorInvalidValue;
     AttnTcArgs a = tc_args(p);
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -409,7 +393,7 @@ cudaError_t attn_tc_fwd(const AttnProb& p, const void* q, const void* k, const v
     a.o = static_cast<__nv_bfloat16*>(o);
     a.lse = lse;
     a.err = err;
-    return p.hd <= 64 ? fwd_hd<64>(p, tq, tk, tv, a, st) : fwd_hd<128>(p, tq, tk, tv, a, st);
+    return p.hd <= 64 ? fwd_hd<64>(p, tq, tk, tv, to, a, st) : fwd_hd<128>(p, tq, tk, tv, to, a, st);
 }
 
 }  // namespace dynconv
