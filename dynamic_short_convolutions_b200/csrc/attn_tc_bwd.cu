@@ -38,6 +38,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_tc.cuh"
 #include "prof.h"
@@ -133,12 +134,6 @@ __device__ __forceinline__ void feed_ring(uint8_t* ring, typename BwdSmem<HD>::S
     }
 }
 
-// p (columns base .. base + 31 of a row) = 2^(s f - lse2), 0 outside columns from .. to where masked
-__device__ __forceinline__ void hide32z(float (&s)[32], int base, int from, int to) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e)
-        if (base + e < from || base + e > to) s[e] = 0.f;
-}
 // What bf16 rounding leaves of 32 values.
 __device__ __forceinline__ void remainder32(float (&f)[32]) {
 #pragma unroll
@@ -380,20 +375,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        for (uint32_t i = 0; i < items; ++i, phase ^= 1) {
+        // One item; two copies of the code, so that the tiles every key is seen by whole pay nothing for masks.
+        auto item = [&](auto with_mask, uint32_t i) {
+            constexpr bool kMask = decltype(with_mask)::value;
             const int32_t q0 = (t0 + t) * kRows;
-            const bool masked = t == 0 || q0 + kRows > full_to;
             const int from = j - q0 - 64 * w, to = end - 1 - q0 - 64 * w;
             const float* st = stats + (i & 1) * 2 * kRows + 64 * w;
+            int see[2] = {kSeeAll, kSeeAll};
+            uint32_t bits[2] = {~0u, ~0u};
+            if (kMask) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    see[b] = seen_run(32 * b, from, to);
+                    bits[b] = seen_bits(32 * b, from, to);
+                }
+            }
             float p[2][32], f[2][32];
-            if (!wait(&x.s_full, phase)) break;
+            if (!wait(&x.s_full, phase)) return false;
             tmem_ld32(at, p[0]);
             tmem_ld32(at + 32, p[1]);
             tmem_wait_ld();
             signal(&x.s_free);
-            if (!wait(&x.stat_full[i & 1], (i >> 1) & 1)) break;
+            if (!wait(&x.stat_full[i & 1], (i >> 1) & 1)) return false;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
+                if (kMask && see[b] == kSeeNone) {
+                    fill32(p[b], 0.f);
+                    continue;
+                }
 #pragma unroll
                 for (int e = 0; e < 32; e += 4) {
                     const float4 l = *reinterpret_cast<const float4*>(st + 32 * b + e);
@@ -402,9 +411,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 }
 #pragma unroll
                 for (int e = 0; e < 32; ++e) p[b][e] = ex2(p[b][e]);
-                if (masked) hide32z(p[b], 32 * b, from, to);
+                if (kMask && see[b] == kSeeSome) hide32(p[b], bits[b], 0.f);
             }
-            if (!wait(&x.dp_full, phase)) break;
+            if (!wait(&x.dp_full, phase)) return false;
             tmem_ld32(at + kDP, f[0]);
             tmem_ld32(at + kDP + 32, f[1]);
             tmem_wait_ld();
@@ -414,17 +423,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             signal(&x.p_ready);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
+                if (kMask && see[b] == kSeeNone) {
+                    fill32(f[b], 0.f);
+                } else {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 d = *reinterpret_cast<const float4*>(st + kRows + 32 * b + e);
-                    add2(f[b][e], f[b][e + 1], -d.x, -d.y);
-                    add2(f[b][e + 2], f[b][e + 3], -d.z, -d.w);
-                    mul2v(f[b][e], f[b][e + 1], p[b][e], p[b][e + 1]);
-                    mul2v(f[b][e + 2], f[b][e + 3], p[b][e + 2], p[b][e + 3]);
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 d = *reinterpret_cast<const float4*>(st + kRows + 32 * b + e);
+                        add2(f[b][e], f[b][e + 1], -d.x, -d.y);
+                        add2(f[b][e + 2], f[b][e + 3], -d.z, -d.w);
+                        mul2v(f[b][e], f[b][e + 1], p[b][e], p[b][e + 1]);
+                        mul2v(f[b][e + 2], f[b][e + 3], p[b][e + 2], p[b][e + 3]);
+                    }
+                    if (kMask && see[b] == kSeeSome) hide32(f[b], bits[b], 0.f);
                 }
-                if (masked) hide32z(f[b], 32 * b, from, to);
                 store32(at + kDP + 32 + 16 * b, f[b]);
-                if (t == 0) {
+                if (kMask && t == 0) {
                     remainder32(f[b]);
                     store32(at + 16 * b, f[b]);
                 }
@@ -432,6 +445,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             tmem_wait_st();
             signal(&x.ds_ready);
             if (lane == 0) mbar_arrive(&x.stat_free[i & 1]);
+            return true;
+        };
+        for (uint32_t i = 0; i < items; ++i, phase ^= 1) {
+            const bool masked = t == 0 || (t0 + t + 1) * kRows > full_to;
+            if (!(masked ? item(std::true_type{}, i) : item(std::false_type{}, i))) break;
             if (++t == per_head) t = 0;
         }
         ok = ok && wait(&x.done, 0) && wait(&x.scanned, 0);
@@ -675,34 +693,50 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        for (uint32_t i = 0; i < items; ++i, phase ^= 1) {
+        auto item = [&](auto with_mask, uint32_t i) {
+            constexpr bool kMask = decltype(with_mask)::value;
             const int32_t c0 = (lo + (int32_t)i) * kRows;
-            const bool final = i == items - 1, masked = final || c0 < full_from;
+            const bool final = kMask && i == items - 1;
             const int from = start - c0 - 64 * w, to = n - c0 - 64 * w;
+            int see[2] = {kSeeAll, kSeeAll};
+            uint32_t bits[2] = {~0u, ~0u};
+            if (kMask) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    see[b] = seen_run(32 * b, from, to);
+                    bits[b] = seen_bits(32 * b, from, to);
+                }
+            }
             float p[2][32], f[2][32];
-            if (!wait(&x.s_full, phase)) break;
+            if (!wait(&x.s_full, phase)) return false;
             tmem_ld32(at, p[0]);
             tmem_ld32(at + 32, p[1]);
             tmem_wait_ld();
             signal(&x.s_free);
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < 2; ++b) {
+                if (kMask && see[b] == kSeeNone) {
+                    fill32(p[b], 0.f);
+                    continue;
+                }
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     fma2(p[b][e], p[b][e + 1], cs, ls);
                     p[b][e] = ex2(p[b][e]);
                     p[b][e + 1] = ex2(p[b][e + 1]);
                 }
-            if (!wait(&x.dp_full, phase)) break;
+                if (kMask && see[b] == kSeeSome) hide32(p[b], bits[b], 0.f);
+            }
+            if (!wait(&x.dp_full, phase)) return false;
             tmem_ld32(at + kDP, f[0]);
             tmem_ld32(at + kDP + 32, f[1]);
             tmem_wait_ld();
             signal(&x.dp_free);
-            if (masked) {
+            if (kMask) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    hide32z(p[b], 32 * b, from, to);
-                    hide32z(f[b], 32 * b, from, to);
+                    if (see[b] == kSeeSome) hide32(f[b], bits[b], 0.f);
+                    else if (see[b] == kSeeNone) fill32(f[b], 0.f);
                 }
             }
             if (final) {
@@ -721,10 +755,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
+                if (!(kMask && see[b] == kSeeNone)) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    add2(f[b][e], f[b][e + 1], dl, dl);
-                    mul2v(f[b][e], f[b][e + 1], p[b][e], p[b][e + 1]);
+                    for (int e = 0; e < 32; e += 2) {
+                        add2(f[b][e], f[b][e + 1], dl, dl);
+                        mul2v(f[b][e], f[b][e + 1], p[b][e], p[b][e + 1]);
+                    }
                 }
                 store32(ds_at + 64 * (i & 1) + 16 * b, f[b]);
                 if (final) {
@@ -734,6 +770,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             }
             tmem_wait_st();
             signal(&x.ds_ready);
+            return true;
+        };
+        for (uint32_t i = 0; i < items; ++i, phase ^= 1) {
+            const bool masked = i == items - 1 || (lo + (int32_t)i) * kRows < full_from;
+            if (!(masked ? item(std::true_type{}, i) : item(std::false_type{}, i))) break;
         }
         if (!met) element_sync();                            // after an abort: the other warps may wait there
         ok = ok && wait(&x.done, 0) && wait(&x.scanned, 0);
@@ -764,7 +805,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
 int dkv_ranks(const AttnProb& p, int64_t blocks) {
     static const int force = getenv("DKV_R") ? atoi(getenv("DKV_R")) : 0;
     int ranks = 1;
-    while (ranks * 2 <= std::min(p.group, 8) && (force ? ranks < force : blocks * ranks < 4 * num_sms())) ranks *= 2;
+    while (ranks * 2 <= std::min(p.group, 8) && (force ? ranks < force : blocks * ranks < 3 * num_sms())) ranks *= 2;
     return ranks;
 }
 
