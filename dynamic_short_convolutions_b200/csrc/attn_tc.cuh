@@ -52,6 +52,13 @@ __device__ __forceinline__ void load_head_tile(uint8_t* dst, const CUtensorMap* 
     for (int a = 0; a < HD / 64; ++a) tma_load_3d(dst + a * kAtom, map, bar, 64 * a, head, row);
 }
 
+// The reverse (one thread); tokens from N on and channels from hd on are not written.
+template <int HD>
+__device__ __forceinline__ void store_head_tile(const CUtensorMap* map, const uint8_t* src, int head, int32_t row) {
+#pragma unroll
+    for (int a = 0; a < HD / 64; ++a) tma_store_3d(map, src + a * kAtom, 64 * a, head, row);
+}
+
 // ---------------------------------------------------------------- tcgen05 forms
 // D[tmem] (+)= A[tmem] * B[smem]: A holds a row per lane, two bf16 of the K index per column.
 __device__ __forceinline__ void umma_ts_bf16(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
@@ -146,14 +153,13 @@ __device__ __forceinline__ void add2(float& x, float& y, float a0, float a1) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
 }
 
-// 32 columns of an accumulator, times `mul`, to channels base .. base + 31 of a row (hd of them are real)
-__device__ __forceinline__ void put32(__nv_bfloat16* row, int base, int hd, const float (&f)[32], float mul) {
+// Columns 32 b .. 32 b + 31 of a row of an accumulator, times `mul`, as bf16 into a tile that TMA stores.
+__device__ __forceinline__ void tile_put32(uint8_t* tile, uint32_t row, int b, const float (&f)[32], float mul) {
 #pragma unroll
     for (int e = 0; e < 32; e += 8)
-        if (base + e < hd)
-            *reinterpret_cast<uint4*>(row + base + e) =
-                make_uint4(pack_bf16(f[e] * mul, f[e + 1] * mul), pack_bf16(f[e + 2] * mul, f[e + 3] * mul),
-                           pack_bf16(f[e + 4] * mul, f[e + 5] * mul), pack_bf16(f[e + 6] * mul, f[e + 7] * mul));
+        *reinterpret_cast<uint4*>(tile + (b / 2) * kAtom + sw128_off(row, (b % 2) * 4 + e / 8)) =
+            make_uint4(pack_bf16(f[e] * mul, f[e + 1] * mul), pack_bf16(f[e + 2] * mul, f[e + 3] * mul),
+                       pack_bf16(f[e + 4] * mul, f[e + 5] * mul), pack_bf16(f[e + 6] * mul, f[e + 7] * mul));
 }
 
 // ---------------------------------------------------------------- masks

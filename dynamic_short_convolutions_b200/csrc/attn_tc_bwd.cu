@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                                                                   const __grid_constant__ CUtensorMap tk,
                                                                   const __grid_constant__ CUtensorMap tv,
                                                                   const __grid_constant__ CUtensorMap td,
+                                                                  const __grid_constant__ CUtensorMap tdk,
+                                                                  const __grid_constant__ CUtensorMap tdv,
                                                                   const AttnTcArgs a) {
     using S = BwdSmem<HD>;
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -273,6 +275,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                                  kIdG, add || c > 0);
             }
         };
+        // A wait that finds its barrier complete still takes some 100 cycles, in which the tensor cores run dry: the
+        // two loads of the next item are asked after together, and tiles that TMA brought need no tcgen05 fence.
+        auto landed = [&](const Spot<HD>& p, const Spot<HD>& q) {
+            const bool u = mbar_try_wait(&x.full[p.slot], p.parity), v = mbar_try_wait(&x.full[q.slot], q.parity);
+            return (u && v) || (mbar_wait(&x.full[p.slot], p.parity, &x.abort_flag, a.err) &&
+                                mbar_wait(&x.full[q.slot], q.parity, &x.abort_flag, a.err));
+        };
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             const bool got = mbar_wait(bar, parity, &x.abort_flag, a.err);
             tc_fence_after();
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             const Spot<HD> q(2 * i), d(2 * i + 1), q1(2 * i + 2), d1(2 * i + 3);
             const bool more = i + 1 < items;
             auto next_scores = [&]() {
-                ok = ok && wait(&x.full[q1.slot], q1.parity) && wait(&x.s_free, phase);
+                ok = ok && landed(q1, d1) && wait(&x.s_free, phase);
                 if (ok) nt(0, k_at, r_at + q1.slot * S::tile, &x.s_full);
             };
             if (more && t > 0) next_scores();
@@ -305,10 +314,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 if (lead) umma_commit(&x.empty[q.slot]);
             }
             if (more && t == 0) next_scores();
-            if (more) {
-                ok = ok && wait(&x.full[d1.slot], d1.parity);
-                if (ok) nt(kDP, v_at, r_at + d1.slot * S::tile, &x.dp_full);
-            }
+            if (more && ok) nt(kDP, v_at, r_at + d1.slot * S::tile, &x.dp_full);
             if (++t == per_head) t = 0;
             __syncwarp();
         }
@@ -453,6 +459,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             if (++t == per_head) t = 0;
         }
         ok = ok && wait(&x.done, 0) && wait(&x.scanned, 0);
+        ok = !named_bar_any<1, 256>(!ok);                    // all warps go on, or none
         if (!ok) x.again = -1;                               // nothing is written then
         if (ranks > 1) {
             // this block's part, for the cluster: warps 0-3 dv, warps 4-7 dk
@@ -468,17 +475,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                     *reinterpret_cast<float4*>(row + 32 * b + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
             }
         } else if (ok && !x.again) {
-            // warps 0-3 write dv, warps 4-7 dk
-            __nv_bfloat16* row = w ? a.dk + (int64_t)j * a.dks : a.dv + (int64_t)j * a.dvs;
-            row += (int64_t)kv * a.hd;
+            // warps 0-3 dv, warps 4-7 dk, through the resident tiles and TMA
             const uint32_t src = tb + ((uint32_t)((warp & 3) * 32) << 16) + (w ? kDK : kDV);
-            const float mul = w ? a.scale : 1.f;
 #pragma unroll
             for (int b = 0; b < HD / 32; ++b) {
                 float f[32];
                 tmem_ld32(src + 32 * b, f);
                 tmem_wait_ld();
-                if (j < a.N) put32(row, 32 * b, a.hd, f, mul);
+                tile_put32(w ? sK : sV, (warp & 3) * 32 + lane, b, f, w ? a.scale : 1.f);
+            }
+            fence_async_smem();
+            element_sync();
+            if (threadIdx.x == 0) {
+                store_head_tile<HD>(&tdv, sV, kv, key0);
+                store_head_tile<HD>(&tdk, sK, kv, key0);
+                tma_store_commit();
             }
         } else if (ok) {
             const int32_t r = key0 + warp * 16;
@@ -491,7 +502,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         tc_fence_after();
         tmem_dealloc(tb, 512);
     }
-    if (ranks == 1) return;
+    if (ranks == 1) {
+        if (threadIdx.x == 0) tma_store_wait_all();          // the gradients have left shared memory
+        return;
+    }
     // Every thread of every block comes here, whatever became of its waits, so the cluster's barriers end.
     cluster.sync();
     int bad = 0;
@@ -532,6 +546,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                                                                  const __grid_constant__ CUtensorMap tk,
                                                                  const __grid_constant__ CUtensorMap tv,
                                                                  const __grid_constant__ CUtensorMap td,
+                                                                 const __grid_constant__ CUtensorMap tdq,
                                                                  const AttnTcArgs a) {
     using S = BwdSmem<HD>;
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -584,6 +599,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 umma_commit(bar);
             }
         };
+        auto landed = [&](const Spot<HD>& p) { return mbar_wait(&x.full[p.slot], p.parity, &x.abort_flag, a.err); };
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             const bool got = mbar_wait(bar, parity, &x.abort_flag, a.err);
             tc_fence_after();
@@ -600,9 +616,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         for (uint32_t i = 0; ok && i < items; ++i, phase ^= 1) {
             const Spot<HD> k(2 * i), k1(2 * i + 2), v1(2 * i + 3);
             if (i + 1 < items) {
-                ok = wait(&x.full[k1.slot], k1.parity) && wait(&x.s_free, phase);
+                ok = landed(k1) && wait(&x.s_free, phase);
                 if (ok) nt(0, q_at, r_at + k1.slot * S::tile, &x.s_full);
-                ok = ok && wait(&x.full[v1.slot], v1.parity) && wait(&x.dp_free, phase);
+                ok = ok && landed(v1) && wait(&x.dp_free, phase);
                 if (ok) {
                     nt(kDP, o_at, r_at + v1.slot * S::tile, &x.dp_full);
                     if (lead) umma_commit(&x.empty[v1.slot]);
@@ -778,15 +794,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         }
         if (!met) element_sync();                            // after an abort: the other warps may wait there
         ok = ok && wait(&x.done, 0) && wait(&x.scanned, 0);
+        ok = !named_bar_any<1, 256>(!ok);                    // all warps go on, or none
         if (ok && !x.again) {
-            __nv_bfloat16* to = a.dq + (int64_t)n * a.dqs + (int64_t)head * a.hd;
+            // each half of the warps takes half of the channels, through Q's tile and TMA
 #pragma unroll
-            for (int b = 0; b < HD / 64; ++b) {              // each half of the warps writes half of the channels
-                const int c = 32 * (b + w * (HD / 64));
+            for (int b = w * (HD / 64); b < (w + 1) * (HD / 64); ++b) {
                 float f[32];
-                tmem_ld32(tb + ((uint32_t)((warp & 3) * 32) << 16) + kDQ + c, f);
+                tmem_ld32(tb + ((uint32_t)((warp & 3) * 32) << 16) + kDQ + 32 * b, f);
                 tmem_wait_ld();
-                if (n < a.N) put32(to, c, a.hd, f, a.scale);
+                tile_put32(sQ, row, b, f, a.scale);
+            }
+            fence_async_smem();
+            element_sync();
+            if (threadIdx.x == 0) {
+                store_head_tile<HD>(&tdq, sQ, head, row0);
+                tma_store_commit();
             }
         } else if (ok) {
             const int32_t r = row0 + warp * 16;
@@ -799,6 +821,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         tc_fence_after();
         tmem_dealloc(tb, 512);
     }
+    if (threadIdx.x == 0) tma_store_wait_all();              // dq has left shared memory
 }
 
 // Blocks that share the heads of a group (a power of two up to 8).
@@ -811,13 +834,14 @@ int dkv_ranks(const AttnProb& p, int64_t blocks) {
 
 template <int HD>
 cudaError_t bwd_hd(const AttnProb& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const CUtensorMap& td, const AttnTcArgs& a, cudaStream_t st) {
+                   const CUtensorMap& td, const CUtensorMap& tdq, const CUtensorMap& tdk, const CUtensorMap& tdv,
+                   const AttnTcArgs& a, cudaStream_t st) {
     constexpr uint32_t smem = BwdSmem<HD>::bytes;
     cudaError_t e = DC_SMEM_LIMIT(attn_dkv_kernel<HD>, smem);
     if (e == cudaSuccess) e = DC_SMEM_LIMIT(attn_dq_kernel<HD>, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kRows - 1) / kRows;
-    DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<HD><<<(unsigned)(tiles * p.heads), kBwdThreads, smem, st>>>(tq, tk, tv, td, a));
+    DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<HD><<<(unsigned)(tiles * p.heads), kBwdThreads, smem, st>>>(tq, tk, tv, td, tdq, a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int ranks = dkv_ranks(p, tiles * p.kvh);
     cudaLaunchConfig_t cfg = {};
@@ -831,7 +855,7 @@ cudaError_t bwd_hd(const AttnProb& p, const CUtensorMap& tq, const CUtensorMap& 
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ranks > 1 ? 1 : 0;
-    DC_LAUNCH(kAttnTcDkv, st, e = cudaLaunchKernelEx(&cfg, attn_dkv_kernel<HD>, tq, tk, tv, td, a));
+    DC_LAUNCH(kAttnTcDkv, st, e = cudaLaunchKernelEx(&cfg, attn_dkv_kernel<HD>, tq, tk, tv, td, tdk, tdv, a));
     return e;
 }
 
@@ -842,9 +866,11 @@ cudaError_t attn_tc_bwd(const AttnProb& p, const void* d_o, const void* q, const
                         const void* o, const float* lse, float* delta, void* dq, void* dk, void* dv, uint32_t* err,
                         cudaStream_t st) {
     using namespace attn_tc;
-    CUtensorMap tq, tk, tv, td;
+    CUtensorMap tq, tk, tv, td, tdq, tdk, tdv;
     if (!make_head_map(&tq, q, p.N, p.heads, p.hd, p.qs) || !make_head_map(&tk, k, p.N, p.kvh, p.hd, p.ks) ||
-        !make_head_map(&tv, v, p.N, p.kvh, p.hd, p.vs) || !make_head_map(&td, d_o, p.N, p.heads, p.hd, p.dos))
+        !make_head_map(&tv, v, p.N, p.kvh, p.hd, p.vs) || !make_head_map(&td, d_o, p.N, p.heads, p.hd, p.dos) ||
+        !make_head_map(&tdq, dq, p.N, p.heads, p.hd, p.dqs) || !make_head_map(&tdk, dk, p.N, p.kvh, p.hd, p.dks) ||
+        !make_head_map(&tdv, dv, p.N, p.kvh, p.hd, p.dvs))
         return cudaErrorInvalidValue;
     AttnTcArgs a = tc_args(p);
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -858,7 +884,8 @@ cudaError_t attn_tc_bwd(const AttnProb& p, const void* d_o, const void* q, const
     a.lse = const_cast<float*>(lse);
     a.delta = delta;
     a.err = err;
-    return p.hd <= 64 ? bwd_hd<64>(p, tq, tk, tv, td, a, st) : bwd_hd<128>(p, tq, tk, tv, td, a, st);
+    return p.hd <= 64 ? bwd_hd<64>(p, tq, tk, tv, td, tdq, tdk, tdv, a, st)
+                      : bwd_hd<128>(p, tq, tk, tv, td, tdq, tdk, tdv, a, st);
 }
 
 }  // namespace dynconv

@@ -328,18 +328,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
                 float f[32];
                 tmem_ld32(tO + 32 * b, f);
                 tmem_wait_ld();
-                const uint32_t r = warp * 32 + lane;
-#pragma unroll
-                for (int e = 0; e < 32; e += 8)
-                    *reinterpret_cast<uint4*>(sQ + (b / 2) * kAtom + sw128_off(r, (b % 2) * 4 + e / 8)) =
-                        make_uint4(pack_bf16(f[e] * inv, f[e + 1] * inv), pack_bf16(f[e + 2] * inv, f[e + 3] * inv),
-                                   pack_bf16(f[e + 4] * inv, f[e + 5] * inv), pack_bf16(f[e + 6] * inv, f[e + 7] * inv));
+                tile_put32(sQ, warp * 32 + lane, b, f, inv);
             }
             fence_async_smem();
             softmax_sync();
             if (threadIdx.x == 0) {
-#pragma unroll
-                for (int c = 0; c < HD / 64; ++c) tma_store_3d(&to, sQ + c * kAtom, 64 * c, head, row0);
+                store_head_tile<HD>(&to, sQ, head, row0);
                 tma_store_commit();
             }
             if (a.lse != nullptr && n < a.N) a.lse[(int64_t)head * a.N + n] = (m + __log2f(l)) * kLn2;
