@@ -16,15 +16,20 @@
 //
 // Masked places: the score is replaced before the maximum, and in masked tiles a product with a
 // masked probability is not added at all (0 x NaN would be NaN).
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "attn.h"
 #include "common.cuh"
 #include "prof.h"
 #include "smem_limit.h"
+#include "tmap.h"
 
 namespace dynconv {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kTile = 64;
 constexpr int kThreads = 256;
@@ -34,6 +39,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 template <int HD>
 constexpr int ld_of() { return HD + 4; }
+// Stages of the forward's and dq's ring: two where two blocks still fit an SM.
+template <int HD>
+constexpr int stages_of() { return HD == 64 ? 2 : 1; }
 
 struct SimtArgs {
     int32_t N, seqlen, n_docs;
@@ -69,6 +77,31 @@ __device__ __forceinline__ void load_tile(float* dst, const T* __restrict__ src,
             const int r = i / HD, c = i % HD;
             dst[r * LD + c] = row0 + r < N && c < hd ? to_f32(src[(int64_t)(row0 + r) * stride + c]) : 0.f;
         }
+    }
+}
+
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// load_tile, fp32 rows on 16-byte boundaries as asynchronous copies (complete after copies_wait and a barrier).
+template <typename T, int HD>
+__device__ __forceinline__ void fetch_tile(float* dst, const T* __restrict__ src, int64_t stride, int32_t row0, int32_t N,
+                                           int hd, bool vec) {
+    if (sizeof(T) != 4 || !vec) {
+        load_tile<T, HD>(dst, src, stride, row0, N, hd, vec);
+        return;
+    }
+    constexpr int LD = ld_of<HD>();
+#pragma unroll
+    for (int i = threadIdx.x; i < kTile * (HD / 4); i += kThreads) {
+        const int r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+        const bool real = row0 + r < N && c < hd;
+        const T* p = src + (real ? (int64_t)(row0 + r) * stride + c : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(dst + r * LD + c)),
+                     "l"(p), "r"(real ? 16 : 0)
+                     : "memory");
     }
 }
 
@@ -164,12 +197,10 @@ template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const T* __restrict__ q, const T* __restrict__ k,
                                                                  const T* __restrict__ v, T* __restrict__ o,
                                                                  float* __restrict__ lse, SimtArgs a, int vec) {
-    constexpr int LD = ld_of<HD>();
+    constexpr int LD = ld_of<HD>(), NS = stages_of<HD>();
     extern __shared__ float sm[];
     float* sQ = sm;
-    float* sK = sQ + kTile * LD;
-    float* sV = sK + kTile * LD;
-    float* sP = sK;                        // the keys are read before the probabilities are written
+    float* ring = sQ + kTile * LD;         // stage s: K at ring + 2 s tiles, V behind it
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int head = blockIdx.x % a.heads, kv = head / a.group;
     const int32_t tiles = (a.N + kTile - 1) / kTile;
@@ -193,11 +224,24 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const T* __rest
         for (int c = 0; c < HD / 16; ++c) acc[i][c] = 0.f;
     }
     const float cs = a.scale * kLog2e;
-    for (int32_t k0 = first_key / kTile * kTile; k0 <= last; k0 += kTile) {
+    auto fetch = [&](int32_t k0, int at) {
+        if (k0 <= last) {
+            fetch_tile<T, HD>(ring + 2 * at * kTile * LD, k, a.ks, k0, a.N, a.hd, vec);
+            fetch_tile<T, HD>(ring + (2 * at + 1) * kTile * LD, v, a.vs, k0, a.N, a.hd, vec);
+        }
+        copies_close();
+    };
+    const int32_t k_first = first_key / kTile * kTile;
+    if (NS == 2) fetch(k_first, 0);
+    int at = 0;
+    for (int32_t k0 = k_first; k0 <= last; k0 += kTile, at ^= NS - 1) {
+        __syncthreads();                   // the stage fetched into now is read
+        fetch(NS == 2 ? k0 + kTile : k0, NS == 2 ? at ^ 1 : 0);
+        copies_wait<NS - 1>();
         __syncthreads();
-        load_tile<T, HD>(sK, k, a.ks, k0, a.N, a.hd, vec);
-        load_tile<T, HD>(sV, v, a.vs, k0, a.N, a.hd, vec);
-        __syncthreads();
+        const float* sK = ring + 2 * at * kTile * LD;
+        const float* sV = sK + kTile * LD;
+        float* sP = ring + 2 * at * kTile * LD;      // the keys are read before the probabilities are written
         float s[4][4];
         tile_nt<HD>(sQ, sK, s, ty, tx);
         const bool masked = k0 + kTile - 1 > row0 || k0 < full_from;
@@ -254,13 +298,11 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restr
                                                                 const float* __restrict__ lse,
                                                                 const float* __restrict__ delta, T* __restrict__ dq,
                                                                 SimtArgs a, int vec) {
-    constexpr int LD = ld_of<HD>();
+    constexpr int LD = ld_of<HD>(), NS = stages_of<HD>();
     extern __shared__ float sm[];
     float* sQ = sm;
     float* sO = sQ + kTile * LD;
-    float* sK = sO + kTile * LD;
-    float* sV = sK + kTile * LD;
-    float* sD = sV;                        // the values are read before ds is written
+    float* ring = sO + kTile * LD;         // stage s: K at ring + 2 s tiles, V behind it
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int head = blockIdx.x % a.heads, kv = head / a.group;
     const int32_t tiles = (a.N + kTile - 1) / kTile;
@@ -285,11 +327,24 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restr
         for (int c = 0; c < HD / 16; ++c) acc[i][c] = 0.f;
     }
     const float cs = a.scale * kLog2e;
-    for (int32_t k0 = first_key / kTile * kTile; k0 <= last; k0 += kTile) {
+    auto fetch = [&](int32_t k0, int at) {
+        if (k0 <= last) {
+            fetch_tile<T, HD>(ring + 2 * at * kTile * LD, k, a.ks, k0, a.N, a.hd, vec);
+            fetch_tile<T, HD>(ring + (2 * at + 1) * kTile * LD, v, a.vs, k0, a.N, a.hd, vec);
+        }
+        copies_close();
+    };
+    const int32_t k_first = first_key / kTile * kTile;
+    if (NS == 2) fetch(k_first, 0);
+    int at = 0;
+    for (int32_t k0 = k_first; k0 <= last; k0 += kTile, at ^= NS - 1) {
+        __syncthreads();                   // the stage fetched into now is read
+        fetch(NS == 2 ? k0 + kTile : k0, NS == 2 ? at ^ 1 : 0);
+        copies_wait<NS - 1>();
         __syncthreads();
-        load_tile<T, HD>(sK, k, a.ks, k0, a.N, a.hd, vec);
-        load_tile<T, HD>(sV, v, a.vs, k0, a.N, a.hd, vec);
-        __syncthreads();
+        const float* sK = ring + 2 * at * kTile * LD;
+        const float* sV = sK + kTile * LD;
+        float* sD = ring + (2 * at + 1) * kTile * LD;        // the values are read before ds is written
         float s[4][4], dp[4][4];
         tile_nt<HD>(sQ, sK, s, ty, tx);
         tile_nt<HD>(sO, sV, dp, ty, tx);
@@ -316,7 +371,8 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restr
 }
 
 // dk and dv of 64 keys of one key/value head: every head of the group, every tile of queries that sees
-// a key of the tile, in order (no atomics).  Scores are held transposed: rows are keys.
+// a key of the tile, in order (no atomics).  Scores are held transposed: rows are keys.  With few key tiles the
+// heads of a group are shared out over a cluster of blocks.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __restrict__ d_o, const T* __restrict__ q,
                                                                  const T* __restrict__ k, const T* __restrict__ v,
@@ -332,10 +388,12 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __rest
     float* sP = sO + kTile * LD;
     float* sD = sP + kTile * kLdP;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    const int kv = blockIdx.x % a.kvh;
-    const int32_t row0 = (int32_t)(blockIdx.x / a.kvh) * kTile;           // early keys have the most queries
-    load_tile<T, HD>(sK, k + (int64_t)kv * a.hd, a.ks, row0, a.N, a.hd, vec);
-    load_tile<T, HD>(sV, v + (int64_t)kv * a.hd, a.vs, row0, a.N, a.hd, vec);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int kv = (int)(blockIdx.x / ranks) % a.kvh;
+    const int32_t row0 = (int32_t)(blockIdx.x / ranks / a.kvh) * kTile;   // early keys have the most queries
+    fetch_tile<T, HD>(sK, k + (int64_t)kv * a.hd, a.ks, row0, a.N, a.hd, vec);
+    fetch_tile<T, HD>(sV, v + (int64_t)kv * a.hd, a.vs, row0, a.N, a.hd, vec);
     const int32_t last = min(row0 + kTile, a.N) - 1;
     int32_t s0, first_end, e_last;
     seg_bounds32(row0, a.cu, a.n_docs, a.seqlen, a.N, s0, first_end);
@@ -351,12 +409,13 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __rest
         for (int c = 0; c < HD / 16; ++c) acck[i][c] = accv[i][c] = 0.f;
     }
     const float cs = a.scale * kLog2e;
-    for (int g = 0; g < a.group; ++g) {
-        const int head = kv * a.group + g;
+    // this block's heads of the group
+    for (int head = kv * a.group + rank * a.group / ranks; head < kv * a.group + (rank + 1) * a.group / ranks; ++head) {
         for (int32_t q0 = row0; q0 < e_last; q0 += kTile) {
             __syncthreads();
-            load_tile<T, HD>(sQ, q + (int64_t)head * a.hd, a.qs, q0, a.N, a.hd, vec);
-            load_tile<T, HD>(sO, d_o + (int64_t)head * a.hd, a.dos, q0, a.N, a.hd, vec);
+            fetch_tile<T, HD>(sQ, q + (int64_t)head * a.hd, a.qs, q0, a.N, a.hd, vec);
+            fetch_tile<T, HD>(sO, d_o + (int64_t)head * a.hd, a.dos, q0, a.N, a.hd, vec);
+            copies_close();
             float ls[4], dl[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -364,6 +423,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __rest
                 ls[j] = lse[(int64_t)head * a.N + n] * kLog2e;
                 dl[j] = delta[(int64_t)head * a.N + n];
             }
+            copies_wait<0>();
             __syncthreads();
             float s[4][4], dp[4][4];
             tile_nt<HD>(sK, sQ, s, ty, tx);
@@ -393,8 +453,38 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __rest
             }
         }
     }
-    store_rows<T, HD>(dk + (int64_t)kv * a.hd, a.dks, row0, a.N, a.hd, acck, mk, ty, tx);
-    store_rows<T, HD>(dv + (int64_t)kv * a.hd, a.dvs, row0, a.N, a.hd, accv, mv, ty, tx);
+    dk += (int64_t)kv * a.hd;
+    dv += (int64_t)kv * a.hd;
+    if (ranks == 1) {
+        store_rows<T, HD>(dk, a.dks, row0, a.N, a.hd, acck, mk, ty, tx);
+        store_rows<T, HD>(dv, a.dvs, row0, a.N, a.hd, accv, mv, ty, tx);
+        return;
+    }
+    // partial sums of the cluster's blocks, added in the order of their ranks, each block a share of the rows
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int jj = 0; jj < HD / 64; ++jj) {
+            const int at = (4 * ty + i) * LD + 4 * tx + 64 * jj;
+            *reinterpret_cast<float4*>(sQ + at) = make_float4(acck[i][4 * jj], acck[i][4 * jj + 1], acck[i][4 * jj + 2], acck[i][4 * jj + 3]);
+            *reinterpret_cast<float4*>(sO + at) = make_float4(accv[i][4 * jj], accv[i][4 * jj + 1], accv[i][4 * jj + 2], accv[i][4 * jj + 3]);
+        }
+    cluster.sync();
+    const int per = kTile / ranks;
+    for (int i = threadIdx.x; i < per * HD; i += kThreads) {
+        const int r = rank * per + i / HD, c = i % HD;
+        float x = 0.f, y = 0.f;
+        for (int n = 0; n < ranks; ++n) {
+            x += cluster.map_shared_rank(sQ, n)[r * LD + c];
+            y += cluster.map_shared_rank(sO, n)[r * LD + c];
+        }
+        if (row0 + r < a.N && c < a.hd) {
+            dk[(int64_t)(row0 + r) * a.dks + c] = from_f32<T>(x * a.scale);
+            dv[(int64_t)(row0 + r) * a.dvs + c] = from_f32<T>(y);
+        }
+    }
+    cluster.sync();                        // no block leaves while its part is read
 }
 
 // A warp per (token, head); lanes over the channels.
@@ -428,7 +518,7 @@ int vec_ok(const AttnProb& p, bool bwd) {
 template <typename T, int HD>
 cudaError_t fwd_t(const AttnProb& p, const void* q, const void* k, const void* v, void* o, float* lse,
                   cudaStream_t st) {
-    constexpr size_t smem = sizeof(float) * 3 * kTile * ld_of<HD>();
+    constexpr size_t smem = sizeof(float) * (1 + 2 * stages_of<HD>()) * kTile * ld_of<HD>();
     cudaError_t e = DC_SMEM_LIMIT((attn_fwd_simt_kernel<T, HD>), smem);
     if (e != cudaSuccess) return e;
     const unsigned grid = (unsigned)((p.N + kTile - 1) / kTile * p.heads);
@@ -441,17 +531,30 @@ cudaError_t fwd_t(const AttnProb& p, const void* q, const void* k, const void* v
 template <typename T, int HD>
 cudaError_t bwd_t(const AttnProb& p, const void* d_o, const void* q, const void* k, const void* v, const float* lse,
                   const float* delta, void* dq, void* dk, void* dv, cudaStream_t st) {
-    constexpr size_t smem_q = sizeof(float) * 4 * kTile * ld_of<HD>();
-    constexpr size_t smem_kv = smem_q + sizeof(float) * 2 * kTile * kLdP;
+    constexpr size_t smem_q = sizeof(float) * (2 + 2 * stages_of<HD>()) * kTile * ld_of<HD>();
+    constexpr size_t smem_kv = sizeof(float) * (4 * kTile * ld_of<HD>() + 2 * kTile * kLdP);
     cudaError_t e = DC_SMEM_LIMIT((attn_dq_simt_kernel<T, HD>), smem_q);
     if (e == cudaSuccess) e = DC_SMEM_LIMIT((attn_dkv_simt_kernel<T, HD>), smem_kv);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kTile - 1) / kTile;
-    DC_LAUNCH(kAttnSimtDkv, st, attn_dkv_simt_kernel<T, HD><<<(unsigned)(tiles * p.kvh), kThreads, smem_kv, st>>>(
-                                    static_cast<const T*>(d_o), static_cast<const T*>(q), static_cast<const T*>(k),
-                                    static_cast<const T*>(v), lse, delta, static_cast<T*>(dk), static_cast<T*>(dv),
-                                    args_of(p), vec_ok(p, true)));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    int ranks = 1;
+    while (ranks * 2 <= std::min(p.group, 8) && tiles * p.kvh * ranks < 2 * num_sms()) ranks *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * p.kvh * ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_kv;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ranks > 1 ? 1 : 0;
+    DC_LAUNCH(kAttnSimtDkv, st, e = cudaLaunchKernelEx(&cfg, attn_dkv_simt_kernel<T, HD>, static_cast<const T*>(d_o),
+                                                       static_cast<const T*>(q), static_cast<const T*>(k),
+                                                       static_cast<const T*>(v), lse, delta, static_cast<T*>(dk),
+                                                       static_cast<T*>(dv), args_of(p), vec_ok(p, true)));
+    if (e != cudaSuccess) return e;
     DC_LAUNCH(kAttnSimtDq, st, attn_dq_simt_kernel<T, HD><<<(unsigned)(tiles * p.heads), kThreads, smem_q, st>>>(
                                    static_cast<const T*>(d_o), static_cast<const T*>(q), static_cast<const T*>(k),
                                    static_cast<const T*>(v), lse, delta, static_cast<T*>(dq), args_of(p),
