@@ -30,12 +30,18 @@ struct AttnProb {
     float scale;            // of the scores
     const int32_t* cu;
     int64_t n_docs;
+    // of packed documents, written by attn_prep: every token's document (start, end), and the query and key tiles
+    // in descending order of their work
+    const int2* seg;
+    const int32_t *order_q, *order_k;
 };
-// Workspace of the attention passes: the error word, then D[heads][N] of the backward.
+// Workspace of the attention passes: the error word, D[heads][N] of the backward, what attn_prep writes.
 struct AttnWs {
-    size_t delta, total;
+    size_t delta, seg, order, total;
 };
-AttnWs attn_ws(const AttnProb& p);
+AttnWs attn_ws(const AttnProb& p, bool packed);
+constexpr int kTcTile = 128, kSimtTile = 64;      // tokens per tile of either kernel family
+cudaError_t attn_prep(const AttnProb& p, int tile, int2* seg, int32_t* order, uint32_t* err, cudaStream_t st);
 // Why the tensor-core kernels do not take the problem (nullptr when they do).
 const char* attn_tc_refusal(const AttnProb& p);
 

@@ -168,12 +168,29 @@ bool attn_tc(const AttnProb& p) { return p.algo != DYNCONV_ALGO_SIMT && attn_tc_
 
 uint32_t* err_of(void* ws) { return static_cast<uint32_t*>(ws); }
 
+// Packed documents: the check of cu_seqlens and the kernels' view of them, into the workspace.
+dynconv_status prepare_docs(AttnProb* p, void* ws, cudaStream_t st) {
+    const AttnWs w = attn_ws(*p, true);
+    char* base = static_cast<char*>(ws);
+    int2* seg = reinterpret_cast<int2*>(base + w.seg);
+    int32_t* order = reinterpret_cast<int32_t*>(base + w.order);
+    const int tile = attn_tc(*p) ? kTcTile : kSimtTile;
+    p->seg = seg;
+    p->order_q = order;
+    p->order_k = order + (p->N + tile - 1) / tile;
+    return cuda_status(attn_prep(*p, tile, seg, order, err_of(ws), st), "packed documents");
+}
+
 }  // namespace
 
-AttnWs attn_ws(const AttnProb& p) {
+AttnWs attn_ws(const AttnProb& p, bool packed) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t N = (size_t)p.N;
     AttnWs w{};
     w.delta = 256;
-    w.total = w.delta + ((size_t)p.N * p.heads * sizeof(float) + 255) / 256 * 256;
+    w.seg = w.delta + up(N * p.heads * sizeof(float));
+    w.order = w.seg + (packed ? up(N * sizeof(int2)) : 0);
+    w.total = w.order + (packed ? up(2 * ((N + kSimtTile - 1) / kSimtTile) * sizeof(int32_t)) : 0);
     return w;
 }
 
@@ -235,7 +252,7 @@ size_t dynconv_attn_workspace_bytes(const dynconv_attn_desc* desc) {
     set_error("%s", "");
     AttnProb p;
     if (make_attn(desc, &p) != DYNCONV_OK) return 0;
-    return attn_ws(p).total;
+    return attn_ws(p, desc->batch == 1).total;        // one sequence: packed documents may be given
 }
 
 dynconv_status dynconv_attn_query_family(const dynconv_attn_desc* desc, int32_t* fwd_family, int32_t* bwd_family) {
@@ -265,12 +282,10 @@ dynconv_status dynconv_attn_fwd(const dynconv_attn_desc* desc, const int32_t* cu
     if (p.N == 0) return DYNCONV_OK;
     if ((s = validate_ptr(q, "q", true)) || (s = validate_ptr(k, "k", true)) || (s = validate_ptr(v, "v", true)) ||
         (s = validate_ptr(o, "o", true)) || (s = validate_ptr(lse, "lse", false)) ||
-        (s = check_ws(ws, ws_bytes, attn_ws(p).total)))
+        (s = check_ws(ws, ws_bytes, attn_ws(p, desc->batch == 1).total)))
         return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cu_seqlens &&
-        (s = cuda_status(launch_check_seqlens(cu_seqlens, n_docs, p.N, err_of(ws), st), "cu_seqlens check")))
-        return s;
+    if (cu_seqlens && (s = prepare_docs(&p, ws, st)) != DYNCONV_OK) return s;
     return cuda_status(attn_tc(p) ? attn_tc_fwd(p, q, k, v, o, lse, err_of(ws), st)
                                   : attn_simt_fwd(p, q, k, v, o, lse, st),
                        "attention forward launch");
@@ -291,13 +306,11 @@ dynconv_status dynconv_attn_bwd(const dynconv_attn_desc* desc, const int32_t* cu
     if ((s = validate_ptr(d_o, "d_o", true)) || (s = validate_ptr(q, "q", true)) || (s = validate_ptr(k, "k", true)) ||
         (s = validate_ptr(v, "v", true)) || (s = validate_ptr(o, "o", true)) || (s = validate_ptr(lse, "lse", true)) ||
         (s = validate_ptr(dq, "dq", true)) || (s = validate_ptr(dk, "dk", true)) || (s = validate_ptr(dv, "dv", true)) ||
-        (s = check_ws(ws, ws_bytes, attn_ws(p).total)))
+        (s = check_ws(ws, ws_bytes, attn_ws(p, desc->batch == 1).total)))
         return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cu_seqlens &&
-        (s = cuda_status(launch_check_seqlens(cu_seqlens, n_docs, p.N, err_of(ws), st), "cu_seqlens check")))
-        return s;
-    float* delta = reinterpret_cast<float*>(static_cast<char*>(ws) + attn_ws(p).delta);
+    if (cu_seqlens && (s = prepare_docs(&p, ws, st)) != DYNCONV_OK) return s;
+    float* delta = reinterpret_cast<float*>(static_cast<char*>(ws) + attn_ws(p, desc->batch == 1).delta);
     if (attn_tc(p))
         return cuda_status(attn_tc_bwd(p, d_o, q, k, v, o, lse, delta, dq, dk, dv, err_of(ws), st),
                            "attention backward launch");

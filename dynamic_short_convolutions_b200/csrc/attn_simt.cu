@@ -31,7 +31,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kTile = 64;
+constexpr int kTile = kSimtTile;
 constexpr int kThreads = 256;
 constexpr int kLdP = kTile + 4;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -44,11 +44,12 @@ template <int HD>
 constexpr int stages_of() { return HD == 64 ? 2 : 1; }
 
 struct SimtArgs {
-    int32_t N, seqlen, n_docs;
+    int32_t N, seqlen;
     int heads, kvh, group, hd;
     int64_t qs, ks, vs, os, dos, dqs, dks, dvs;
     float scale;
-    const int32_t* cu;
+    const int2* seg;
+    const int32_t *order_q, *order_k;
 };
 
 // rows row0 .. row0 + 63 of one head (channels hd, zero beyond hd and beyond N) into fp32 shared memory
@@ -105,31 +106,58 @@ __device__ __forceinline__ void fetch_tile(float* dst, const T* __restrict__ src
     }
 }
 
-// acc[i][j] = A[4 ty + i] . B[tx + 16 j] over HD channels
+// Two fp32 lanes at once: d += a * b, each lane one fused multiply-add (the packed fp32 FMA of sm_100).
+__device__ __forceinline__ void pair_fma(uint64_t& d, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+
+// acc[i][j] = A[4 ty + i] . B[tx + 16 j] over HD channels; even and odd channels summed apart (packed FMAs: half the
+// instructions of a kernel that the issue rate bounds)
 template <int HD>
 __device__ __forceinline__ void tile_nt(const float* A, const float* B, float (&acc)[4][4], int ty, int tx) {
     constexpr int LD = ld_of<HD>();
+    uint64_t sum[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) sum[i][j] = 0;
 #pragma unroll 4
     for (int c = 0; c < HD; c += 4) {
-        float4 a[4], b[4];
+        ulonglong2 a[4], b[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * LD + c);
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(A + (4 * ty + i) * LD + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * LD + c);
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const ulonglong2*>(B + (tx + 16 * j) * LD + c);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
-                acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
-                acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
-                acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+                pair_fma(sum[i][j], a[i].x, b[j].x);
+                pair_fma(sum[i][j], a[i].y, b[j].y);
             }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(sum[i][j]));
+            acc[i][j] = lo + hi;
+        }
+}
+
+// Whether a tile holds an infinity or a NaN: the block's answer (a barrier).  A masked place has probability 0, so
+// without them the plain products serve masked tiles too; with them tile_nn leaves masked terms out.
+template <int HD>
+__device__ __forceinline__ bool tile_odd(const float* X, bool ask) {
+    constexpr int LD = ld_of<HD>();
+    bool odd = false;
+    if (ask)
+        for (int i = threadIdx.x; i < kTile * (HD / 4); i += kThreads) {
+            const float4 f = *reinterpret_cast<const float4*>(X + i / (HD / 4) * LD + i % (HD / 4) * 4);
+            odd = odd || !(fabsf(f.x) < INFINITY && fabsf(f.y) < INFINITY && fabsf(f.z) < INFINITY && fabsf(f.w) < INFINITY);
+        }
+    return __syncthreads_or(odd) != 0;
 }
 
 // acc[i][4 jj + e] += sum_c P[4 ty + i][c] X[c][4 tx + 64 jj + e]; with MASK only over c in [lo_i, hi_i]
@@ -204,20 +232,21 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const T* __rest
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int head = blockIdx.x % a.heads, kv = head / a.group;
     const int32_t tiles = (a.N + kTile - 1) / kTile;
-    const int32_t row0 = (tiles - 1 - (int32_t)(blockIdx.x / a.heads)) * kTile;   // long rows first
+    const int32_t row0 = tile_of((int32_t)(blockIdx.x / a.heads), tiles, a.seqlen % kTile ? 0 : a.seqlen / kTile, a.order_q,
+                                 false) * kTile;
     q += (int64_t)head * a.hd;
     o += (int64_t)head * a.hd;
     k += (int64_t)kv * a.hd;
     v += (int64_t)kv * a.hd;
     load_tile<T, HD>(sQ, q, a.qs, row0, a.N, a.hd, vec);
     const int32_t last = min(row0 + kTile, a.N) - 1;
-    const int32_t first_key = seg_start32(row0, a.cu, a.n_docs, a.seqlen);
-    const int32_t full_from = seg_start32(last, a.cu, a.n_docs, a.seqlen);
+    const int32_t first_key = doc_of(row0, a.seg, a.seqlen).x;
+    const int32_t full_from = doc_of(last, a.seg, a.seqlen).x;
     int32_t start[4];
     float m[4], l[4], acc[4][HD / 16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        start[i] = seg_start32(min(row0 + 4 * ty + i, a.N - 1), a.cu, a.n_docs, a.seqlen);
+        start[i] = doc_of(min(row0 + 4 * ty + i, a.N - 1), a.seg, a.seqlen).x;
         m[i] = -INFINITY;
         l[i] = 0.f;
 #pragma unroll
@@ -271,13 +300,13 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const T* __rest
 #pragma unroll
             for (int c = 0; c < HD / 16; ++c) acc[i][c] *= corr;
         }
-        __syncthreads();
+        const bool odd = tile_odd<HD>(sV, masked);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) sP[(4 * ty + i) * kLdP + tx + 16 * j] = s[i][j];
         __syncthreads();
-        if (masked) tile_nn<HD, true>(sP, sV, acc, ty, tx, lo, hi);
+        if (odd) tile_nn<HD, true>(sP, sV, acc, ty, tx, lo, hi);
         else tile_nn<HD, false>(sP, sV, acc, ty, tx, lo, hi);
     }
     float inv[4];
@@ -306,20 +335,21 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restr
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int head = blockIdx.x % a.heads, kv = head / a.group;
     const int32_t tiles = (a.N + kTile - 1) / kTile;
-    const int32_t row0 = (tiles - 1 - (int32_t)(blockIdx.x / a.heads)) * kTile;
+    const int32_t row0 = tile_of((int32_t)(blockIdx.x / a.heads), tiles, a.seqlen % kTile ? 0 : a.seqlen / kTile, a.order_q,
+                                 false) * kTile;
     load_tile<T, HD>(sQ, q + (int64_t)head * a.hd, a.qs, row0, a.N, a.hd, vec);
     load_tile<T, HD>(sO, d_o + (int64_t)head * a.hd, a.dos, row0, a.N, a.hd, vec);
     k += (int64_t)kv * a.hd;
     v += (int64_t)kv * a.hd;
     const int32_t last = min(row0 + kTile, a.N) - 1;
-    const int32_t first_key = seg_start32(row0, a.cu, a.n_docs, a.seqlen);
-    const int32_t full_from = seg_start32(last, a.cu, a.n_docs, a.seqlen);
+    const int32_t first_key = doc_of(row0, a.seg, a.seqlen).x;
+    const int32_t full_from = doc_of(last, a.seg, a.seqlen).x;
     int32_t start[4];
     float ls[4], dl[4], acc[4][HD / 16], mul[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int32_t n = min(row0 + 4 * ty + i, a.N - 1);
-        start[i] = seg_start32(n, a.cu, a.n_docs, a.seqlen);
+        start[i] = doc_of(n, a.seg, a.seqlen).x;
         ls[i] = lse[(int64_t)head * a.N + n] * kLog2e;
         dl[i] = delta[(int64_t)head * a.N + n];
         mul[i] = a.scale;
@@ -350,7 +380,7 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restr
         tile_nt<HD>(sO, sV, dp, ty, tx);
         const bool masked = k0 + kTile - 1 > row0 || k0 < full_from;
         int lo[4], hi[4];
-        __syncthreads();
+        const bool odd = tile_odd<HD>(sK, masked);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             lo[i] = start[i] - k0;
@@ -364,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restr
             }
         }
         __syncthreads();
-        if (masked) tile_nn<HD, true>(sD, sK, acc, ty, tx, lo, hi);
+        if (odd) tile_nn<HD, true>(sD, sK, acc, ty, tx, lo, hi);
         else tile_nn<HD, false>(sD, sK, acc, ty, tx, lo, hi);
     }
     store_rows<T, HD>(dq + (int64_t)head * a.hd, a.dqs, row0, a.N, a.hd, acc, mul, ty, tx);
@@ -391,18 +421,18 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __rest
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int kv = (int)(blockIdx.x / ranks) % a.kvh;
-    const int32_t row0 = (int32_t)(blockIdx.x / ranks / a.kvh) * kTile;   // early keys have the most queries
+    const int32_t row0 = tile_of((int32_t)(blockIdx.x / ranks / a.kvh), (a.N + kTile - 1) / kTile,
+                                 a.seqlen % kTile ? 0 : a.seqlen / kTile, a.order_k, true) * kTile;
     fetch_tile<T, HD>(sK, k + (int64_t)kv * a.hd, a.ks, row0, a.N, a.hd, vec);
     fetch_tile<T, HD>(sV, v + (int64_t)kv * a.hd, a.vs, row0, a.N, a.hd, vec);
     const int32_t last = min(row0 + kTile, a.N) - 1;
-    int32_t s0, first_end, e_last;
-    seg_bounds32(row0, a.cu, a.n_docs, a.seqlen, a.N, s0, first_end);
-    seg_bounds32(last, a.cu, a.n_docs, a.seqlen, a.N, s0, e_last);        // queries end with the last key's document
+    const int32_t first_end = doc_of(row0, a.seg, a.seqlen).y;
+    const int32_t e_last = doc_of(last, a.seg, a.seqlen).y;               // queries end with the last key's document
     int32_t end[4];
     float acck[4][HD / 16], accv[4][HD / 16], mk[4], mv[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        seg_bounds32(min(row0 + 4 * ty + i, a.N - 1), a.cu, a.n_docs, a.seqlen, a.N, s0, end[i]);
+        end[i] = doc_of(min(row0 + 4 * ty + i, a.N - 1), a.seg, a.seqlen).y;
         mk[i] = a.scale;
         mv[i] = 1.f;
 #pragma unroll
@@ -430,6 +460,11 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __rest
             tile_nt<HD>(sV, sO, dp, ty, tx);
             const bool masked = q0 < row0 + kTile || q0 + kTile > first_end;
             int lo[4], hi[4];
+            bool odd = false;
+            if (masked) {
+                odd = tile_odd<HD>(sQ, true);
+                odd = tile_odd<HD>(sO, true) || odd;
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 lo[i] = row0 + 4 * ty + i - q0;
@@ -444,7 +479,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __rest
                 }
             }
             __syncthreads();
-            if (masked) {
+            if (odd) {
                 tile_nn<HD, true>(sP, sO, accv, ty, tx, lo, hi);
                 tile_nn<HD, true>(sD, sQ, acck, ty, tx, lo, hi);
             } else {
@@ -506,8 +541,8 @@ __global__ void __launch_bounds__(kThreads) attn_delta_kernel(const T* __restric
 }
 
 SimtArgs args_of(const AttnProb& p) {
-    return SimtArgs{(int32_t)p.N, (int32_t)p.seqlen, (int32_t)p.n_docs, p.heads, p.kvh, p.group, p.hd, p.qs, p.ks, p.vs,
-                    p.os, p.dos, p.dqs, p.dks, p.dvs, p.scale, p.cu};
+    return SimtArgs{(int32_t)p.N, (int32_t)p.seqlen, p.heads, p.kvh, p.group, p.hd, p.qs, p.ks, p.vs,
+                    p.os, p.dos, p.dqs, p.dks, p.dvs, p.scale, p.seg, p.order_q, p.order_k};
 }
 
 // 16-byte (fp32) or 8-byte (bf16) loads of four channels: head starts and rows on such boundaries

@@ -13,7 +13,7 @@ namespace attn_tc {
 
 using namespace tc;
 
-constexpr int kRows = 128;                       // tokens per tile: the lanes of TMEM
+constexpr int kRows = kTcTile;                   // 128 tokens per tile: the lanes of TMEM
 constexpr uint32_t kAtom = kRows * 128;          // bytes of a 128-token x 64-channel tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -226,9 +226,10 @@ __device__ __forceinline__ void axpy4(float4& a, float f, float4 x) {
 }
 
 struct AttnTcArgs {
-    int32_t N, seqlen, n_docs;
+    int32_t N, seqlen;
     int heads, kvh, group, hd;
-    const int32_t* cu;
+    const int2* seg;
+    const int32_t *order_q, *order_k;
     float scale;
     uint32_t* err;
     // plain addresses, for the rows recomputed one by one and the outputs
@@ -243,12 +244,13 @@ inline AttnTcArgs tc_args(const AttnProb& p) {
     AttnTcArgs a{};
     a.N = (int32_t)p.N;
     a.seqlen = (int32_t)p.seqlen;
-    a.n_docs = (int32_t)p.n_docs;
     a.heads = p.heads;
     a.kvh = p.kvh;
     a.group = p.group;
     a.hd = p.hd;
-    a.cu = p.cu;
+    a.seg = p.seg;
+    a.order_q = p.order_q;
+    a.order_k = p.order_k;
     a.scale = p.scale;
     a.qs = p.qs; a.ks = p.ks; a.vs = p.vs; a.os = p.os;
     a.dos = p.dos; a.dqs = p.dqs; a.dks = p.dks; a.dvs = p.dvs;

@@ -154,8 +154,7 @@ __device__ __noinline__ void dkv_rows_again(const AttnTcArgs& a, int kv, int32_t
     const float cs = a.scale * kLog2e;
     for (int r = 0; r < count; ++r) {
         const int32_t j = key0 + r;
-        int32_t s0, end;
-        seg_bounds32(j, a.cu, a.n_docs, a.seqlen, a.N, s0, end);
+        const int32_t end = doc_of(j, a.seg, a.seqlen).y;
         const float4 k = row4(a.k + (int64_t)j * a.ks + (int64_t)kv * a.hd, lane, a.hd);
         const float4 v = row4(a.v + (int64_t)j * a.vs + (int64_t)kv * a.hd, lane, a.hd);
         float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
@@ -188,7 +187,7 @@ __device__ __noinline__ void dq_rows_again(const AttnTcArgs& a, int head, int32_
         const float dl = warp_dot(d, row4(a.o + (int64_t)n * a.os + (int64_t)head * a.hd, lane, a.hd));
         if (lane == 0) a.delta[(int64_t)head * a.N + n] = dl;
         float4 dq = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int32_t j = seg_start32(n, a.cu, a.n_docs, a.seqlen); j <= n; ++j) {
+        for (int32_t j = doc_of(n, a.seg, a.seqlen).x; j <= n; ++j) {
             const float4 k = row4(a.k + (int64_t)j * a.ks + (int64_t)kv * a.hd, lane, a.hd);
             const float4 v = row4(a.v + (int64_t)j * a.vs + (int64_t)kv * a.hd, lane, a.hd);
             const float p = exp2f(fmaf(warp_dot(q, k), cs, -ls));
@@ -219,12 +218,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int kv = (int)(blockIdx.x / ranks) % a.kvh;
-    const int32_t key0 = (int32_t)(blockIdx.x / ranks / a.kvh) * kRows;  // early keys have the most queries
+    const int32_t key0 = tile_of((int32_t)(blockIdx.x / ranks / a.kvh), (a.N + kRows - 1) / kRows,
+                                 a.seqlen % kRows ? 0 : a.seqlen / kRows, a.order_k, true) * kRows;
     const int head0 = kv * a.group + rank * a.group / ranks;             // this block's heads
     const int heads = kv * a.group + (rank + 1) * a.group / ranks - head0;
-    int32_t s0, full_to, e_last;
-    seg_bounds32(key0, a.cu, a.n_docs, a.seqlen, a.N, s0, full_to);      // queries below it see every key of the tile
-    seg_bounds32(min(key0 + kRows, a.N) - 1, a.cu, a.n_docs, a.seqlen, a.N, s0, e_last);
+    const int32_t full_to = doc_of(key0, a.seg, a.seqlen).y;             // queries below it see every key of the tile
+    const int32_t e_last = doc_of(min(key0 + kRows, a.N) - 1, a.seg, a.seqlen).y;
     const int32_t t0 = key0 / kRows, per_head = (e_last - 1) / kRows - t0 + 1;
     const uint32_t items = (uint32_t)per_head * heads;
     if (misplaced(sm, a.err)) return;
@@ -365,8 +364,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         const int32_t j = key0 + (warp & 3) * 32 + lane;
         const uint32_t at = tb + ((uint32_t)((warp & 3) * 32) << 16) + 64 * w;
         const float cs = a.scale * kLog2e;
-        int32_t end = 0;
-        if (j < a.N) seg_bounds32(j, a.cu, a.n_docs, a.seqlen, a.N, s0, end);
+        const int32_t end = j < a.N ? doc_of(j, a.seg, a.seqlen).y : 0;
         bool ok = true;
         uint32_t phase = 0;
         int32_t t = 0;
@@ -559,9 +557,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.heads, kv = head / a.group;
     const int32_t tiles = (a.N + kRows - 1) / kRows;
-    const int32_t row0 = (tiles - 1 - (int32_t)(blockIdx.x / a.heads)) * kRows;           // long rows first
-    const int32_t lo = seg_start32(row0, a.cu, a.n_docs, a.seqlen) / kRows, hi = row0 / kRows;
-    const int32_t full_from = seg_start32(min(row0 + kRows, a.N) - 1, a.cu, a.n_docs, a.seqlen);
+    const int32_t row0 = tile_of((int32_t)(blockIdx.x / a.heads), tiles, a.seqlen % kRows ? 0 : a.seqlen / kRows, a.order_q,
+                                 false) * kRows;
+    const int32_t lo = doc_of(row0, a.seg, a.seqlen).x / kRows, hi = row0 / kRows;
+    const int32_t full_from = doc_of(min(row0 + kRows, a.N) - 1, a.seg, a.seqlen).x;
     const uint32_t items = (uint32_t)(hi - lo + 1);
     if (misplaced(sm, a.err)) return;
     if (threadIdx.x == 0) bwd_init<HD>(x);
@@ -692,7 +691,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 if ((lane & 15) == 0) sD[16 * warp + 2 * it + (lane >> 4)] = d;
             }
         }
-        const int32_t start = n < a.N ? seg_start32(n, a.cu, a.n_docs, a.seqlen) : INT32_MAX;
+        const int32_t start = n < a.N ? doc_of(n, a.seg, a.seqlen).x : INT32_MAX;
         const float ls = n < a.N ? -a.lse[(int64_t)head * a.N + n] * kLog2e : 0.f;
         element_sync();
         float dl = -sD[row];

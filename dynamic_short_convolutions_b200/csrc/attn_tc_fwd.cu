@@ -52,7 +52,7 @@ __device__ __noinline__ void fwd_rows_again(const AttnTcArgs& a, int head, int32
     const float cs = a.scale * kLog2e;
     for (int r = 0; r < count; ++r) {
         const int32_t n = row0 + r;
-        const int32_t s0 = seg_start32(n, a.cu, a.n_docs, a.seqlen);
+        const int32_t s0 = doc_of(n, a.seg, a.seqlen).x;
         const float4 q = row4(a.q + (int64_t)n * a.qs + (int64_t)head * a.hd, lane, a.hd);
         float m = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -120,7 +120,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.heads, kv = head / a.group;
     const int32_t tiles = (a.N + kRows - 1) / kRows;
-    const int32_t row0 = (tiles - 1 - (int32_t)(blockIdx.x / a.heads)) * kRows;           // long rows first
+    const int32_t row0 = tile_of((int32_t)(blockIdx.x / a.heads), tiles, a.seqlen % kRows ? 0 : a.seqlen / kRows, a.order_q,
+                                 false) * kRows;
     if (threadIdx.x == 0) {
         mbar_init(&q_full, 1);
         for (int s = 0; s < S::slots; ++s) {
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
         tmem_alloc(&tmem_base, 256);
         tmem_relinquish();
     }
-    const int32_t lo = seg_start32(row0, a.cu, a.n_docs, a.seqlen) / kRows;
+    const int32_t lo = doc_of(row0, a.seg, a.seqlen).x / kRows;
     const int32_t items = row0 / kRows - lo + 1;             // tiles of keys
     tc_fence_before();
     __syncthreads();
@@ -214,8 +215,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const uint32_t tS = tb + lanes, tP = tS + kP, tO = tS + kO;
         const float cs = a.scale * kLog2e;
-        const int32_t full_from = seg_start32(min(row0 + kRows, a.N) - 1, a.cu, a.n_docs, a.seqlen);
-        const int32_t start = n < a.N ? seg_start32(n, a.cu, a.n_docs, a.seqlen) : INT32_MAX;
+        const int32_t full_from = doc_of(min(row0 + kRows, a.N) - 1, a.seg, a.seqlen).x;
+        const int32_t start = n < a.N ? doc_of(n, a.seg, a.seqlen).x : INT32_MAX;
         float m = -INFINITY, l0 = 0.f, l1 = 0.f;             // running maximum (log2 units), halves of the sum
         bool ok = true;
         uint32_t phase = 0;
