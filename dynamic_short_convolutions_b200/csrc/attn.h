@@ -5,6 +5,8 @@
 
 namespace dynconv {
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 // A validated rotary problem.
 struct RopeProb {
     int dtype;              // 0 fp32, 1 bf16

@@ -1,0 +1,401 @@
+// attn_decode_tc.cu -- a serving step over a cache on the tensor cores, for steps with many rows (drafted trees,
+// large groups; bf16): the rows of a sequence's tokens and a group's heads share every key and value read.
+//
+// A block takes 128 rows r = m * group + g of one key/value head of one sequence and one run of its cached rows, as
+// the forward of attn_tc_fwd.cu with keys and values by TMA from the cache and 512 columns of TMEM for itself: two
+// buffers of scores, P beside them, O.  The rotated q goes in as value and remainder (two products: nothing else
+// rounds it).  Rows of the last tile behind the cached ones hold whatever the cache holds there: their scores are
+// masked and their values set to zero in shared memory.  The drafted rows are one more tile, filled from k and v
+// and written to the cache by the block of the last run; infinities and NaN among their values are left out of
+// the product (0 x NaN would reach rows that do not see them) and added to the rows that see them.
+//
+// Warps: 0-3 softmax (a row per thread), q, the drafted tile; 4 issues the MMAs; 5 the TMA loads.
+#include <algorithm>
+
+#include "attn_decode.cuh"
+#include "attn_tc.cuh"
+#include "prof.h"
+#include "smem_limit.h"
+
+namespace dynconv {
+
+using namespace attn_dec;
+using namespace attn_tc;
+
+namespace {
+
+constexpr int kBlock = 192;
+
+template <int HD>
+struct DecTcSmem {
+    static constexpr uint32_t tile = kAtom * (HD / 64);
+    static constexpr int slots = HD == 128 ? 4 : 8;
+    static constexpr int ld = HD + 4;                            // a row of the result, padded
+    static constexpr uint32_t bytes = 1024 + tile * (2 + slots);
+    // the result and the join's weights use the tiles' memory
+    static_assert(kRows * ld * 4 + 2 * kRows * 64 * 4 <= tile * (2 + slots), "results fit the tiles");
+};
+
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Byte offset of 16-byte chunk c (8 channels) of row r in a tile of 64-channel atoms.
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(c / 8) * kAtom + sw128_off(r, c % 8); }
+
+template <int HD>
+__global__ void __launch_bounds__(kBlock, 1) attn_decode_tc_kernel(const __grid_constant__ CUtensorMap tk,
+                                                                   const __grid_constant__ CUtensorMap tv,
+                                                                   const __nv_bfloat16* __restrict__ q,
+                                                                   const __nv_bfloat16* __restrict__ k,
+                                                                   const __nv_bfloat16* __restrict__ v,
+                                                                   __nv_bfloat16* k_cache, __nv_bfloat16* v_cache,
+                                                                   __nv_bfloat16* __restrict__ o, const DecArgs a) {
+    using S = DecTcSmem<HD>;
+    constexpr int C = HD / 8;                                    // 16-byte chunks per row
+    constexpr uint32_t kP = 256, kO = 320;                       // TMEM columns; S at 0 and 128
+    extern __shared__ uint8_t raw[];
+    uint8_t* sQ = align1024(raw);                                // q, then its remainder
+    uint8_t* ring = sQ + 2 * S::tile;                            // place 2 i: K of tile i, 2 i + 1: its V
+    __shared__ uint64_t q_full, full[S::slots], empty[S::slots], s_full[2], s_free[2], p_ready, pv_done, drained;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag, poison;
+    __shared__ uint64_t seen[64];
+    __shared__ const float* turn[64];
+    __shared__ float smax[kRows], ssum[kRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Place p = place_of<kRows>(a, kRows);
+    if (!p.idle && !look_up(a, p, seen, turn)) {
+        p.idle = true;
+        if (threadIdx.x == 0) atomicOr(a.err, kErrRopePos);
+    }
+    if (p.idle) {
+        zero_rows<__nv_bfloat16, kRows>(a, p, o);
+        return;
+    }
+    const int64_t slot = (p.b * a.kvh + p.kv) * a.max_len;       // the cache's first row
+    const int tiles = (int)((p.to - p.from + kRows - 1) / kRows), items = tiles + (p.tail ? 1 : 0);
+    if (threadIdx.x == 0) {
+        mbar_init(&q_full, 1);
+        for (int s = 0; s < S::slots; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {                            // of either buffer of scores
+            mbar_init(&s_full[b], 1);
+            mbar_init(&s_free[b], 4);
+        }
+        mbar_init(&p_ready, 4);
+        mbar_init(&pv_done, 1);
+        mbar_init(&drained, 1);
+        abort_flag = 0;
+        poison = 0;
+        fence_mbar_init();
+    }
+    if (warp == 4) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = tmem_base;
+
+    if (warp == 5) {
+        if (lane == 0) {
+            const int32_t cache = (int32_t)(p.b * a.kvh + p.kv);
+            int n = 0;
+            for (; n < 2 * tiles; ++n) {
+                const int s = n % S::slots, use = n / S::slots;
+                if (use > 0 && !mbar_wait(&empty[s], (use - 1) & 1, &abort_flag, a.err)) break;
+                mbar_arrive_expect_tx(&full[s], S::tile);
+                const int32_t row = (int32_t)p.from + (n >> 1) * kRows;
+#pragma unroll
+                for (int c = 0; c < HD / 64; ++c)
+                    tma_load_3d(ring + s * S::tile + c * kAtom, n & 1 ? &tv : &tk, &full[s], 64 * c, row, cache);
+            }
+            if (*(volatile int*)&abort_flag)                     // no copy may land after the block has gone
+                for (int m = n > S::slots ? n - S::slots : 0; m < n; ++m)
+                    mbar_wait_drain(&full[m % S::slots], (m / S::slots) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 4) {
+        constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
+        constexpr uint32_t kIdO = idesc_bf16(128, HD, false, true);
+        const uint32_t q_at = smem_u32(sQ), r_at = smem_u32(ring);
+        const bool lead = elect_one();
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool got = mbar_wait(bar, parity, &abort_flag, a.err);
+            tc_fence_after();
+            return got;
+        };
+        auto scores = [&](int i) {
+            const int n = 2 * i, s = n % S::slots;
+            if (!wait(&full[s], (n / S::slots) & 1)) return false;
+            if (lead) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+                    if (part == 0 || a.rot)
+#pragma unroll
+                        for (int c = 0; c < HD / 16; ++c)
+                            umma_bf16(tb + 128 * (i & 1), kmajor_desc(q_at + part * S::tile + (c / 4) * kAtom, c % 4),
+                                      kmajor_desc(r_at + s * S::tile + (c / 4) * kAtom, c % 4), kIdS, part + c != 0);
+                umma_commit(&s_full[i & 1]);
+                umma_commit(&empty[s]);
+            }
+            return true;
+        };
+        bool ok = items == 0 || (wait(&q_full, 0) && scores(0));
+        for (int i = 0; ok && i < items; ++i) {
+            const int n = 2 * i + 1, s = n % S::slots;
+            // the buffer of the next scores was read two tiles ago
+            if (i + 1 < items) ok = (i == 0 || wait(&s_free[(i - 1) & 1], ((i - 1) >> 1) & 1)) && scores(i + 1);
+            ok = ok && wait(&full[s], (n / S::slots) & 1) && wait(&p_ready, i & 1);
+            if (ok && lead) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    umma_ts_bf16(tb + kO, tb + kP + 8 * c, mnmajor_desc(r_at + s * S::tile, kAtom, 16 * c), kIdO,
+                                 i > 0 || c > 0);
+                umma_commit(&pv_done);
+                umma_commit(&empty[s]);
+            }
+            __syncwarp();
+        }
+        if (lead) umma_commit(&drained);                         // every MMA done before TMEM is freed
+        mbar_wait_drain(&drained, 0);
+    } else {
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = mbar_wait(bar, parity, &abort_flag, a.err);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc_fence_after();
+            return ok;
+        };
+        auto signal = [&](uint64_t* bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        const int r = threadIdx.x, row = p.tile * kRows + r;     // this thread's row
+        const int token = row < a.rows ? row / a.group : -1;
+        // ---- q
+#pragma unroll 4
+        for (int i = threadIdx.x; i < kRows * C; i += kThreads) {
+            const int t = i / C, c = i % C, at = p.tile * kRows + t;
+            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (at < a.rows && c * 8 < a.hd) {
+                const int m = at / a.group, g = at - m * a.group;
+                turned(q + (p.b * a.M + m) * a.qs + ((int64_t)p.kv * a.group + g) * a.hd, c * 8, turn[m], a.rot, a.half, x);
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                hi[e] = pack_bf16(x[2 * e], x[2 * e + 1]);
+                lo[e] = pack_bf16(x[2 * e] - bf16_lo(hi[e]), x[2 * e + 1] - bf16_hi(hi[e]));
+            }
+            *reinterpret_cast<uint4*>(sQ + chunk_at(t, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (a.rot) *reinterpret_cast<uint4*>(sQ + S::tile + chunk_at(t, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_async_smem();
+        rows_sync();
+        if (threadIdx.x == 0) mbar_arrive(&q_full);
+        // ---- the drafted tile
+        auto draft = [&]() {
+            const int n = 2 * tiles;
+            uint8_t* kt = ring + n % S::slots * S::tile;
+            uint8_t* vt = ring + (n + 1) % S::slots * S::tile;
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+                if (n + w >= S::slots && !wait(&empty[(n + w) % S::slots], ((n + w) / S::slots - 1) & 1)) return false;
+            bool bad = false;
+#pragma unroll 2
+            for (int i = threadIdx.x; i < kRows * C; i += kThreads) {
+                const int t = i / C, c = i % C;
+                uint4 x = make_uint4(0, 0, 0, 0), y = x;
+                if (t < a.M && c * 8 < a.hd) {
+                    float f[8];
+                    turned(k + (p.b * a.M + t) * a.ks + (int64_t)p.kv * a.hd, c * 8, turn[t], a.rot, a.half, f);
+                    x = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+                    y = __ldg(reinterpret_cast<const uint4*>(v + (p.b * a.M + t) * a.vs + (int64_t)p.kv * a.hd + c * 8));
+                    if (p.tile == 0) {
+                        *reinterpret_cast<uint4*>(k_cache + (slot + p.len + t) * a.hd + c * 8) = x;
+                        *reinterpret_cast<uint4*>(v_cache + (slot + p.len + t) * a.hd + c * 8) = y;
+                    }
+                    uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t odd = nonfinite_bits(w[e]);
+                        bad = bad || odd;
+                        w[e] &= ~((odd & 0x8000u ? 0xFFFFu : 0u) | (odd & 0x80000000u ? 0xFFFF0000u : 0u));
+                    }
+                }
+                *reinterpret_cast<uint4*>(kt + chunk_at(t, c)) = x;
+                *reinterpret_cast<uint4*>(vt + chunk_at(t, c)) = y;
+            }
+            if (bad) poison = 1;
+            fence_async_smem();
+            rows_sync();
+            if (threadIdx.x == 0) {
+                mbar_arrive(&full[n % S::slots]);
+                mbar_arrive(&full[(n + 1) % S::slots]);
+            }
+            return true;
+        };
+        // ---- softmax
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const uint32_t tP = tb + lanes + kP, tO = tb + lanes + kO;
+        const float cs = a.scale * kLog2e;
+        float m = -INFINITY, l0 = 0.f, l1 = 0.f;                 // running maximum (log2 units), halves of the sum
+        bool met = false;                                        // the drafted tile's barrier
+        for (int i = 0; i < items; ++i) {
+            const uint32_t tS = tb + lanes + 128 * (i & 1);
+            const int64_t left = i < tiles ? p.to - p.from - (int64_t)i * kRows : 0;       // cached rows of the tile
+            uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+            if (i == tiles) {
+                if (!draft()) break;
+                met = true;
+                const uint64_t s = token >= 0 ? seen[token] : 0;
+                bits[0] = (uint32_t)s;
+                bits[1] = (uint32_t)(s >> 32);
+                bits[2] = bits[3] = 0;
+            } else if (left < kRows) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) bits[b] = seen_bits(32 * b, 0, (int)left - 1);
+            }
+            if (!wait(&s_full[i & 1], (i >> 1) & 1)) break;
+            float s0[32], s1[32], mx[4];
+            tmem_ld32(tS + 64, s0);
+            tmem_ld32(tS + 96, s1);
+            tmem_wait_ld();
+            hide32(s0, bits[2], -INFINITY);
+            hide32(s1, bits[3], -INFINITY);
+            mx[0] = max32(s0);
+            mx[1] = max32(s1);
+            tmem_ld32(tS, s0);
+            tmem_ld32(tS + 32, s1);
+            tmem_wait_ld();
+            hide32(s0, bits[0], -INFINITY);
+            hide32(s1, bits[1], -INFINITY);
+            mx[2] = max32(s0);
+            mx[3] = max32(s1);
+            const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cs);
+            if (i > 0 && !wait(&pv_done, (i - 1) & 1)) break;
+            if (__any_sync(0xFFFFFFFFu, top - m > kGrow)) {
+                if (i > 0) {
+                    const float c = top == -INFINITY ? 1.f : ex2(m - top);
+                    l0 *= c;
+                    l1 *= c;
+#pragma unroll 1
+                    for (int b = 0; b < HD / 32; ++b) {
+                        float f[32];
+                        tmem_ld32(tO + 32 * b, f);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) mul2(f[e], f[e + 1], c);
+                        tmem_st32(tO + 32 * b, f);
+                    }
+                }
+                m = top;
+            }
+            const float neg = m == -INFINITY ? 0.f : -m;         // a row that has seen no key yet
+            probs32(s0, cs, neg, l0, l1, tP);
+            probs32(s1, cs, neg, l0, l1, tP + 16);
+            tmem_ld32(tS + 64, s0);
+            tmem_ld32(tS + 96, s1);
+            tmem_wait_ld();
+            signal(&s_free[i & 1]);
+            hide32(s0, bits[2], -INFINITY);
+            hide32(s1, bits[3], -INFINITY);
+            probs32(s0, cs, neg, l0, l1, tP + 32);
+            probs32(s1, cs, neg, l0, l1, tP + 48);
+            tmem_wait_st();
+            if (i < tiles && left < kRows) {
+                // values behind the cached rows: zeros
+                const int n = 2 * i + 1;
+                if (!wait(&full[n % S::slots], (n / S::slots) & 1)) break;
+                if (r >= left)
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        *reinterpret_cast<uint4*>(ring + n % S::slots * S::tile + chunk_at(r, c)) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+            }
+            signal(&p_ready);
+        }
+        if (p.tail && !met) rows_sync();                         // after an abort: the other warps may wait there
+        ok = ok && (items == 0 || wait(&pv_done, (items - 1) & 1));
+        ok = !named_bar_any<1, 128>(!ok);                        // all go on, or none: the tiles' memory is free
+        if (ok) {
+            float* so = reinterpret_cast<float*>(sQ);
+            const uint64_t bad = poison && p.tail && token >= 0 ? seen[token] : 0;
+#pragma unroll 1
+            for (int b = 0; b < HD / 32; ++b) {
+                float f[32];
+                if (items > 0) {
+                    tmem_ld32(tO + 32 * b, f);
+                    tmem_wait_ld();
+                } else {
+                    fill32(f, 0.f);
+                }
+                if (bad != 0)
+                    for (int j = 0; j < a.M; ++j)
+                        if (bad >> j & 1)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * b + e < a.hd) {
+                                    const float x = __bfloat162float(v[(p.b * a.M + j) * a.vs + (int64_t)p.kv * a.hd + 32 * b + e]);
+                                    if (!(fabsf(x) < INFINITY)) f[e] += x;
+                                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4*>(so + r * S::ld + 32 * b + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            }
+            smax[r] = m;
+            ssum[r] = l0 + l1;
+            rows_sync();
+            finish<__nv_bfloat16, HD, kRows, 1, S::ld>(a, p, so, smax, ssum, so + kRows * S::ld, o, [] { rows_sync(); });
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_dealloc(tb, 512);
+    }
+}
+
+template <int HD>
+cudaError_t launch_tc(const CUtensorMap& tk, const CUtensorMap& tv, const DecArgs& a, unsigned grid, const void* q,
+                      const void* k, const void* v, void* kc, void* vc, void* o, cudaStream_t st) {
+    using B = __nv_bfloat16;
+    constexpr uint32_t smem = DecTcSmem<HD>::bytes;
+    cudaError_t e = DC_SMEM_LIMIT(attn_decode_tc_kernel<HD>, smem);
+    if (e != cudaSuccess) return e;
+    DC_LAUNCH(kAttnDecodeTc, st, attn_decode_tc_kernel<HD><<<grid, kBlock, smem, st>>>(
+                                     tk, tv, static_cast<const B*>(q), static_cast<const B*>(k), static_cast<const B*>(v),
+                                     static_cast<B*>(kc), static_cast<B*>(vc), static_cast<B*>(o), a));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// A cache as [batch * kv_heads][max_len][hd], boxes of 128 rows x 64 channels of one head: rows from max_len on and
+// channels from hd on read zero, and no coordinate passes 32 bits however long the caches are.
+static bool make_cache_map(CUtensorMap* map, const void* base, const DecodeProb& p) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)p.hd, (cuuint64_t)p.max_len, (cuuint64_t)(p.batch * p.kvh)};
+    cuuint64_t strides[2] = {(cuuint64_t)p.hd * 2, (cuuint64_t)p.hd * 2 * p.max_len};
+    cuuint32_t box[3] = {64, kRows, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t attn_decode_tc(const DecodeProb& p, const DecArgs& a, unsigned grid, const void* q, const void* k,
+                           const void* v, void* k_cache, void* v_cache, void* o, cudaStream_t st) {
+    CUtensorMap tk, tv;
+    if (!make_cache_map(&tk, k_cache, p) || !make_cache_map(&tv, v_cache, p))
+        return cudaErrorInvalidValue;
+    return p.hd <= 64 ? launch_tc<64>(tk, tv, a, grid, q, k, v, k_cache, v_cache, o, st)
+                      : launch_tc<128>(tk, tv, a, grid, q, k, v, k_cache, v_cache, o, st);
+}
+
+}  // namespace dynconv

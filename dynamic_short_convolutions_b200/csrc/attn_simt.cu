@@ -34,8 +34,6 @@ namespace cg = cooperative_groups;
 constexpr int kTile = kSimtTile;
 constexpr int kThreads = 256;
 constexpr int kLdP = kTile + 4;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <int HD>
 constexpr int ld_of() { return HD + 4; }

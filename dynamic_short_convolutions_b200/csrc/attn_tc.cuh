@@ -15,8 +15,6 @@ using namespace tc;
 
 constexpr int kRows = kTcTile;                   // 128 tokens per tile: the lanes of TMEM
 constexpr uint32_t kAtom = kRows * 128;          // bytes of a 128-token x 64-channel tile
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- tensor maps
 // [N tokens][heads][hd] bf16, a box of 128 tokens x one head x 64 channels; channels from hd on and tokens
@@ -185,6 +183,39 @@ __device__ __forceinline__ void hide32(float (&s)[32], uint32_t bits, float x) {
 #pragma unroll
     for (int e = 0; e < 32; ++e) s[e] = bits >> e & 1 ? s[e] : x;
 }
+
+// ---------------------------------------------------------------- softmax of a row
+constexpr float kGrow = 8.f;                     // log2 growth of the maximum that makes a row rescale
+__device__ __forceinline__ float max32(const float (&s)[32]) {
+    float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
+#pragma unroll
+    for (int e = 4; e < 32; e += 4) {
+        a = fmaxf(fmaxf(a, s[e]), s[e + 1]);
+        b = fmaxf(fmaxf(b, s[e + 2]), s[e + 3]);
+    }
+    return fmaxf(a, b);
+}
+// 32 probabilities 2^(s f + g): summed (even and odd columns apart), rounded to bf16 and stored to 16 columns of TMEM
+__device__ __forceinline__ void probs32(float (&s)[32], float f, float g, float& l0, float& l1, uint32_t to) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        fma2(s[e], s[e + 1], f, g);
+        s[e] = ex2(s[e]);
+        s[e + 1] = ex2(s[e + 1]);
+        add2(l0, l1, s[e], s[e + 1]);
+        w[e / 2] = pack_bf16(s[e], s[e + 1]);
+    }
+    tmem_st16(to, w);
+}
+
+__device__ __forceinline__ void zeros16(uint32_t to) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) w[e] = 0;
+    tmem_st16(to, w);
+}
+
 
 // ---------------------------------------------------------------- infinities and NaN
 // Whether a word of two bf16 holds an infinity or a NaN (an exponent of ones): bit 7 of either half of

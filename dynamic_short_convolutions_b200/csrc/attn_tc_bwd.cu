@@ -67,7 +67,7 @@ struct BwdSmem {
     static_assert(2 * kRows * part_ld * sizeof(float) <= stats, "partial gradients fit the tiles");
     struct Shared {
         uint64_t resident, full[slots], empty[slots], stat_full[2], stat_free[2];
-        uint64_t s_full, s_free, dp_full, dp_free, p_ready, ds_ready, done, scanned;
+        uint64_t s_full, s_free, dp_full, dp_free, p_ready, ds_ready[2], done, scanned;
         uint32_t tmem_base;
         int abort_flag, again;
     };
@@ -97,7 +97,8 @@ __device__ __forceinline__ void bwd_init(typename BwdSmem<HD>::Shared& x) {
     mbar_init(&x.dp_full, 1);
     mbar_init(&x.dp_free, 8);
     mbar_init(&x.p_ready, 8);
-    mbar_init(&x.ds_ready, 8);
+    mbar_init(&x.ds_ready[0], 8);
+    mbar_init(&x.ds_ready[1], 8);
     mbar_init(&x.done, 1);
     mbar_init(&x.scanned, 1);
     x.abort_flag = 0;
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 grad(kDV, kDP, r_at + d.slot * S::tile, i > 0);
                 if (lead) umma_commit(&x.empty[d.slot]);
             }
-            ok = ok && wait(&x.ds_ready, phase);
+            ok = ok && wait(&x.ds_ready[0], phase);
             if (ok) {
                 grad(kDK, kDP + 32, r_at + q.slot * S::tile, i > 0);
                 // the diagonal tile's remainders lie in the columns of S: the next scores come after them
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 }
             }
             tmem_wait_st();
-            signal(&x.ds_ready);
+            signal(&x.ds_ready[0]);
             if (lane == 0) mbar_arrive(&x.stat_free[i & 1]);
             return true;
         };
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tb = x.tmem_base;
-    constexpr uint32_t kDP = 128, kDQ = 256, kDS = 384;      // dS: two buffers of 64 columns
+    constexpr uint32_t kDP = 128, kDQ = 256, kDS = 384;      // dS: two buffers of 64 columns, a barrier each
 
     if (warp == 9) {
         if (lane == 0) {
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                     if (lead) umma_commit(&x.empty[v1.slot]);
                 }
             }
-            ok = ok && wait(&x.ds_ready, phase);
+            ok = ok && wait(&x.ds_ready[i & 1], (i >> 1) & 1);
             if (ok && lead) {
                 const uint32_t at = r_at + k.slot * S::tile;
 #pragma unroll
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 }
             }
             tmem_wait_st();
-            signal(&x.ds_ready);
+            signal(&x.ds_ready[i & 1]);
             return true;
         };
         for (uint32_t i = 0; i < items; ++i, phase ^= 1) {

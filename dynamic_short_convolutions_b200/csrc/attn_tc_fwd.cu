@@ -34,7 +34,6 @@ namespace {
 constexpr int kFwdThreads = 192;
 // The softmax warps' barrier.
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-constexpr float kGrow = 8.f;                     // log2 growth of the maximum that makes a row rescale
 
 template <int HD>
 struct FwdSmem {
@@ -70,36 +69,6 @@ __device__ __noinline__ void fwd_rows_again(const AttnTcArgs& a, int head, int32
              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
         if (a.lse != nullptr && lane == 0) a.lse[(int64_t)head * a.N + n] = (m + log2f(l)) * kLn2;
     }
-}
-
-__device__ __forceinline__ float max32(const float (&s)[32]) {
-    float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
-#pragma unroll
-    for (int e = 4; e < 32; e += 4) {
-        a = fmaxf(fmaxf(a, s[e]), s[e + 1]);
-        b = fmaxf(fmaxf(b, s[e + 2]), s[e + 3]);
-    }
-    return fmaxf(a, b);
-}
-// 32 probabilities 2^(s f + g): summed (even and odd columns apart), rounded to bf16 and stored to 16 columns of TMEM
-__device__ __forceinline__ void probs32(float (&s)[32], float f, float g, float& l0, float& l1, uint32_t to) {
-    uint32_t w[16];
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-        fma2(s[e], s[e + 1], f, g);
-        s[e] = ex2(s[e]);
-        s[e + 1] = ex2(s[e + 1]);
-        add2(l0, l1, s[e], s[e + 1]);
-        w[e / 2] = pack_bf16(s[e], s[e + 1]);
-    }
-    tmem_st16(to, w);
-}
-
-__device__ __forceinline__ void zeros16(uint32_t to) {
-    uint32_t w[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = 0;
-    tmem_st16(to, w);
 }
 
 template <int HD>

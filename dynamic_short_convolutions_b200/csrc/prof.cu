@@ -32,7 +32,7 @@ const char* kNames[kKernelCount] = {
     "check_seqlens", "tc_gen", "tc_lowrank_fwd", "tc_lowrank_bwd", "tc_gen_bwd", "tc_reduce",
     "tc_headwise_fwd", "tc_headwise_bwd", "tc_prep", "decode_gen", "decode_conv", "simt_rope",
     "rope", "attn_prep", "attn_simt_fwd", "attn_simt_dkv", "attn_simt_dq", "attn_delta", "attn_tc_fwd", "attn_tc_dkv", "attn_tc_dq",
-    "attn_decode",
+    "attn_decode", "attn_decode_tc",
 };
 
 cudaEvent_t take_event() {

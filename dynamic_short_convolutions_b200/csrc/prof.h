@@ -9,7 +9,7 @@ enum KernelId {
     kSimtGen = 0, kSimtWiden, kSimtConvFwd, kSimtConvBwd, kSimtDB, kSimtHTX, kSimtDh,
     kCheckSeqlens, kTcGen, kTcLowrankFwd, kTcLowrankBwd, kTcGenBwd, kTcReduce,
     kTcHeadwiseFwd, kTcHeadwiseBwd, kTcPrep, kDecodeGen, kDecodeConv, kSimtRope,
-    kRope, kAttnPrep, kAttnSimtFwd, kAttnSimtDkv, kAttnSimtDq, kAttnDelta, kAttnTcFwd, kAttnTcDkv, kAttnTcDq, kAttnDecode,
+    kRope, kAttnPrep, kAttnSimtFwd, kAttnSimtDkv, kAttnSimtDq, kAttnDelta, kAttnTcFwd, kAttnTcDkv, kAttnTcDq, kAttnDecode, kAttnDecodeTc,
     kKernelCount
 };
 

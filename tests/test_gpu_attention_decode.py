@@ -89,6 +89,8 @@ CASES = [  # lens, tokens, heads, kv_heads, head_dim, max_len, rotated
     ([31, 32, 33], 17, 3, 3, 96, 64, 6),
     ([2000, 1999], 5, 5, 1, 128, 2048, 128),
     ([700], 33, 2, 2, 8, 800, 0),
+    ([128, 256, 255, 129, 0], 12, 16, 4, 64, 300, 32),
+    ([3000, 2049], 60, 16, 2, 128, 3100, 128),
 ]
 
 
@@ -121,9 +123,10 @@ def test_idle_slots_and_rows_that_see_nothing(dtype):
     assert (o[6] == 0).all()                                     # no cached row either
 
 
+@pytest.mark.parametrize("heads", [2, 8, 16])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_stale_and_masked_rows_may_hold_anything(dtype):
-    lens, tokens, heads, kv, hd = [100, 7], 8, 8, 2, 128
+def test_stale_and_masked_rows_may_hold_anything(dtype, heads):
+    lens, tokens, kv, hd = [100, 7], 8, 2, 128
     trees = [[1 << m for m in range(8)], [1, 3, 7, 9, 16, 48, 64, 193]]
     dec, q, k, v, table = _setup(dtype, lens, tokens, heads, kv, hd, 300, 128, True, seed=4)
     for b, n in enumerate(lens):
