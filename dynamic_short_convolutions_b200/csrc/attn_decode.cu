@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __nv_bfloat
             *reinterpret_cast<float2*>(so + r * HD + 8 * n + 2 * (lane & 3)) = make_float2(acc[n][2 * h], acc[n][2 * h + 1]);
     }
     __syncthreads();
-    finish<__nv_bfloat16, HD, ROWS, TW, HD>(a, p, so, smax, ssum, so + TW * ROWS * HD, o, [] { __syncthreads(); });
+    finish<__nv_bfloat16, HD, ROWS, TW>(a, p, so, smax, ssum, so + TW * ROWS * HD, o);
 }
 
 // ---------------------------------------------------------------- fp32
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
         for (int e = 0; e < E; ++e) so[(4 * warp + r) * HD + lane * E + e] = acc[r][e];
     }
     __syncthreads();
-    finish<float, HD, kRowsF, 1, HD>(a, p, so, smax, ssum, so + kRowsF * HD, o, [] { __syncthreads(); });
+    finish<float, HD, kRowsF, 1>(a, p, so, smax, ssum, so + kRowsF * HD, o);
 }
 
 // Rows a block takes: 16 or 32 where they are all there are (its warps then share out the tokens), else the 128 of
@@ -506,18 +506,23 @@ int64_t attn_decode_groups(const DecodeProb& p) {
 }
 
 // Runs the cache is split into: as many as keep all blocks on the GPU at once (two per SM; one of the tcgen05
-// kernel), but no run of a full cache below four tiles (two).  Measured: one sequence of 12 heads over ~1200 rows
+// kernel, whose runs are the blocks of a cluster: 1, 2, 4 or 8), but no run of a full cache below four tiles
+// (two).  Measured: one sequence of 12 heads over ~1200 rows
 // takes 8.7 us with runs of at least 256 rows, 9.3 with 128; 64 sequences do not care (88 us with 1 to 3 runs).
 int attn_decode_splits(const DecodeProb& p) {
     const int64_t groups = std::max<int64_t>(1, attn_decode_groups(p));
     const bool tc = tile_rows(p) == kTcTile;
     const int64_t shortest = tc ? 2 * kTcTile : 4 * (p.dtype == 0 ? kTokF : kTok);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({(tc ? 148 : 2 * 148) / groups, (p.max_len + shortest - 1) / shortest, 64}));
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>({(tc ? 148 : 2 * 148) / groups, (p.max_len + shortest - 1) / shortest, 64}));
+    if (!tc) return (int)most;
+    int ranks = 1;
+    while (ranks < 8 && ranks * 2 <= most) ranks *= 2;
+    return ranks;
 }
 
 size_t attn_decode_part_bytes(const DecodeProb& p) {
     const int n = attn_decode_splits(p), hd = p.hd <= 64 ? 64 : 128;
-    return n == 1 ? 0 : (size_t)attn_decode_groups(p) * n * tile_rows(p) * (hd + 2) * sizeof(float);
+    return n == 1 || tile_rows(p) == kTcTile ? 0 : (size_t)attn_decode_groups(p) * n * tile_rows(p) * (hd + 2) * sizeof(float);
 }
 
 cudaError_t attn_decode(const DecodeProb& p, const void* q, const void* k, const void* v, void* kc, void* vc,

@@ -10,7 +10,7 @@
 namespace dynconv {
 namespace attn_dec {
 
-constexpr int kThreads = 128;              // that work on rows and tiles
+constexpr int kThreads = 128;
 
 struct DecArgs {
     int M, heads, kvh, group, hd, rows, n_split;     // rows = M * group
@@ -94,6 +94,39 @@ __device__ __forceinline__ void turned(const T* x, int c, const float* f, int ro
     }
 }
 
+// Rows of bf16 heads, rotated, 16 bytes at a time and both halves of a pair together where the half layout allows:
+// a unit u of a row is chunk u, or, where paired, chunks u and u + rot / 16.  put(chunk, values) takes each.
+__device__ __forceinline__ bool paired(const DecArgs& a) { return a.rot > 0 && a.half && (a.rot / 2) % 8 == 0; }
+__device__ __forceinline__ int units_of(const DecArgs& a, int chunks) { return paired(a) ? chunks - a.rot / 16 : chunks; }
+template <typename Put>
+__device__ __forceinline__ void turn_unit(const DecArgs& a, const __nv_bfloat16* x, int u, const float* f, Put put) {
+    const int hc = a.rot / 16;                                   // chunks of half of the rotated channels
+    if (!paired(a) || u >= hc) {
+        float v[8];
+        const int c = paired(a) ? u + hc : u;
+        turned(x, c * 8, f, a.rot, a.half, v);
+        put(c, v);
+        return;
+    }
+    const uint4 l = __ldg(reinterpret_cast<const uint4*>(x + u * 8)), r = __ldg(reinterpret_cast<const uint4*>(x + (u + hc) * 8));
+    float4 z[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = __ldg(reinterpret_cast<const float4*>(f + u * 16) + e);
+    const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, rw[4] = {r.x, r.y, r.z, r.w};
+    float lo[8], hi[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float a0 = __uint_as_float(lw[e] << 16), a1 = __uint_as_float(lw[e] & 0xFFFF0000u);
+        const float b0 = __uint_as_float(rw[e] << 16), b1 = __uint_as_float(rw[e] & 0xFFFF0000u);
+        lo[2 * e] = a0 * z[e].x - b0 * z[e].y;
+        hi[2 * e] = a0 * z[e].y + b0 * z[e].x;
+        lo[2 * e + 1] = a1 * z[e].z - b1 * z[e].w;
+        hi[2 * e + 1] = a1 * z[e].w + b1 * z[e].z;
+    }
+    put(u, lo);
+    put(u + hc, hi);
+}
+
 // What a block works on.
 struct Place {
     int64_t b;
@@ -139,15 +172,14 @@ __device__ __forceinline__ bool look_up(const DecArgs& a, const Place& p, uint64
     return __syncthreads_and(ok) != 0;
 }
 
-// Joins NP partial results of ROWS rows in shared memory (so [NP][ROWS], rows LD floats apart, not yet divided by
-// the sum, smax and ssum [NP][ROWS]) and either writes o or leaves this run's part and, as the last block of its rows, joins the
+// Joins NP partial results of ROWS rows in shared memory (so [NP][ROWS][HD] not yet divided by the sum, smax and
+// ssum [NP][ROWS]) and either writes o or leaves this run's part and, as the last block of its rows, joins the
 // runs.  The loads of a join are independent of one another (weights first, then 16 values in flight per
 // thread and more): a load and its use in turn, run by run, took longer than the attention itself.
-// `weights`: shared memory for 2 x ROWS x n_split floats (n_split <= 64); `sync`: the barrier of the kThreads threads
-// that call this.
-template <typename T, int HD, int ROWS, int NP, int LD, typename Sync>
+// `weights`: shared memory for 2 x ROWS x n_split floats (n_split <= 64).
+template <typename T, int HD, int ROWS, int NP>
 __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const float* so, const float* smax,
-                                       const float* ssum, float* weights, T* __restrict__ o, Sync sync) {
+                                       const float* ssum, float* weights, T* __restrict__ o) {
     __shared__ int last;
     __shared__ float inverse[ROWS];
     constexpr int kItems = ROWS * HD / 4 / kThreads;             // runs of four channels per thread
@@ -165,7 +197,7 @@ __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const f
             *reinterpret_cast<uint2*>(to) = make_uint2(pack2(s.x * inv, s.y * inv), pack2(s.z * inv, s.w * inv));
         }
     };
-#pragma unroll (kItems < 8 ? kItems : 8)
+#pragma unroll
     for (int it = 0; it < kItems; ++it) {
         const int i = threadIdx.x + it * kThreads, r = i / (HD / 4), c = (i % (HD / 4)) * 4;
         if (r >= rows) break;
@@ -177,7 +209,7 @@ __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const f
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
             const float w = exp2f(smax[n * ROWS + r] - use);
-            const float4 x = *reinterpret_cast<const float4*>(so + (n * ROWS + r) * LD + c);
+            const float4 x = *reinterpret_cast<const float4*>(so + (n * ROWS + r) * HD + c);
             s.x += w * x.x; s.y += w * x.y; s.z += w * x.z; s.w += w * x.w;
             l += w * ssum[n * ROWS + r];
         }
@@ -190,14 +222,14 @@ __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const f
     }
     if (a.n_split == 1) return;
     __threadfence();
-    sync();
+    __syncthreads();
     if (threadIdx.x == 0) {
         const uint32_t done = atomicAdd(a.count + group, 1u);
         last = done == (uint32_t)a.n_split - 1;
         if (last) a.count[group] = 0;            // ready for the next call
         __threadfence();
     }
-    sync();
+    __syncthreads();
     if (!last) return;
     float* sums = weights + ROWS * a.n_split;
     for (int i = threadIdx.x; i < a.n_split * rows; i += kThreads) {
@@ -206,7 +238,7 @@ __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const f
         weights[r * a.n_split + n] = x.x;
         sums[r * a.n_split + n] = x.y;
     }
-    sync();
+    __syncthreads();
     if (threadIdx.x < rows) {
         float* w = weights + threadIdx.x * a.n_split;
         const float* l = sums + threadIdx.x * a.n_split;
@@ -219,33 +251,30 @@ __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const f
         }
         inverse[threadIdx.x] = sum > 0.f ? 1.f / sum : sum;
     }
-    sync();
-    constexpr int kStep = kItems < 8 ? kItems : 8;               // runs of channels at a time
-    for (int first = 0; first < kItems; first += kStep) {
-        float4 s[kStep];
+    __syncthreads();
+    float4 s[kItems];
 #pragma unroll
-        for (int it = 0; it < kStep; ++it) s[it] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll (kStep >= 8 ? 2 : 16 / kStep)
-        for (int n = 0; n < a.n_split; ++n) {
-            float4 x[kStep];
+    for (int it = 0; it < kItems; ++it) s[it] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll (kItems >= 8 ? 2 : 16 / kItems)
+    for (int n = 0; n < a.n_split; ++n) {
+        float4 x[kItems];
 #pragma unroll
-            for (int it = 0; it < kStep; ++it) {
-                const int i = threadIdx.x + (first + it) * kThreads, r = i / (HD / 4), c = (i % (HD / 4)) * 4;
-                x[it] = r < rows ? __ldcg(reinterpret_cast<const float4*>(parts + ((int64_t)n * ROWS + r) * HD + c))
-                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int it = 0; it < kStep; ++it) {
-                const int r = (threadIdx.x + (first + it) * kThreads) / (HD / 4);
-                const float w = r < rows ? weights[r * a.n_split + n] : 0.f;
-                s[it].x += w * x[it].x; s[it].y += w * x[it].y; s[it].z += w * x[it].z; s[it].w += w * x[it].w;
-            }
+        for (int it = 0; it < kItems; ++it) {
+            const int i = threadIdx.x + it * kThreads, r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+            x[it] = r < rows ? __ldcg(reinterpret_cast<const float4*>(parts + ((int64_t)n * ROWS + r) * HD + c))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int it = 0; it < kStep; ++it) {
-            const int i = threadIdx.x + (first + it) * kThreads, r = i / (HD / 4), c = (i % (HD / 4)) * 4;
-            if (r < rows && c < a.hd) put(r, c, s[it], inverse[r]);
+        for (int it = 0; it < kItems; ++it) {
+            const int r = (threadIdx.x + it * kThreads) / (HD / 4);
+            const float w = r < rows ? weights[r * a.n_split + n] : 0.f;
+            s[it].x += w * x[it].x; s[it].y += w * x[it].y; s[it].z += w * x[it].z; s[it].w += w * x[it].w;
         }
+    }
+#pragma unroll
+    for (int it = 0; it < kItems; ++it) {
+        const int i = threadIdx.x + it * kThreads, r = i / (HD / 4), c = (i % (HD / 4)) * 4;
+        if (r < rows && c < a.hd) put(r, c, s[it], inverse[r]);
     }
 }
 

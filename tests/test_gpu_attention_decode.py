@@ -91,6 +91,7 @@ CASES = [  # lens, tokens, heads, kv_heads, head_dim, max_len, rotated
     ([700], 33, 2, 2, 8, 800, 0),
     ([128, 256, 255, 129, 0], 12, 16, 4, 64, 300, 32),
     ([3000, 2049], 60, 16, 2, 128, 3100, 128),
+    ([1500, 1499, 1281] * 13, 9, 16, 4, 64, 1600, 64),          # a run of many tiles, then the drafted one
 ]
 
 
