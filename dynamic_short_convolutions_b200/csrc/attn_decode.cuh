@@ -5,6 +5,7 @@
 #include <algorithm>
 
 #include "attn.h"
+#include "attn_tc.cuh"
 #include "common.cuh"
 
 namespace dynconv {
@@ -127,6 +128,20 @@ __device__ __forceinline__ void turn_unit(const DecArgs& a, const __nv_bfloat16*
     put(u + hc, hi);
 }
 
+// A bf16 cache as [batch * kv_heads][max_len][hd], boxes of `rows` rows x 64 channels of one head: rows from max_len
+// on and channels from hd on read zero, and no coordinate passes 32 bits however long the caches are.
+inline bool make_cache_map(CUtensorMap* map, const void* base, const DecodeProb& p, uint32_t rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)p.hd, (cuuint64_t)p.max_len, (cuuint64_t)(p.batch * p.kvh)};
+    cuuint64_t strides[2] = {(cuuint64_t)p.hd * 2, (cuuint64_t)p.hd * 2 * p.max_len};
+    cuuint32_t box[3] = {64, rows, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // What a block works on.
 struct Place {
     int64_t b;
@@ -183,6 +198,7 @@ __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const f
     __shared__ int last;
     __shared__ float inverse[ROWS];
     constexpr int kItems = ROWS * HD / 4 / kThreads;             // runs of four channels per thread
+    static_assert(kItems >= 1, "a thread has work");
     const int tiles = (a.rows + ROWS - 1) / ROWS;
     const int64_t group = (p.b * a.kvh + p.kv) * tiles + p.tile;
     const int rows = min(ROWS, a.rows - p.tile * ROWS);

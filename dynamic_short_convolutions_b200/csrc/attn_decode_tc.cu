@@ -443,24 +443,10 @@ cudaError_t launch_tc(const CUtensorMap& tk, const CUtensorMap& tv, const DecArg
 
 }  // namespace
 
-// A cache as [batch * kv_heads][max_len][hd], boxes of 128 rows x 64 channels of one head: rows from max_len on and
-// channels from hd on read zero, and no coordinate passes 32 bits however long the caches are.
-static bool make_cache_map(CUtensorMap* map, const void* base, const DecodeProb& p) {
-    auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)p.hd, (cuuint64_t)p.max_len, (cuuint64_t)(p.batch * p.kvh)};
-    cuuint64_t strides[2] = {(cuuint64_t)p.hd * 2, (cuuint64_t)p.hd * 2 * p.max_len};
-    cuuint32_t box[3] = {64, kRows, 1};
-    cuuint32_t es[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 cudaError_t attn_decode_tc(const DecodeProb& p, const DecArgs& a, unsigned grid, const void* q, const void* k,
                            const void* v, void* k_cache, void* v_cache, void* o, cudaStream_t st) {
     CUtensorMap tk, tv;
-    if (!make_cache_map(&tk, k_cache, p) || !make_cache_map(&tv, v_cache, p))
+    if (!make_cache_map(&tk, k_cache, p, kRows) || !make_cache_map(&tv, v_cache, p, kRows))
         return cudaErrorInvalidValue;
     return p.hd <= 64 ? launch_tc<64>(tk, tv, a, grid, q, k, v, k_cache, v_cache, o, st)
                       : launch_tc<128>(tk, tv, a, grid, q, k, v, k_cache, v_cache, o, st);

@@ -5,7 +5,7 @@
 // caller's fp32 table, so that any context scaling is a matter of that table.  The products and
 // their sum are in fp32, rounded once to the storage type.
 //
-// Memory-bound: x is read and y written once.  A block takes one token (its position and table
+// Memory-bound: x is read and y written once (82 to 88 % of the copy rate).  A block takes one token (its position and table
 // row once, the row staying in L1 for every head), a thread one unit of 16 bytes of a head -- for
 // the half layout the two 16-byte runs that pair up -- so loads and stores are 16 bytes wide
 // where sizes and strides allow it; otherwise a unit is one pair (or one copied channel).
@@ -36,6 +36,7 @@ struct RopeArgs {
 template <typename T, int V, bool HALF>
 __global__ void __launch_bounds__(256) rope_heads_kernel(const T* x, T* y, RopeArgs a) {
     constexpr int kSpan = HALF ? V : (V == 1 ? 2 : V);       // channels of the rotated half / run per unit
+    constexpr int kPairs = HALF ? V : (V == 1 ? 1 : V / 2);  // pairs per unit
     const int64_t n = blockIdx.x;
     int64_t p;
     if (a.pos != nullptr)
@@ -55,43 +56,33 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const T* x, T* y, RopeA
     T* yr = y + n * a.ys;
     for (int u = threadIdx.x; u < total; u += blockDim.x) {
         const int h = u / units, w = u - h * units;
-        const T* xh = xr + (int64_t)h * a.hd;
-        T* yh = yr + (int64_t)h * a.hd;
-        if (w >= turned) {
-            const int c = a.rot + (w - turned) * V;
-            *reinterpret_cast<Vec<T, V>*>(yh + c) = *reinterpret_cast<const Vec<T, V>*>(xh + c);
-        } else if (HALF) {
-            const int c = w * V, o = a.rot / 2;
-            const Vec<T, V> l = *reinterpret_cast<const Vec<T, V>*>(xh + c);
-            const Vec<T, V> r = *reinterpret_cast<const Vec<T, V>*>(xh + c + o);
-            Vec<T, V> lo, hi;
+        const int at = h * a.hd + (w >= turned ? a.rot + (w - turned) * V : w * kSpan);
+        Vec<T, V> l = *reinterpret_cast<const Vec<T, V>*>(xr + at), r;
+        if (w < turned) {
+            if (HALF) r = *reinterpret_cast<const Vec<T, V>*>(xr + at + a.rot / 2);
+            else if (V == 1) r = *reinterpret_cast<const Vec<T, V>*>(xr + at + 1);
+            // the factors: two pairs a load (a load's lanes are a run apart, so its width sets the L1 traffic)
+            const float* z = row + (HALF ? 2 * w * V : w * kSpan);
+            float f[2 * kPairs];
+            if (kPairs >= 2) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float2 f = __ldg(reinterpret_cast<const float2*>(row + 2 * (c + e)));
-                const float p0 = to_f32(l.v[e]), p1 = to_f32(r.v[e]), s = sgn * f.y;
-                lo.v[e] = from_f32<T>(p0 * f.x - p1 * s);
-                hi.v[e] = from_f32<T>(p0 * s + p1 * f.x);
+                for (int e = 0; e < kPairs / 2; ++e)
+                    *reinterpret_cast<float4*>(&f[4 * e]) = __ldg(reinterpret_cast<const float4*>(z) + e);
+            } else {
+                *reinterpret_cast<float2*>(&f[0]) = __ldg(reinterpret_cast<const float2*>(z));
             }
-            *reinterpret_cast<Vec<T, V>*>(yh + c) = lo;
-            *reinterpret_cast<Vec<T, V>*>(yh + c + o) = hi;
-        } else if (V == 1) {
-            const int c = 2 * w;
-            const float2 f = __ldg(reinterpret_cast<const float2*>(row + c));
-            const float p0 = to_f32(xh[c]), p1 = to_f32(xh[c + 1]), s = sgn * f.y;
-            yh[c] = from_f32<T>(p0 * f.x - p1 * s);
-            yh[c + 1] = from_f32<T>(p0 * s + p1 * f.x);
-        } else {
-            const int c = w * V;
-            Vec<T, V> z = *reinterpret_cast<const Vec<T, V>*>(xh + c);
 #pragma unroll
-            for (int e = 0; e + 1 < V; e += 2) {
-                const float2 f = __ldg(reinterpret_cast<const float2*>(row + c + e));
-                const float p0 = to_f32(z.v[e]), p1 = to_f32(z.v[e + 1]), s = sgn * f.y;
-                z.v[e] = from_f32<T>(p0 * f.x - p1 * s);
-                z.v[e + 1] = from_f32<T>(p0 * s + p1 * f.x);
+            for (int e = 0; e < kPairs; ++e) {
+                T& x = HALF || V == 1 ? l.v[HALF ? e : 0] : l.v[(2 * e) % V];
+                T& y = HALF || V == 1 ? r.v[HALF ? e : 0] : l.v[(2 * e + 1) % V];
+                const float p0 = to_f32(x), p1 = to_f32(y), c = f[2 * e], s = sgn * f[2 * e + 1];
+                x = from_f32<T>(p0 * c - p1 * s);
+                y = from_f32<T>(p0 * s + p1 * c);
             }
-            *reinterpret_cast<Vec<T, V>*>(yh + c) = z;
+            if (HALF) *reinterpret_cast<Vec<T, V>*>(yr + at + a.rot / 2) = r;
+            else if (V == 1) *reinterpret_cast<Vec<T, V>*>(yr + at + 1) = r;
         }
+        *reinterpret_cast<Vec<T, V>*>(yr + at) = l;
     }
 }
 
@@ -100,9 +91,12 @@ cudaError_t launch_v(const RopeProb& p, const T* x, T* y, const RopeArgs& a, cud
     const int span = HALF ? V : (V == 1 ? 2 : V);
     const int units = (HALF ? p.rot / 2 / span : p.rot / span) + (a.copy ? (p.hd - p.rot + V - 1) / V : 0);
     const int total = units * p.heads;
-    // a thread takes total / iters units: whole warps, no block above 256 threads, the last trip full
-    const int iters = (total + 255) / 256;
-    const int threads = std::min(256, ((total + iters - 1) / iters + 31) / 32 * 32);
+    // A thread takes total / trips units: whole warps, no block above 256 threads, the last trip full.  Small blocks of
+    // three trips keep more tokens in flight (16384 tokens x 20 x 128 bf16: 32.0 us, 33.0 with one trip; 15992 x 12 x
+    // 64 fp32, half of it rotated: 17.1 and 18.1); with fewer tokens than fill the GPU one trip is sooner done
+    // (64 tokens x 20 x 128: 2.1 us, 3.1 with three).
+    const int trips = std::max(p.N >= 8 * 148 ? 3 : 1, (total + 255) / 256);
+    const int threads = std::min(256, ((total + trips - 1) / trips + 31) / 32 * 32);
     DC_LAUNCH(kRope, st, rope_heads_kernel<T, V, HALF><<<(unsigned)p.N, threads, 0, st>>>(x, y, a));
     return cudaGetLastError();
 }
