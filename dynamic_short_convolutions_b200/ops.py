@@ -103,20 +103,18 @@ def _device(device) -> torch.device:
     return torch.device(d.type, torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
 
 
-class _On:
-    """Makes a CUDA device current for a call where it is not (kernels launch on the current device)."""
+def _on(device: torch.device, call, *args) -> None:
+    """call(*args) with `device` current (kernels launch on the current device)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        call(*args)
+    else:
+        with torch.cuda.device(device):
+            call(*args)
 
-    def __init__(self, device: torch.device):
-        self.to = device.index if device.index is not None and device.index != torch.cuda.current_device() else None
 
-    def __enter__(self):
-        if self.to is not None:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.to)
-
-    def __exit__(self, *exc):
-        if self.to is not None:
-            torch.cuda.set_device(self.back)
+def _like(t: torch.Tensor, rows: int, width: int) -> torch.Tensor:
+    """An uninitialised [rows, width] tensor of t's type, on its device."""
+    return torch.empty_like(t) if t.shape == (rows, width) and t.is_contiguous() else t.new_empty((rows, width))
 
 
 class DynConvPlan:
@@ -268,17 +266,16 @@ class RopePlan:
 
     def apply(self, x, y=None, positions=None, cu_seqlens=None, inverse: bool = False, stream=None):
         """y = R(p) x, or the transposed rotation (the backward).  ``y=x`` rotates in place."""
+        _rows(x, "x", self.N, self.width, self.dtype, self.strides[0], self.device)
         if y is None:
             if self.strides[1] not in (0, self.width):
                 raise ValueError("a plan with a strided y needs the y to write")
-            y = torch.empty((self.N, self.width), dtype=self.dtype, device=self.device)
+            y = _like(x, self.N, self.width)
         else:
             _rows(y, "y", self.N, self.width, self.dtype, self.strides[1], self.device)
-        _rows(x, "x", self.N, self.width, self.dtype, self.strides[0], self.device)
         _flat(positions, "positions", torch.int32, self.device, (self.N,))
         _cu(cu_seqlens, self.device)
-        with _On(self.device):
-            L.dynconv_rope(self.desc[int(inverse)], cu_seqlens, positions, x, y, self.ws, stream)
+        _on(self.device, L.dynconv_rope, self.desc[int(inverse)], cu_seqlens, positions, x, y, self.ws, stream)
         return y
 
 
@@ -317,12 +314,11 @@ class AttnPlan:
         """o [N, heads * head_dim]; with ``want_lse`` (o, lse), lse fp32 [heads, N] for :meth:`backward`."""
         self._inputs(q, k, v, cu_seqlens)
         if o is None:
-            o = torch.empty((self.N, self.wq), dtype=self.dtype, device=self.device)
+            o = _like(q, self.N, self.wq)
         else:
             _rows(o, "o", self.N, self.wq, self.dtype, 0, self.device)
         lse = torch.empty((self.heads, self.N), dtype=torch.float32, device=self.device) if want_lse else None
-        with _On(self.device):
-            L.dynconv_attn_fwd(self.desc, cu_seqlens, q, k, v, o, lse, self.ws, stream)
+        _on(self.device, L.dynconv_attn_fwd, self.desc, cu_seqlens, q, k, v, o, lse, self.ws, stream)
         return (o, lse) if want_lse else o
 
     def backward(self, d_o, q, k, v, o, lse, cu_seqlens=None, out=None, stream=None):
@@ -332,9 +328,7 @@ class AttnPlan:
         if out is None:
             if any(self.grad_strides):
                 raise ValueError("a plan with strided gradients needs the tensors to write (out)")
-            out = {"dq": torch.empty((self.N, self.wq), dtype=self.dtype, device=self.device),
-                   "dk": torch.empty((self.N, self.wk), dtype=self.dtype, device=self.device),
-                   "dv": torch.empty((self.N, self.wk), dtype=self.dtype, device=self.device)}
+            out = {"dq": _like(q, self.N, self.wq), "dk": _like(k, self.N, self.wk), "dv": _like(v, self.N, self.wk)}
         for name, t, width, stride in (("d_o", d_o, self.wq, 0), ("o", o, self.wq, 0),
                                        ("dq", out["dq"], self.wq, self.grad_strides[0]),
                                        ("dk", out["dk"], self.wk, self.grad_strides[1]),
@@ -343,9 +337,8 @@ class AttnPlan:
         if lse is None:
             raise ValueError("the backward needs the forward's lse (want_lse=True)")
         _flat(lse, "lse", torch.float32, self.device, (self.heads, self.N))
-        with _On(self.device):
-            L.dynconv_attn_bwd(self.desc, cu_seqlens, d_o, q, k, v, o, lse, out["dq"], out["dk"], out["dv"], self.ws,
-                               stream)
+        _on(self.device, L.dynconv_attn_bwd, self.desc, cu_seqlens, d_o, q, k, v, o, lse, out["dq"], out["dk"], out["dv"],
+            self.ws, stream)
         return out
 
 
@@ -393,16 +386,16 @@ class AttnDecoder:
         [batch, tokens]): bit j of an entry set where that token sees drafted token j, its own bit included;
         None: a chain."""
         rows = self.batch * self.tokens
+        _rows(q, "q", rows, self.wq, self.dtype, self.strides[0], self.device)
         if o is None:
-            o = torch.empty((rows, self.wq), dtype=self.dtype, device=self.device)
+            o = _like(q, rows, self.wq)
         else:
             _rows(o, "o", rows, self.wq, self.dtype, 0, self.device)
-        _rows(q, "q", rows, self.wq, self.dtype, self.strides[0], self.device)
         _rows(k, "k", rows, self.wk, self.dtype, self.strides[1], self.device)
         _rows(v, "v", rows, self.wk, self.dtype, self.strides[2], self.device)
         _flat(ancestors, "ancestors", torch.int64, self.device, (self.batch, self.tokens))
-        with _On(self.device):
-            L.dynconv_attn_decode(self.desc, q, k, v, self.k_cache, self.v_cache, self.lens, ancestors, o, self.ws, stream)
+        _on(self.device, L.dynconv_attn_decode, self.desc, q, k, v, self.k_cache, self.v_cache, self.lens, ancestors, o,
+            self.ws, stream)
         return o
 
     def advance(self, kept=None):
