@@ -17,14 +17,15 @@ constexpr int kRows = kTcTile;                   // 128 tokens per tile: the lan
 constexpr uint32_t kAtom = kRows * 128;          // bytes of a 128-token x 64-channel tile
 
 // ---------------------------------------------------------------- tensor maps
-// [N tokens][heads][hd] bf16, a box of 128 tokens x one head x 64 channels; channels from hd on and tokens
+// [N tokens][heads][hd] bf16, a box of `rows` tokens x one head x 64 channels; channels from hd on and tokens
 // from N on read zero, so every head width up to 128 runs on tiles of 64 or 128 channels.
-inline bool make_head_map(CUtensorMap* map, const void* base, int64_t N, int heads, int hd, int64_t row_stride) {
+inline bool make_head_map(CUtensorMap* map, const void* base, int64_t N, int heads, int hd, int64_t row_stride,
+                          uint32_t rows = kRows) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)N};
     cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)row_stride * 2};
-    cuuint32_t box[3] = {64, 1, kRows};
+    cuuint32_t box[3] = {64, 1, rows};
     cuuint32_t es[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

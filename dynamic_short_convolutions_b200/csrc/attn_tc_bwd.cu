@@ -1,4 +1,5 @@
-// attn_tc_bwd.cu -- causal attention backward on the tensor cores (bf16 storage).
+// attn_tc_bwd.cu -- causal attention backward on the tensor cores (bf16 storage), heads of 72 to 128 channels (narrow
+// ones: attn_tc_bwd64.cu).
 //
 //   P = exp(scale S - lse),  dP = dO V^T,  dS = P (dP - D)
 //   dV = P^T dO,  dK = scale dS^T Q   (over every query of the document, every head of the group)
@@ -35,20 +36,16 @@
 // tensor cores waiting for L2: 4250 cycles per item instead of ~2500 at HD = 128).
 //   dkv: S(i+1) | dV(i) | dK(i) dP(i+1)    P and dS lie in the columns of dP, read into registers before
 //   dq:  S(i+1) | dP(i+1) | dQ(i)          dS has two buffers of its own
-#include <cooperative_groups.h>
-
 #include <algorithm>
 #include <type_traits>
 
-#include "attn_tc.cuh"
+#include "attn_tc_bwd.cuh"
 #include "prof.h"
 #include "smem_limit.h"
 
 namespace dynconv {
 namespace attn_tc {
 namespace {
-
-namespace cg = cooperative_groups;
 
 constexpr int kBwdThreads = 384;
 // The element warps' barrier (256 threads).
@@ -61,10 +58,8 @@ struct BwdSmem {
     static constexpr uint32_t tile = kAtom * (HD / 64);
     static constexpr int slots = HD == 128 ? 5 : 10;
     static constexpr uint32_t ring = 2 * tile, stats = ring + slots * tile, shared = stats + 2 * 2 * kRows * sizeof(float);
-    // a block's partial dV and dK for its cluster, in the memory of the tiles: rows padded by 16 bytes, so that
-    // a lane per row writes without bank conflicts
-    static constexpr int part_ld = HD + 4;
-    static_assert(2 * kRows * part_ld * sizeof(float) <= stats, "partial gradients fit the tiles");
+    // a block's partial dV and dK for its cluster, in the memory of the tiles
+    static_assert(2 * kRows * part_ld<HD>() * sizeof(float) <= stats, "partial gradients fit the tiles");
     struct Shared {
         uint64_t resident, full[slots], empty[slots], stat_full[2], stat_free[2];
         uint64_t s_full, s_free, dp_full, dp_free, p_ready, ds_ready[2], done, scanned;
@@ -132,70 +127,6 @@ __device__ __forceinline__ void feed_ring(uint8_t* ring, typename BwdSmem<HD>::S
             const Spot<HD> at(m);
             mbar_wait_drain(&x.full[at.slot], at.parity);
         }
-    }
-}
-
-// What bf16 rounding leaves of 32 values.
-__device__ __forceinline__ void remainder32(float (&f)[32]) {
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-        const uint32_t w = pack_bf16(f[e], f[e + 1]);
-        f[e] -= bf16_lo(w);
-        f[e + 1] -= bf16_hi(w);
-    }
-}
-__device__ __forceinline__ void store32(uint32_t to, const float (&f)[32]) {
-    uint32_t w[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
-    tmem_st16(to, w);
-}
-// dk and dv of `count` keys from key0 on (all below N), key by key over the queries that see it.
-__device__ __noinline__ void dkv_rows_again(const AttnTcArgs& a, int kv, int32_t key0, int count, int lane) {
-    const float cs = a.scale * kLog2e;
-    for (int r = 0; r < count; ++r) {
-        const int32_t j = key0 + r;
-        const int32_t end = doc_of(j, a.seg, a.seqlen).y;
-        const float4 k = row4(a.k + (int64_t)j * a.ks + (int64_t)kv * a.hd, lane, a.hd);
-        const float4 v = row4(a.v + (int64_t)j * a.vs + (int64_t)kv * a.hd, lane, a.hd);
-        float4 dk = make_float4(0.f, 0.f, 0.f, 0.f), dv = dk;
-        for (int g = 0; g < a.group; ++g) {
-            const int64_t h = kv * a.group + g;
-            for (int32_t n = j; n < end; ++n) {
-                const float4 q = row4(a.q + (int64_t)n * a.qs + h * a.hd, lane, a.hd);
-                const float4 d = row4(a.d_o + (int64_t)n * a.dos + h * a.hd, lane, a.hd);
-                const float p = exp2f(fmaf(warp_dot(q, k), cs, -a.lse[h * a.N + n] * kLog2e));
-                const float ds = p * (warp_dot(d, v) - a.delta[h * a.N + n]);
-                axpy4(dv, p, d);
-                axpy4(dk, ds, q);
-            }
-        }
-        put4(a.dv + (int64_t)j * a.dvs + (int64_t)kv * a.hd, lane, a.hd, dv);
-        put4(a.dk + (int64_t)j * a.dks + (int64_t)kv * a.hd, lane, a.hd,
-             make_float4(dk.x * a.scale, dk.y * a.scale, dk.z * a.scale, dk.w * a.scale));
-    }
-}
-
-// dq of `count` queries from row0 on (all below N), row by row over the keys it sees.
-__device__ __noinline__ void dq_rows_again(const AttnTcArgs& a, int head, int32_t row0, int count, int lane) {
-    const int kv = head / a.group;
-    const float cs = a.scale * kLog2e;
-    for (int r = 0; r < count; ++r) {
-        const int32_t n = row0 + r;
-        const float4 q = row4(a.q + (int64_t)n * a.qs + (int64_t)head * a.hd, lane, a.hd);
-        const float4 d = row4(a.d_o + (int64_t)n * a.dos + (int64_t)head * a.hd, lane, a.hd);
-        const float ls = a.lse[(int64_t)head * a.N + n] * kLog2e;
-        const float dl = warp_dot(d, row4(a.o + (int64_t)n * a.os + (int64_t)head * a.hd, lane, a.hd));
-        if (lane == 0) a.delta[(int64_t)head * a.N + n] = dl;
-        float4 dq = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int32_t j = doc_of(n, a.seg, a.seqlen).x; j <= n; ++j) {
-            const float4 k = row4(a.k + (int64_t)j * a.ks + (int64_t)kv * a.hd, lane, a.hd);
-            const float4 v = row4(a.v + (int64_t)j * a.vs + (int64_t)kv * a.hd, lane, a.hd);
-            const float p = exp2f(fmaf(warp_dot(q, k), cs, -ls));
-            axpy4(dq, p * (warp_dot(d, v) - dl), k);
-        }
-        put4(a.dq + (int64_t)n * a.dqs + (int64_t)head * a.hd, lane, a.hd,
-             make_float4(dq.x * a.scale, dq.y * a.scale, dq.z * a.scale, dq.w * a.scale));
     }
 }
 
@@ -462,7 +393,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         if (!ok) x.again = -1;                               // nothing is written then
         if (ranks > 1) {
             // this block's part, for the cluster: warps 0-3 dv, warps 4-7 dk
-            float* row = reinterpret_cast<float*>(sm) + (size_t)(w * kRows + (warp & 3) * 32 + lane) * S::part_ld;
+            float* row = reinterpret_cast<float*>(sm) + (size_t)(w * kRows + (warp & 3) * 32 + lane) * part_ld<HD>();
             const uint32_t src = tb + ((uint32_t)((warp & 3) * 32) << 16) + (w ? kDK : kDV);
 #pragma unroll
             for (int b = 0; b < HD / 32; ++b) {
@@ -505,38 +436,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         if (threadIdx.x == 0) tma_store_wait_all();          // the gradients have left shared memory
         return;
     }
-    // Every thread of every block comes here, whatever became of its waits, so the cluster's barriers end.
-    cluster.sync();
-    int bad = 0;
-    for (int r = 0; r < ranks; ++r) {
-        const int f = *cluster.map_shared_rank(&x.again, r);
-        bad = f < 0 || bad < 0 ? -1 : bad | f;
-    }
-    const int per = kRows / ranks, r0 = rank * per;          // the rows this block adds up
-    if (bad == 0) {
-        const float* part = reinterpret_cast<const float*>(sm);
-        for (int i = threadIdx.x; i < 2 * per * (HD / 8); i += kBwdThreads) {
-            const int c = i % (HD / 8) * 8, r = i / (HD / 8) % per, w = i / (HD / 8) / per;
-            const int32_t j = key0 + r0 + r;
-            float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-            for (int n = 0; n < ranks; ++n) {
-                const float4* p = reinterpret_cast<const float4*>(
-                    cluster.map_shared_rank(part, n) + (size_t)(w * kRows + r0 + r) * S::part_ld + c);
-                const float4 u = p[0], v = p[1];
-                lo.x += u.x; lo.y += u.y; lo.z += u.z; lo.w += u.w;
-                hi.x += v.x; hi.y += v.y; hi.z += v.z; hi.w += v.w;
-            }
-            if (j >= a.N || c >= a.hd) continue;
-            const float m = w ? a.scale : 1.f;
-            __nv_bfloat16* to = (w ? a.dk + (int64_t)j * a.dks : a.dv + (int64_t)j * a.dvs) + (int64_t)kv * a.hd + c;
-            *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(lo.x * m, lo.y * m), pack_bf16(lo.z * m, lo.w * m),
-                                                       pack_bf16(hi.x * m, hi.y * m), pack_bf16(hi.z * m, hi.w * m));
-        }
-    } else if (bad > 0 && warp < 8) {
-        const int32_t n = (per + 7) / 8, r = key0 + r0 + warp * n;
-        dkv_rows_again(a, kv, r, min(min(n, per - warp * n), a.N - r), lane);
-    }
-    cluster.sync();                                          // no block leaves while its part is read
+    join_parts<HD, kBwdThreads, 8>(a, cluster, &x.again, reinterpret_cast<const float*>(sm), kv, key0);
 }
 
 // ---------------------------------------------------------------- dq
@@ -824,38 +724,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     if (threadIdx.x == 0) tma_store_wait_all();              // dq has left shared memory
 }
 
-// Blocks that share the heads of a group (a power of two up to 8).
-int dkv_ranks(const AttnProb& p, int64_t blocks) {
-    static const int force = getenv("DKV_R") ? atoi(getenv("DKV_R")) : 0;
-    int ranks = 1;
-    while (ranks * 2 <= std::min(p.group, 8) && (force ? ranks < force : blocks * ranks < 3 * num_sms())) ranks *= 2;
-    return ranks;
-}
-
 template <int HD>
-cudaError_t bwd_hd(const AttnProb& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                   const CUtensorMap& td, const CUtensorMap& tdq, const CUtensorMap& tdk, const CUtensorMap& tdv,
-                   const AttnTcArgs& a, cudaStream_t st) {
+cudaError_t bwd_wide(const AttnProb& p, const BwdMaps& m, const AttnTcArgs& a, cudaStream_t st) {
     constexpr uint32_t smem = BwdSmem<HD>::bytes;
     cudaError_t e = DC_SMEM_LIMIT(attn_dkv_kernel<HD>, smem);
     if (e == cudaSuccess) e = DC_SMEM_LIMIT(attn_dq_kernel<HD>, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kRows - 1) / kRows;
-    DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<HD><<<(unsigned)(tiles * p.heads), kBwdThreads, smem, st>>>(tq, tk, tv, td, tdq, a));
+    DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<HD><<<(unsigned)(tiles * p.heads), kBwdThreads, smem, st>>>(m.q, m.k, m.v, m.d,
+                                                                                                       m.dq, a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int ranks = dkv_ranks(p, tiles * p.kvh);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * p.kvh * ranks));
-    cfg.blockDim = dim3(kBwdThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = ranks > 1 ? 1 : 0;
-    DC_LAUNCH(kAttnTcDkv, st, e = cudaLaunchKernelEx(&cfg, attn_dkv_kernel<HD>, tq, tk, tv, td, tdk, tdv, a));
+    DC_LAUNCH(kAttnTcDkv, st, e = launch_ranks(attn_dkv_kernel<HD>, ranks, (unsigned)(tiles * p.kvh * ranks), kBwdThreads,
+                                               smem, st, m.q, m.k, m.v, m.d, m.dk, m.dv, a));
     return e;
 }
 
@@ -866,11 +747,15 @@ cudaError_t attn_tc_bwd(const AttnProb& p, const void* d_o, const void* q, const
                         const void* o, const float* lse, float* delta, void* dq, void* dk, void* dv, uint32_t* err,
                         cudaStream_t st) {
     using namespace attn_tc;
-    CUtensorMap tq, tk, tv, td, tdq, tdk, tdv;
-    if (!make_head_map(&tq, q, p.N, p.heads, p.hd, p.qs) || !make_head_map(&tk, k, p.N, p.kvh, p.hd, p.ks) ||
-        !make_head_map(&tv, v, p.N, p.kvh, p.hd, p.vs) || !make_head_map(&td, d_o, p.N, p.heads, p.hd, p.dos) ||
-        !make_head_map(&tdq, dq, p.N, p.heads, p.hd, p.dqs) || !make_head_map(&tdk, dk, p.N, p.kvh, p.hd, p.dks) ||
-        !make_head_map(&tdv, dv, p.N, p.kvh, p.hd, p.dvs))
+    BwdMaps m;
+    if (!make_head_map(&m.q, q, p.N, p.heads, p.hd, p.qs) || !make_head_map(&m.k, k, p.N, p.kvh, p.hd, p.ks) ||
+        !make_head_map(&m.v, v, p.N, p.kvh, p.hd, p.vs) || !make_head_map(&m.d, d_o, p.N, p.heads, p.hd, p.dos) ||
+        !make_head_map(&m.dq, dq, p.N, p.heads, p.hd, p.dqs) || !make_head_map(&m.dk, dk, p.N, p.kvh, p.hd, p.dks) ||
+        !make_head_map(&m.dv, dv, p.N, p.kvh, p.hd, p.dvs))
+        return cudaErrorInvalidValue;
+    if (p.hd <= 64 &&
+        (!make_head_map(&m.q64, q, p.N, p.heads, p.hd, p.qs, 64) || !make_head_map(&m.k64, k, p.N, p.kvh, p.hd, p.ks, 64) ||
+         !make_head_map(&m.v64, v, p.N, p.kvh, p.hd, p.vs, 64) || !make_head_map(&m.d64, d_o, p.N, p.heads, p.hd, p.dos, 64)))
         return cudaErrorInvalidValue;
     AttnTcArgs a = tc_args(p);
     a.q = static_cast<const __nv_bfloat16*>(q);
@@ -884,8 +769,7 @@ cudaError_t attn_tc_bwd(const AttnProb& p, const void* d_o, const void* q, const
     a.lse = const_cast<float*>(lse);
     a.delta = delta;
     a.err = err;
-    return p.hd <= 64 ? bwd_hd<64>(p, tq, tk, tv, td, tdq, tdk, tdv, a, st)
-                      : bwd_hd<128>(p, tq, tk, tv, td, tdq, tdk, tdv, a, st);
+    return p.hd <= 64 ? bwd_narrow(p, m, a, st) : bwd_wide<128>(p, m, a, st);
 }
 
 }  // namespace dynconv
