@@ -33,6 +33,13 @@ struct Smem64 {
     static_assert(2 * kRows * part_ld<64>() * sizeof(float) <= stats, "partial gradients fit the tiles");
 };
 
+// Barriers and TMEM stand once all have come here; the loading warp only arrives.
+__device__ __forceinline__ void started_arrive() { asm volatile("bar.arrive 2, 192;" ::: "memory"); }
+__device__ __forceinline__ void started_sync() {
+    tc_fence_before();
+    asm volatile("bar.sync 2, 192;" ::: "memory");
+    tc_fence_after();
+}
 __device__ __forceinline__ void element_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 struct Shared64 {
@@ -101,19 +108,13 @@ __global__ void __launch_bounds__(kThreads64, 2) attn_dkv64_kernel(const __grid_
     const int32_t e_last = doc_of(min(key0 + kRows, a.N) - 1, a.seg, a.seqlen).y;
     const int32_t t0 = key0 / kCols, per_head = (e_last - 1) / kCols - t0 + 1;
     const uint32_t items = (uint32_t)per_head * heads;
-    if (threadIdx.x == 0) init64(x, 2);
-    if (warp == 4) {
-        tmem_alloc(&x.tmem_base, 256);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tb = x.tmem_base;
     constexpr uint32_t kDP = 64, kDV = 128, kDK = 192;
 
     if (warp == 5) {
         // loads by lane 0; the statistics of an item, read one item ahead, by the warp
+        if (lane == 0) init64(x, 2);
+        __syncwarp();
+        started_arrive();                                    // the loads need no TMEM
         if (lane == 0) {
             mbar_arrive_expect_tx(&x.resident, 2 * kAtom);
             tma_load_3d(sK, &tk, &x.resident, 0, kv, key0);
@@ -158,6 +159,10 @@ __global__ void __launch_bounds__(kThreads64, 2) attn_dkv64_kernel(const __grid_
         }
         __syncwarp();
     } else if (warp == 4) {
+        tmem_alloc(&x.tmem_base, 256);
+        tmem_relinquish();
+        started_sync();
+        const uint32_t tb = x.tmem_base;
         const uint32_t k_at = smem_u32(sK), v_at = smem_u32(sV), r_at = smem_u32(ring);
         const bool lead = elect_one();
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -203,9 +208,10 @@ __global__ void __launch_bounds__(kThreads64, 2) attn_dkv64_kernel(const __grid_
         mbar_wait_drain(&x.done, 0);
     } else {
         const int32_t j = key0 + warp * 32 + lane;
-        const uint32_t at = tb + ((uint32_t)(warp * 32) << 16);
-        const float cs = a.scale * kLog2e;
         const int32_t end = j < a.N ? doc_of(j, a.seg, a.seqlen).y : 0;
+        started_sync();
+        const uint32_t at = x.tmem_base + ((uint32_t)(warp * 32) << 16);
+        const float cs = a.scale * kLog2e;
         bool ok = true;
         uint32_t phase = 0;
         int32_t t = 0;
@@ -335,10 +341,10 @@ __global__ void __launch_bounds__(kThreads64, 2) attn_dkv64_kernel(const __grid_
     __syncthreads();
     if (warp == 4) {
         tc_fence_after();
-        tmem_dealloc(tb, 256);
+        tmem_dealloc(x.tmem_base, 256);
     }
     if (ranks == 1) {
-        if (threadIdx.x == 0) tma_store_wait_all();          // the gradients have left shared memory
+        if (threadIdx.x == 0) tma_store_wait_read_all();      // the gradients have left shared memory
         return;
     }
     join_parts<64, kThreads64, 4>(a, cluster, &x.again, reinterpret_cast<const float*>(sK), kv, key0);
@@ -367,18 +373,12 @@ __global__ void __launch_bounds__(kThreads64, 2) attn_dq64_kernel(const __grid_c
     const int32_t lo = doc_of(row0, a.seg, a.seqlen).x / kCols;
     const int32_t full_from = doc_of(last, a.seg, a.seqlen).x;
     const int32_t items = last / kCols - lo + 1, plain = row0 / kCols - lo;      // items before the diagonal's
-    if (threadIdx.x == 0) init64(x, 1);
-    if (warp == 4) {
-        tmem_alloc(&x.tmem_base, 256);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tb = x.tmem_base;
     constexpr uint32_t kDP = 64, kDQ = 128, kDS = 192;
 
     if (warp == 5) {
+        if (lane == 0) init64(x, 1);
+        __syncwarp();
+        started_arrive();                                    // the loads need no TMEM
         if (lane == 0) {
             mbar_arrive_expect_tx(&x.resident, 2 * kAtom);
             tma_load_3d(sQ, &tq, &x.resident, 0, head, row0);
@@ -399,6 +399,10 @@ __global__ void __launch_bounds__(kThreads64, 2) attn_dq64_kernel(const __grid_c
         }
         __syncwarp();
     } else if (warp == 4) {
+        tmem_alloc(&x.tmem_base, 256);
+        tmem_relinquish();
+        started_sync();
+        const uint32_t tb = x.tmem_base;
         const uint32_t q_at = smem_u32(sQ), o_at = smem_u32(sO), r_at = smem_u32(ring);
         const bool lead = elect_one();
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -448,7 +452,6 @@ __global__ void __launch_bounds__(kThreads64, 2) attn_dq64_kernel(const __grid_c
     } else {
         const int row = warp * 32 + lane;
         const int32_t n = row0 + row;
-        const uint32_t at = tb + ((uint32_t)(warp * 32) << 16), ds_at = at + kDS;
         const float cs = a.scale * kLog2e;
         {
             // D = dO . O: eight lanes per row, all loads in flight together
@@ -483,6 +486,8 @@ __global__ void __launch_bounds__(kThreads64, 2) attn_dq64_kernel(const __grid_c
         const int32_t start = n < a.N ? doc_of(n, a.seg, a.seqlen).x : INT32_MAX;
         const float ls = n < a.N ? -a.lse[(int64_t)head * a.N + n] * kLog2e : 0.f;
         float dl = -sD[row];
+        started_sync();
+        const uint32_t at = x.tmem_base + ((uint32_t)(warp * 32) << 16), ds_at = at + kDS;
         bool ok = true;
         uint32_t phase = 0;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -604,9 +609,9 @@ __global__ void __launch_bounds__(kThreads64, 2) attn_dq64_kernel(const __grid_c
     __syncthreads();
     if (warp == 4) {
         tc_fence_after();
-        tmem_dealloc(tb, 256);
+        tmem_dealloc(x.tmem_base, 256);
     }
-    if (threadIdx.x == 0) tma_store_wait_all();              // dq has left shared memory
+    if (threadIdx.x == 0) tma_store_wait_read_all();          // dq has left shared memory
 }
 
 }  // namespace
