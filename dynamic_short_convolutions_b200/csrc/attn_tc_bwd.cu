@@ -8,8 +8,8 @@
 // Two kernels, each with its sums in TMEM for its whole run and written once: attn_dkv_kernel takes 128
 // keys of one key/value head and walks the query tiles of every head of the group; attn_dq_kernel takes 128
 // queries of one head and walks the key tiles.  S and dP are computed in both (7 products of a tile pair
-// where one fused kernel needs 5), because the fused kernel would add a 128 x HD fp32 tile of dQ into global
-// memory for every tile pair -- 64 KB per 2.6 us of tensor work and SM at HD = 128, above what L2 reduces --
+// where one fused kernel needs 5), because the fused kernel would add a 128 x 128 fp32 tile of dQ into global
+// memory for every tile pair -- 64 KB per 2.6 us of tensor work and SM, above what L2 reduces --
 // and in an order that changes from run to run.  Here nothing is added atomically and results repeat bitwise.
 //
 // No operand passes through shared memory by hand: the transposed scores S^T = K Q^T put keys on the TMEM
@@ -33,7 +33,7 @@
 // the next scores are computed into S as soon as the element warps hold this item's in registers, the
 // exponentials run before the wait for dP, and the two halves of an item have ring places of their own,
 // given back as soon as their last product is done (both loads of an item together, released together, left the
-// tensor cores waiting for L2: 4250 cycles per item instead of ~2500 at HD = 128).
+// tensor cores waiting for L2: 4250 cycles per item instead of ~2500).
 //   dkv: S(i+1) | dV(i) | dK(i) dP(i+1)    P and dS lie in the columns of dP, read into registers before
 //   dq:  S(i+1) | dP(i+1) | dQ(i)          dS has two buffers of its own
 #include <algorithm>
@@ -47,16 +47,23 @@ namespace dynconv {
 namespace attn_tc {
 namespace {
 
+constexpr int HD = 128;                          // channels that fit; narrower heads are padded by zeros
 constexpr int kBwdThreads = 384;
+// Barriers and TMEM stand once all have come here; the loading warp only arrives.
+__device__ __forceinline__ void started_arrive() { asm volatile("bar.arrive 2, 384;" ::: "memory"); }
+__device__ __forceinline__ void started_sync() {
+    tc_fence_before();
+    asm volatile("bar.sync 2, 384;" ::: "memory");
+    tc_fence_after();
+}
 // The element warps' barrier (256 threads).
 __device__ __forceinline__ void element_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 // Shared memory: two resident tiles, a ring of tiles, the statistics of two items, the barriers.  No slack for
 // alignment: the dynamic part starts on a 1024-byte boundary, since these kernels have no static part (checked).
-template <int HD>
 struct BwdSmem {
     static constexpr uint32_t tile = kAtom * (HD / 64);
-    static constexpr int slots = HD == 128 ? 5 : 10;
+    static constexpr int slots = 5;
     static constexpr uint32_t ring = 2 * tile, stats = ring + slots * tile, shared = stats + 2 * 2 * kRows * sizeof(float);
     // a block's partial dV and dK for its cluster, in the memory of the tiles
     static_assert(2 * kRows * part_ld<HD>() * sizeof(float) <= stats, "partial gradients fit the tiles");
@@ -75,11 +82,10 @@ __device__ __forceinline__ bool misplaced(const void* sm, uint32_t* err) {
     if (threadIdx.x == 0) atomicOr(err, kErrWaitTimeout);
     return true;
 }
-// Barriers of either kernel; thread 0.
-template <int HD>
-__device__ __forceinline__ void bwd_init(typename BwdSmem<HD>::Shared& x) {
+// Barriers of either kernel; one thread.
+__device__ __forceinline__ void bwd_init(BwdSmem::Shared& x) {
     mbar_init(&x.resident, 1);
-    for (int s = 0; s < BwdSmem<HD>::slots; ++s) {
+    for (int s = 0; s < BwdSmem::slots; ++s) {
         mbar_init(&x.full[s], 1);
         mbar_init(&x.empty[s], 2);                           // the last product, the look for infinities
     }
@@ -101,22 +107,21 @@ __device__ __forceinline__ void bwd_init(typename BwdSmem<HD>::Shared& x) {
     fence_mbar_init();
 }
 // Place n of the ring: its slot, and the parity of its use of that slot.
-template <int HD>
 struct Spot {
     int slot;
     uint32_t parity;
     __device__ __forceinline__ explicit Spot(uint32_t n)
-        : slot((int)(n % BwdSmem<HD>::slots)), parity((n / BwdSmem<HD>::slots) & 1) {}
+        : slot((int)(n % BwdSmem::slots)), parity((n / BwdSmem::slots) & 1) {}
 };
 // TMA of the ring's places 0 .. count - 1 by one thread: load(place, destination, barrier).  After an abort no
 // copy may land once the block has gone.
-template <int HD, typename Load>
-__device__ __forceinline__ void feed_ring(uint8_t* ring, typename BwdSmem<HD>::Shared& x, uint32_t count, uint32_t* err,
+template <typename Load>
+__device__ __forceinline__ void feed_ring(uint8_t* ring, BwdSmem::Shared& x, uint32_t count, uint32_t* err,
                                           Load load) {
-    using S = BwdSmem<HD>;
+    using S = BwdSmem;
     uint32_t n = 0;
     for (; n < count; ++n) {
-        const Spot<HD> at(n);
+        const Spot at(n);
         if (n >= S::slots && !mbar_wait(&x.empty[at.slot], at.parity ^ 1, &x.abort_flag, err)) break;
         mbar_arrive_expect_tx(&x.full[at.slot], S::tile);
         load(n, ring + at.slot * S::tile, &x.full[at.slot]);
@@ -124,14 +129,13 @@ __device__ __forceinline__ void feed_ring(uint8_t* ring, typename BwdSmem<HD>::S
     if (*(volatile int*)&x.abort_flag) {
         mbar_wait_drain(&x.resident, 0);
         for (uint32_t m = n > S::slots ? n - S::slots : 0; m < n; ++m) {
-            const Spot<HD> at(m);
+            const Spot at(m);
             mbar_wait_drain(&x.full[at.slot], at.parity);
         }
     }
 }
 
 // ---------------------------------------------------------------- dk, dv
-template <int HD>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_constant__ CUtensorMap tq,
                                                                   const __grid_constant__ CUtensorMap tk,
                                                                   const __grid_constant__ CUtensorMap tv,
@@ -139,13 +143,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                                                                   const __grid_constant__ CUtensorMap tdk,
                                                                   const __grid_constant__ CUtensorMap tdv,
                                                                   const AttnTcArgs a) {
-    using S = BwdSmem<HD>;
+    using S = BwdSmem;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t* sK = sm;
     uint8_t* sV = sm + S::tile;
     uint8_t* ring = sm + S::ring;                            // place 2 i: Q of item i, 2 i + 1: its dO
     float* stats = reinterpret_cast<float*>(sm + S::stats);
-    typename S::Shared& x = *reinterpret_cast<typename S::Shared*>(sm + S::shared);
+    S::Shared& x = *reinterpret_cast<S::Shared*>(sm + S::shared);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -159,30 +163,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
     const int32_t t0 = key0 / kRows, per_head = (e_last - 1) / kRows - t0 + 1;
     const uint32_t items = (uint32_t)per_head * heads;
     if (misplaced(sm, a.err)) return;
-    if (threadIdx.x == 0) bwd_init<HD>(x);
-    if (warp == 8) {
-        tmem_alloc(&x.tmem_base, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tb = x.tmem_base;
     constexpr uint32_t kDP = 128, kDV = 256, kDK = 256 + HD;
 
     if (warp == 9) {
+        if (lane == 0) bwd_init(x);
+        __syncwarp();
+        started_arrive();                                    // the loads need no TMEM
         if (lane == 0) {
             mbar_arrive_expect_tx(&x.resident, 2 * S::tile);
             load_head_tile<HD>(sK, &tk, &x.resident, kv, key0);
             load_head_tile<HD>(sV, &tv, &x.resident, kv, key0);
             int32_t g = 0, t = 0;
-            feed_ring<HD>(ring, x, 2 * items, a.err, [&](uint32_t n, uint8_t* to, uint64_t* bar) {
+            feed_ring(ring, x, 2 * items, a.err, [&](uint32_t n, uint8_t* to, uint64_t* bar) {
                 load_head_tile<HD>(to, n & 1 ? &td : &tq, bar, head0 + g, (t0 + t) * kRows);
                 if ((n & 1) && ++t == per_head) { t = 0; ++g; }
             });
         }
         __syncwarp();
     } else if (warp == 8) {
+        tmem_alloc(&x.tmem_base, 512);
+        tmem_relinquish();
+        started_sync();
+        const uint32_t tb = x.tmem_base;
         constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
         constexpr uint32_t kIdG = idesc_bf16(128, HD, false, true);
         const uint32_t k_at = smem_u32(sK), v_at = smem_u32(sV), r_at = smem_u32(ring);
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
                 umma_commit(bar);
             }
         };
-        // D (HD columns at `to`) += the bf16 rows at `from` (columns 0-63 and 64-127 of the tile 64 columns apart) X
+        // D (128 columns at `to`) += the bf16 rows at `from` (columns 0-63 and 64-127 of the tile 64 columns apart) X
         auto grad = [&](uint32_t to, uint32_t from, uint32_t X, bool add) {
             if (lead) {
 #pragma unroll
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         };
         // A wait that finds its barrier complete still takes some 100 cycles, in which the tensor cores run dry: the
         // two loads of the next item are asked after together, and tiles that TMA brought need no tcgen05 fence.
-        auto landed = [&](const Spot<HD>& p, const Spot<HD>& q) {
+        auto landed = [&](const Spot& p, const Spot& q) {
             const bool u = mbar_try_wait(&x.full[p.slot], p.parity), v = mbar_try_wait(&x.full[q.slot], q.parity);
             return (u && v) || (mbar_wait(&x.full[p.slot], p.parity, &x.abort_flag, a.err) &&
                                 mbar_wait(&x.full[q.slot], q.parity, &x.abort_flag, a.err));
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         uint32_t phase = 0;
         int32_t t = 0;
         for (uint32_t i = 0; ok && i < items; ++i, phase ^= 1) {
-            const Spot<HD> q(2 * i), d(2 * i + 1), q1(2 * i + 2), d1(2 * i + 3);
+            const Spot q(2 * i), d(2 * i + 1), q1(2 * i + 2), d1(2 * i + 3);
             const bool more = i + 1 < items;
             auto next_scores = [&]() {
                 ok = ok && landed(q1, d1) && wait(&x.s_free, phase);
@@ -252,10 +254,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
         if (lead) umma_commit(&x.done);                      // every MMA done
         mbar_wait_drain(&x.done, 0);
     } else if (warp == 10) {
+        started_sync();
         bool ok = true;
         int32_t t = 0;
         for (uint32_t n = 0; ok && n < 2 * items; ++n) {
-            const Spot<HD> at(n);
+            const Spot at(n);
             ok = mbar_wait(&x.full[at.slot], at.parity, &x.abort_flag, a.err);
             if (!ok) break;
             if ((t == 0 || (t0 + t + 1) * kRows > full_to) && tile_nonfinite(ring + at.slot * S::tile, S::tile, lane) &&
@@ -280,6 +283,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
             }
             if (++t == per_head) { t = 0; ++g; }
         };
+        started_sync();
         fetch();
         for (uint32_t i = 0; i < items; ++i) {
             const int b = i & 1;
@@ -294,9 +298,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
     } else {
         const int w = warp >> 2;                             // columns 64 w .. 64 w + 63
         const int32_t j = key0 + (warp & 3) * 32 + lane;
-        const uint32_t at = tb + ((uint32_t)((warp & 3) * 32) << 16) + 64 * w;
         const float cs = a.scale * kLog2e;
         const int32_t end = j < a.N ? doc_of(j, a.seg, a.seqlen).y : 0;
+        started_sync();
+        const uint32_t tb = x.tmem_base;
+        const uint32_t at = tb + ((uint32_t)((warp & 3) * 32) << 16) + 64 * w;
         bool ok = true;
         uint32_t phase = 0;
         int32_t t = 0;
@@ -430,31 +436,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dkv_kernel(const __grid_c
     __syncthreads();
     if (warp == 8) {
         tc_fence_after();
-        tmem_dealloc(tb, 512);
+        tmem_dealloc(x.tmem_base, 512);
     }
     if (ranks == 1) {
-        if (threadIdx.x == 0) tma_store_wait_all();          // the gradients have left shared memory
+        if (threadIdx.x == 0) tma_store_wait_read_all();      // the gradients have left shared memory
         return;
     }
     join_parts<HD, kBwdThreads, 8>(a, cluster, &x.again, reinterpret_cast<const float*>(sm), kv, key0);
 }
 
 // ---------------------------------------------------------------- dq
-template <int HD>
 __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_constant__ CUtensorMap tq,
                                                                  const __grid_constant__ CUtensorMap tk,
                                                                  const __grid_constant__ CUtensorMap tv,
                                                                  const __grid_constant__ CUtensorMap td,
                                                                  const __grid_constant__ CUtensorMap tdq,
                                                                  const AttnTcArgs a) {
-    using S = BwdSmem<HD>;
+    using S = BwdSmem;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t* sQ = sm;
     uint8_t* sO = sm + S::tile;
     uint8_t* ring = sm + S::ring;                            // place 2 i: K of item i, 2 i + 1: its V
     float* sD = reinterpret_cast<float*>(sm + S::stats);     // [128] D, then [2][128] its halves over the last item
     float* sX = sD + kRows;
-    typename S::Shared& x = *reinterpret_cast<typename S::Shared*>(sm + S::shared);
+    S::Shared& x = *reinterpret_cast<S::Shared*>(sm + S::shared);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.heads, kv = head / a.group;
     const int32_t tiles = (a.N + kRows - 1) / kRows;
@@ -464,28 +469,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     const int32_t full_from = doc_of(min(row0 + kRows, a.N) - 1, a.seg, a.seqlen).x;
     const uint32_t items = (uint32_t)(hi - lo + 1);
     if (misplaced(sm, a.err)) return;
-    if (threadIdx.x == 0) bwd_init<HD>(x);
-    if (warp == 8) {
-        tmem_alloc(&x.tmem_base, 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tb = x.tmem_base;
     constexpr uint32_t kDP = 128, kDQ = 256, kDS = 384;      // dS: two buffers of 64 columns, a barrier each
 
     if (warp == 9) {
+        if (lane == 0) bwd_init(x);
+        __syncwarp();
+        started_arrive();                                    // the loads need no TMEM
         if (lane == 0) {
             mbar_arrive_expect_tx(&x.resident, 2 * S::tile);
             load_head_tile<HD>(sQ, &tq, &x.resident, head, row0);
             load_head_tile<HD>(sO, &td, &x.resident, head, row0);
-            feed_ring<HD>(ring, x, 2 * items, a.err, [&](uint32_t n, uint8_t* to, uint64_t* bar) {
+            feed_ring(ring, x, 2 * items, a.err, [&](uint32_t n, uint8_t* to, uint64_t* bar) {
                 load_head_tile<HD>(to, n & 1 ? &tv : &tk, bar, kv, (lo + (int32_t)(n >> 1)) * kRows);
             });
         }
         __syncwarp();
     } else if (warp == 8) {
+        tmem_alloc(&x.tmem_base, 512);
+        tmem_relinquish();
+        started_sync();
+        const uint32_t tb = x.tmem_base;
         constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
         constexpr uint32_t kIdG = idesc_bf16(128, HD, false, true);
         const uint32_t q_at = smem_u32(sQ), o_at = smem_u32(sO), r_at = smem_u32(ring);
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 umma_commit(bar);
             }
         };
-        auto landed = [&](const Spot<HD>& p) { return mbar_wait(&x.full[p.slot], p.parity, &x.abort_flag, a.err); };
+        auto landed = [&](const Spot& p) { return mbar_wait(&x.full[p.slot], p.parity, &x.abort_flag, a.err); };
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             const bool got = mbar_wait(bar, parity, &x.abort_flag, a.err);
             tc_fence_after();
@@ -514,7 +517,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         }
         uint32_t phase = 0;
         for (uint32_t i = 0; ok && i < items; ++i, phase ^= 1) {
-            const Spot<HD> k(2 * i), k1(2 * i + 2), v1(2 * i + 3);
+            const Spot k(2 * i), k1(2 * i + 2), v1(2 * i + 3);
             if (i + 1 < items) {
                 ok = landed(k1) && wait(&x.s_free, phase);
                 if (ok) nt(0, q_at, r_at + k1.slot * S::tile, &x.s_full);
@@ -544,9 +547,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         if (lead) umma_commit(&x.done);
         mbar_wait_drain(&x.done, 0);
     } else if (warp == 10) {
+        started_sync();
         bool ok = true;
         for (uint32_t n = 0; ok && n < 2 * items; ++n) {
-            const Spot<HD> at(n);
+            const Spot at(n);
             const uint32_t i = n >> 1;
             ok = mbar_wait(&x.full[at.slot], at.parity, &x.abort_flag, a.err);
             if (!ok) break;
@@ -560,8 +564,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     } else if (warp < 8) {
         const int w = warp >> 2, row = (warp & 3) * 32 + lane;
         const int32_t n = row0 + row;
-        const uint32_t at = tb + ((uint32_t)((warp & 3) * 32) << 16) + 64 * w;
-        const uint32_t ds_at = tb + ((uint32_t)((warp & 3) * 32) << 16) + kDS + 32 * w;
         const float cs = a.scale * kLog2e;
         {
             // D = dO . O: half a warp per row, 16 rows per warp, all loads in flight together
@@ -594,7 +596,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         }
         const int32_t start = n < a.N ? doc_of(n, a.seg, a.seqlen).x : INT32_MAX;
         const float ls = n < a.N ? -a.lse[(int64_t)head * a.N + n] * kLog2e : 0.f;
-        element_sync();
+        started_sync();                                      // sD is whole, too
+        const uint32_t tb = x.tmem_base;
+        const uint32_t at = tb + ((uint32_t)((warp & 3) * 32) << 16) + 64 * w;
+        const uint32_t ds_at = tb + ((uint32_t)((warp & 3) * 32) << 16) + kDS + 32 * w;
         float dl = -sD[row];
         bool ok = true, met = false;
         uint32_t phase = 0;
@@ -714,28 +719,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             const int32_t r = row0 + warp * 16;
             dq_rows_again(a, head, r, min(16, a.N - r), lane);
         }
+    } else {
+        started_sync();                                      // the twelfth warp
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 8) {
         tc_fence_after();
-        tmem_dealloc(tb, 512);
+        tmem_dealloc(x.tmem_base, 512);
     }
-    if (threadIdx.x == 0) tma_store_wait_all();              // dq has left shared memory
+    if (threadIdx.x == 0) tma_store_wait_read_all();          // dq has left shared memory
 }
 
-template <int HD>
 cudaError_t bwd_wide(const AttnProb& p, const BwdMaps& m, const AttnTcArgs& a, cudaStream_t st) {
-    constexpr uint32_t smem = BwdSmem<HD>::bytes;
-    cudaError_t e = DC_SMEM_LIMIT(attn_dkv_kernel<HD>, smem);
-    if (e == cudaSuccess) e = DC_SMEM_LIMIT(attn_dq_kernel<HD>, smem);
+    constexpr uint32_t smem = BwdSmem::bytes;
+    cudaError_t e = DC_SMEM_LIMIT(attn_dkv_kernel, smem);
+    if (e == cudaSuccess) e = DC_SMEM_LIMIT(attn_dq_kernel, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kRows - 1) / kRows;
-    DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<HD><<<(unsigned)(tiles * p.heads), kBwdThreads, smem, st>>>(m.q, m.k, m.v, m.d,
+    DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<<<(unsigned)(tiles * p.heads), kBwdThreads, smem, st>>>(m.q, m.k, m.v, m.d,
                                                                                                        m.dq, a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int ranks = dkv_ranks(p, tiles * p.kvh);
-    DC_LAUNCH(kAttnTcDkv, st, e = launch_ranks(attn_dkv_kernel<HD>, ranks, (unsigned)(tiles * p.kvh * ranks), kBwdThreads,
+    DC_LAUNCH(kAttnTcDkv, st, e = launch_ranks(attn_dkv_kernel, ranks, (unsigned)(tiles * p.kvh * ranks), kBwdThreads,
                                                smem, st, m.q, m.k, m.v, m.d, m.dk, m.dv, a));
     return e;
 }
@@ -769,7 +775,7 @@ cudaError_t attn_tc_bwd(const AttnProb& p, const void* d_o, const void* q, const
     a.lse = const_cast<float*>(lse);
     a.delta = delta;
     a.err = err;
-    return p.hd <= 64 ? bwd_narrow(p, m, a, st) : bwd_wide<128>(p, m, a, st);
+    return p.hd <= 64 ? bwd_narrow(p, m, a, st) : bwd_wide(p, m, a, st);
 }
 
 }  // namespace dynconv

@@ -33,6 +33,13 @@ namespace {
 
 constexpr int kFwdThreads = 192;
 // The softmax warps' barrier.
+// Barriers and TMEM stand once all have come here; the loading warp only arrives.
+__device__ __forceinline__ void started_arrive() { asm volatile("bar.arrive 2, 192;" ::: "memory"); }
+__device__ __forceinline__ void started_sync() {
+    tc_fence_before();
+    asm volatile("bar.sync 2, 192;" ::: "memory");
+    tc_fence_after();
+}
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 template <int HD>
@@ -91,33 +98,27 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
     const int32_t tiles = (a.N + kRows - 1) / kRows;
     const int32_t row0 = tile_of((int32_t)(blockIdx.x / a.heads), tiles, a.seqlen % kRows ? 0 : a.seqlen / kRows, a.order_q,
                                  false) * kRows;
-    if (threadIdx.x == 0) {
-        mbar_init(&q_full, 1);
-        for (int s = 0; s < S::slots; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        mbar_init(&s_full, 1);
-        mbar_init(&s_free, 4);
-        mbar_init(&p_ready, 4);
-        mbar_init(&pv_done, 1);
-        mbar_init(&drained, 1);
-        abort_flag = 0;
-        again = 0;
-        fence_mbar_init();
-    }
-    if (warp == 4) {
-        tmem_alloc(&tmem_base, 256);
-        tmem_relinquish();
-    }
     const int32_t lo = doc_of(row0, a.seg, a.seqlen).x / kRows;
     const int32_t items = row0 / kRows - lo + 1;             // tiles of keys
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tb = tmem_base;
 
     if (warp == 5) {
+        if (lane == 0) {
+            mbar_init(&q_full, 1);
+            for (int s = 0; s < S::slots; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], 1);
+            }
+            mbar_init(&s_full, 1);
+            mbar_init(&s_free, 4);
+            mbar_init(&p_ready, 4);
+            mbar_init(&pv_done, 1);
+            mbar_init(&drained, 1);
+            abort_flag = 0;
+            again = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        started_arrive();                                    // the loads need no TMEM
         if (lane == 0) {
             mbar_arrive_expect_tx(&q_full, S::tile);
             load_head_tile<HD>(sQ, &tq, &q_full, head, row0);
@@ -136,6 +137,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
         }
         __syncwarp();
     } else if (warp == 4) {
+        tmem_alloc(&tmem_base, 256);
+        tmem_relinquish();
+        started_sync();
+        const uint32_t tb = tmem_base;
         constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);
         constexpr uint32_t kIdO = idesc_bf16(128, HD, false, true);
         const uint32_t q_at = smem_u32(sQ), r_at = smem_u32(ring);
@@ -182,7 +187,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
         // ---- softmax: one row per thread
         const int32_t n = row0 + warp * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        const uint32_t tS = tb + lanes, tP = tS + kP, tO = tS + kO;
+        started_sync();
+        const uint32_t tS = tmem_base + lanes, tP = tS + kP, tO = tS + kO;
         const float cs = a.scale * kLog2e;
         const int32_t full_from = doc_of(min(row0 + kRows, a.N) - 1, a.seg, a.seqlen).x;
         const int32_t start = n < a.N ? doc_of(n, a.seg, a.seqlen).x : INT32_MAX;
@@ -316,9 +322,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
     __syncthreads();
     if (warp == 4) {
         tc_fence_after();
-        tmem_dealloc(tb, 256);
+        tmem_dealloc(tmem_base, 256);
     }
-    if (threadIdx.x == 0) tma_store_wait_all();              // O has left shared memory
+    if (threadIdx.x == 0) tma_store_wait_read_all();          // O has left shared memory
 }
 
 template <int HD>
