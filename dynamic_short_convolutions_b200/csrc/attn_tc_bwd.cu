@@ -69,7 +69,7 @@ struct BwdSmem {
     static_assert(2 * kRows * part_ld<HD>() * sizeof(float) <= stats, "partial gradients fit the tiles");
     struct Shared {
         uint64_t resident, full[slots], empty[slots], stat_full[2], stat_free[2];
-        uint64_t s_full, s_free, dp_full, dp_free, p_ready, ds_ready[2], done, scanned;
+        uint64_t s_full, s_free, dp_full, dp_free, p_ready, ds_ready[2], d_done, done, scanned;
         uint32_t tmem_base;
         int abort_flag, again;
     };
@@ -100,6 +100,7 @@ __device__ __forceinline__ void bwd_init(BwdSmem::Shared& x) {
     mbar_init(&x.p_ready, 8);
     mbar_init(&x.ds_ready[0], 8);
     mbar_init(&x.ds_ready[1], 8);
+    mbar_init(&x.d_done, 8);
     mbar_init(&x.done, 1);
     mbar_init(&x.scanned, 1);
     x.abort_flag = 0;
@@ -450,15 +451,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                                                                  const __grid_constant__ CUtensorMap tk,
                                                                  const __grid_constant__ CUtensorMap tv,
                                                                  const __grid_constant__ CUtensorMap td,
+                                                                 const __grid_constant__ CUtensorMap to,
                                                                  const __grid_constant__ CUtensorMap tdq,
                                                                  const AttnTcArgs a) {
     using S = BwdSmem;
     extern __shared__ __align__(1024) uint8_t sm[];
     uint8_t* sQ = sm;
     uint8_t* sO = sm + S::tile;
-    uint8_t* ring = sm + S::ring;                            // place 2 i: K of item i, 2 i + 1: its V
-    float* sD = reinterpret_cast<float*>(sm + S::stats);     // [128] D, then [2][128] its halves over the last item
-    float* sX = sD + kRows;
+    uint8_t* ring = sm + S::ring;                            // place 0: O, 2 i + 1: K of item i, 2 i + 2: its V
+    float* sX = reinterpret_cast<float*>(sm + S::stats);     // [2][128] halves of a sum over a row
     S::Shared& x = *reinterpret_cast<S::Shared*>(sm + S::shared);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.heads, kv = head / a.group;
@@ -479,8 +480,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             mbar_arrive_expect_tx(&x.resident, 2 * S::tile);
             load_head_tile<HD>(sQ, &tq, &x.resident, head, row0);
             load_head_tile<HD>(sO, &td, &x.resident, head, row0);
-            feed_ring(ring, x, 2 * items, a.err, [&](uint32_t n, uint8_t* to, uint64_t* bar) {
-                load_head_tile<HD>(to, n & 1 ? &tv : &tk, bar, kv, (lo + (int32_t)(n >> 1)) * kRows);
+            feed_ring(ring, x, 2 * items + 1, a.err, [&](uint32_t n, uint8_t* dst, uint64_t* bar) {
+                if (n == 0) load_head_tile<HD>(dst, &to, bar, head, row0);
+                else load_head_tile<HD>(dst, n & 1 ? &tk : &tv, bar, kv, (lo + (int32_t)((n - 1) >> 1)) * kRows);
             });
         }
         __syncwarp();
@@ -508,16 +510,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             tc_fence_after();
             return got;
         };
-        bool ok = wait(&x.resident, 0) && wait(&x.full[0], 0);
-        if (ok) nt(0, q_at, r_at, &x.s_full);
-        ok = ok && wait(&x.full[1], 0);
+        bool ok = wait(&x.resident, 0) && wait(&x.full[1], 0);
+        if (ok) nt(0, q_at, r_at + S::tile, &x.s_full);
+        ok = ok && wait(&x.full[2], 0);
         if (ok) {
-            nt(kDP, o_at, r_at + S::tile, &x.dp_full);
-            if (lead) umma_commit(&x.empty[1]);
+            nt(kDP, o_at, r_at + 2 * S::tile, &x.dp_full);
+            if (lead) umma_commit(&x.empty[2]);
         }
         uint32_t phase = 0;
         for (uint32_t i = 0; ok && i < items; ++i, phase ^= 1) {
-            const Spot k(2 * i), k1(2 * i + 2), v1(2 * i + 3);
+            const Spot k(2 * i + 1), k1(2 * i + 3), v1(2 * i + 4);
             if (i + 1 < items) {
                 ok = landed(k1) && wait(&x.s_free, phase);
                 if (ok) nt(0, q_at, r_at + k1.slot * S::tile, &x.s_full);
@@ -549,12 +551,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     } else if (warp == 10) {
         started_sync();
         bool ok = true;
-        for (uint32_t n = 0; ok && n < 2 * items; ++n) {
+        ok = mbar_wait(&x.d_done, 0, &x.abort_flag, a.err);
+        if (ok && lane == 0) {
+            mbar_arrive(&x.empty[0]);                        // O has been read
+            mbar_arrive(&x.empty[0]);
+        }
+        for (uint32_t n = 1; ok && n < 2 * items + 1; ++n) {
             const Spot at(n);
-            const uint32_t i = n >> 1;
+            const uint32_t i = (n - 1) >> 1;
             ok = mbar_wait(&x.full[at.slot], at.parity, &x.abort_flag, a.err);
             if (!ok) break;
-            if (!(n & 1) && (i == items - 1 || (lo + (int32_t)i) * kRows < full_from) &&
+            if ((n & 1) && (i == items - 1 || (lo + (int32_t)i) * kRows < full_from) &&
                 tile_nonfinite(ring + at.slot * S::tile, S::tile, lane) && lane == 0)
                 x.again = 1;
             __syncwarp();
@@ -565,42 +572,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         const int w = warp >> 2, row = (warp & 3) * 32 + lane;
         const int32_t n = row0 + row;
         const float cs = a.scale * kLog2e;
-        {
-            // D = dO . O: half a warp per row, 16 rows per warp, all loads in flight together
-            uint4 u[8], v[8];
-            const int c = 8 * (lane & 15);
-#pragma unroll
-            for (int it = 0; it < 8; ++it) {
-                const int64_t m = row0 + 16 * warp + 2 * it + (lane >> 4);
-                const bool real = m < a.N && c < a.hd;
-                u[it] = v[it] = make_uint4(0, 0, 0, 0);
-                if (real) {
-                    u[it] = __ldg(reinterpret_cast<const uint4*>(a.o + m * a.os + (int64_t)head * a.hd + c));
-                    v[it] = __ldg(reinterpret_cast<const uint4*>(a.d_o + m * a.dos + (int64_t)head * a.hd + c));
-                }
-            }
-#pragma unroll
-            for (int it = 0; it < 8; ++it) {
-                float d = bf16_lo(u[it].x) * bf16_lo(v[it].x);
-                d = fmaf(bf16_hi(u[it].x), bf16_hi(v[it].x), d);
-                d = fmaf(bf16_lo(u[it].y), bf16_lo(v[it].y), d);
-                d = fmaf(bf16_hi(u[it].y), bf16_hi(v[it].y), d);
-                d = fmaf(bf16_lo(u[it].z), bf16_lo(v[it].z), d);
-                d = fmaf(bf16_hi(u[it].z), bf16_hi(v[it].z), d);
-                d = fmaf(bf16_lo(u[it].w), bf16_lo(v[it].w), d);
-                d = fmaf(bf16_hi(u[it].w), bf16_hi(v[it].w), d);
-#pragma unroll
-                for (int o = 8; o; o >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, o);
-                if ((lane & 15) == 0) sD[16 * warp + 2 * it + (lane >> 4)] = d;
-            }
-        }
         const int32_t start = n < a.N ? doc_of(n, a.seg, a.seqlen).x : INT32_MAX;
         const float ls = n < a.N ? -a.lse[(int64_t)head * a.N + n] * kLog2e : 0.f;
-        started_sync();                                      // sD is whole, too
+        started_sync();
         const uint32_t tb = x.tmem_base;
         const uint32_t at = tb + ((uint32_t)((warp & 3) * 32) << 16) + 64 * w;
         const uint32_t ds_at = tb + ((uint32_t)((warp & 3) * 32) << 16) + kDS + 32 * w;
-        float dl = -sD[row];
         bool ok = true, met = false;
         uint32_t phase = 0;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -614,6 +591,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
+        // D = dO . O of a row, half of the channels by each half of the warps, while the first products run
+        float dl;
+        {
+            wait(&x.resident, 0);
+            ok = ok && wait(&x.full[0], 0);
+            sX[w * kRows + row] = ok ? row_dot(sO + w * kAtom, ring + w * kAtom, row) : 0.f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x.d_done);
+            element_sync();
+            dl = -(sX[row] + sX[kRows + row]);
+            element_sync();                                  // read before the last item's sums lie there
+        }
         auto item = [&](auto with_mask, uint32_t i) {
             constexpr bool kMask = decltype(with_mask)::value;
             const int32_t c0 = (lo + (int32_t)i) * kRows;
@@ -693,7 +682,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             signal(&x.ds_ready[i & 1]);
             return true;
         };
-        for (uint32_t i = 0; i < items; ++i, phase ^= 1) {
+        for (uint32_t i = 0; ok && i < items; ++i, phase ^= 1) {
             const bool masked = i == items - 1 || (lo + (int32_t)i) * kRows < full_from;
             if (!(masked ? item(std::true_type{}, i) : item(std::false_type{}, i))) break;
         }
@@ -737,8 +726,8 @@ cudaError_t bwd_wide(const AttnProb& p, const BwdMaps& m, const AttnTcArgs& a, c
     if (e == cudaSuccess) e = DC_SMEM_LIMIT(attn_dq_kernel, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kRows - 1) / kRows;
-    DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<<<(unsigned)(tiles * p.heads), kBwdThreads, smem, st>>>(m.q, m.k, m.v, m.d,
-                                                                                                       m.dq, a));
+    DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<<<(unsigned)(tiles * p.heads), kBwdThreads, smem, st>>>(m.q, m.k, m.v, m.d, m.o,
+                                                                                                   m.dq, a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int ranks = dkv_ranks(p, tiles * p.kvh);
     DC_LAUNCH(kAttnTcDkv, st, e = launch_ranks(attn_dkv_kernel, ranks, (unsigned)(tiles * p.kvh * ranks), kBwdThreads,
@@ -757,7 +746,7 @@ cudaError_t attn_tc_bwd(const AttnProb& p, const void* d_o, const void* q, const
     if (!make_head_map(&m.q, q, p.N, p.heads, p.hd, p.qs) || !make_head_map(&m.k, k, p.N, p.kvh, p.hd, p.ks) ||
         !make_head_map(&m.v, v, p.N, p.kvh, p.hd, p.vs) || !make_head_map(&m.d, d_o, p.N, p.heads, p.hd, p.dos) ||
         !make_head_map(&m.dq, dq, p.N, p.heads, p.hd, p.dqs) || !make_head_map(&m.dk, dk, p.N, p.kvh, p.hd, p.dks) ||
-        !make_head_map(&m.dv, dv, p.N, p.kvh, p.hd, p.dvs))
+        !make_head_map(&m.dv, dv, p.N, p.kvh, p.hd, p.dvs) || !make_head_map(&m.o, o, p.N, p.heads, p.hd, p.os))
         return cudaErrorInvalidValue;
     if (p.hd <= 64 &&
         (!make_head_map(&m.q64, q, p.N, p.heads, p.hd, p.qs, 64) || !make_head_map(&m.k64, k, p.N, p.kvh, p.hd, p.ks, 64) ||

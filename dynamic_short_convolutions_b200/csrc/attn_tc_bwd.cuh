@@ -78,6 +78,25 @@ __device__ __noinline__ void dq_rows_again(const AttnTcArgs& a, int head, int32_
     }
 }
 
+// Row `row` of two tiles of 64 channels, as TMA laid them out: the sum of their products.
+__device__ __forceinline__ float row_dot(const uint8_t* x, const uint8_t* y, uint32_t row) {
+    float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const uint4 u = *reinterpret_cast<const uint4*>(x + sw128_off(row, c));
+        const uint4 v = *reinterpret_cast<const uint4*>(y + sw128_off(row, c));
+        d0 = fmaf(bf16_lo(u.x), bf16_lo(v.x), d0);
+        d1 = fmaf(bf16_hi(u.x), bf16_hi(v.x), d1);
+        d0 = fmaf(bf16_lo(u.y), bf16_lo(v.y), d0);
+        d1 = fmaf(bf16_hi(u.y), bf16_hi(v.y), d1);
+        d0 = fmaf(bf16_lo(u.z), bf16_lo(v.z), d0);
+        d1 = fmaf(bf16_hi(u.z), bf16_hi(v.z), d1);
+        d0 = fmaf(bf16_lo(u.w), bf16_lo(v.w), d0);
+        d1 = fmaf(bf16_hi(u.w), bf16_hi(v.w), d1);
+    }
+    return d0 + d1;
+}
+
 // Row length of a block's partial gradients in shared memory: padded by 16 bytes, so that a lane per row writes
 // without bank conflicts.
 template <int HD>
@@ -153,7 +172,7 @@ cudaError_t launch_ranks(void (*kernel)(KArgs...), int ranks, unsigned grid, int
 
 // Tensor maps of a backward call: boxes of 128 tokens, and of 64 for the tiles that narrow heads stream.
 struct BwdMaps {
-    CUtensorMap q, k, v, d, dq, dk, dv, q64, k64, v64, d64;
+    CUtensorMap q, k, v, d, o, dq, dk, dv, q64, k64, v64, d64;
 };
 // Head widths up to 64 (attn_tc_bwd64.cu).
 cudaError_t bwd_narrow(const AttnProb& p, const BwdMaps& m, const AttnTcArgs& a, cudaStream_t st);
