@@ -22,12 +22,19 @@
 // rows that see no key outside the diagonal tile it is taken as sum_j P dP instead, which is the same without
 // that rounding (dP - D cancels most where a row sees few keys).
 //
+// attn_dq_kernel is a block per SM that walks its share of the (head, tile) pairs, because a block that came for
+// one pair spent 8 us outside its items (launch, barriers and TMEM, the first loads, the last store) and ~1.4 us on
+// each: now Q of the next pair is loaded once this one's last scores are done, its first scores follow at once,
+// and dO, through whose tile dQ is stored, comes while they are read (16384 tokens, 16 heads of 128: 272 -> 249 us in
+// sequences of 2048, 193 -> 175 in sequences of 1024; writing dQ from the registers, so that dO could come earlier,
+// too: 262 and 185).
+//
 // With few key tiles and large groups the heads of a group are shared out over a cluster of blocks, whose partial
 // dK and dV are added through distributed shared memory in the order of their ranks.
 //
 // Warps: 0-7 the element work (a lane is a row; warps 0-3 take columns 0-63, 4-7 columns 64-127, each
 // writing its bf16 results over columns that it alone has read), 8 MMA issue, 9 TMA, 10 infinities and NaN in
-// masked tiles (see attn_tc_fwd.cu), 11 (dkv) the rows' lse and D.
+// masked tiles (see attn_tc_fwd.cu), 11 (dkv) the rows' lse and D, (dq) the store of dQ.
 //
 // What bounds them is the chain from one item (tile pair) to the next, so every wait on it is moved off:
 // the next scores are computed into S as soon as the element warps hold this item's in registers, the
@@ -70,6 +77,7 @@ struct BwdSmem {
     struct Shared {
         uint64_t resident, full[slots], empty[slots], stat_full[2], stat_free[2];
         uint64_t s_full, s_free, dp_full, dp_free, p_ready, ds_ready[2], d_done, done, scanned;
+        uint64_t q_free, o_full, o_free, staged, drained;             // dq
         uint32_t tmem_base;
         int abort_flag, again;
     };
@@ -103,6 +111,11 @@ __device__ __forceinline__ void bwd_init(BwdSmem::Shared& x) {
     mbar_init(&x.d_done, 8);
     mbar_init(&x.done, 1);
     mbar_init(&x.scanned, 1);
+    mbar_init(&x.q_free, 1);
+    mbar_init(&x.o_full, 1);
+    mbar_init(&x.o_free, 1);
+    mbar_init(&x.staged, 8);
+    mbar_init(&x.drained, 1);
     x.abort_flag = 0;
     x.again = 0;
     fence_mbar_init();
@@ -462,13 +475,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
     float* sX = reinterpret_cast<float*>(sm + S::stats);     // [2][128] halves of a sum over a row
     S::Shared& x = *reinterpret_cast<S::Shared*>(sm + S::shared);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int head = blockIdx.x % a.heads, kv = head / a.group;
-    const int32_t tiles = (a.N + kRows - 1) / kRows;
-    const int32_t row0 = tile_of((int32_t)(blockIdx.x / a.heads), tiles, a.seqlen % kRows ? 0 : a.seqlen / kRows, a.order_q,
-                                 false) * kRows;
-    const int32_t lo = doc_of(row0, a.seg, a.seqlen).x / kRows, hi = row0 / kRows;
-    const int32_t full_from = doc_of(min(row0 + kRows, a.N) - 1, a.seg, a.seqlen).x;
-    const uint32_t items = (uint32_t)(hi - lo + 1);
+    const int32_t tiles = (a.N + kRows - 1) / kRows, total = tiles * a.heads;
+    // The block's tiles: forwards through one stretch of the order (most work first), backwards through the next.
+    struct Tile {
+        int head;
+        int32_t row0, lo, items;
+    };
+    auto tile_at = [&](int32_t t, Tile& c) {
+        const int32_t g = (int32_t)gridDim.x, b = (int32_t)blockIdx.x, u = t * g + (t & 1 ? g - 1 - b : b);
+        if (u >= total) return false;
+        c.head = u % a.heads;
+        c.row0 = tile_of(u / a.heads, tiles, a.seqlen % kRows ? 0 : a.seqlen / kRows, a.order_q, false) * kRows;
+        c.lo = doc_of(c.row0, a.seg, a.seqlen).x / kRows;
+        c.items = c.row0 / kRows - c.lo + 1;
+        return true;
+    };
+    Tile c;
     if (misplaced(sm, a.err)) return;
     constexpr uint32_t kDP = 128, kDQ = 256, kDS = 384;      // dS: two buffers of 64 columns, a barrier each
 
@@ -477,13 +499,42 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         __syncwarp();
         started_arrive();                                    // the loads need no TMEM
         if (lane == 0) {
-            mbar_arrive_expect_tx(&x.resident, 2 * S::tile);
-            load_head_tile<HD>(sQ, &tq, &x.resident, head, row0);
-            load_head_tile<HD>(sO, &td, &x.resident, head, row0);
-            feed_ring(ring, x, 2 * items + 1, a.err, [&](uint32_t n, uint8_t* dst, uint64_t* bar) {
-                if (n == 0) load_head_tile<HD>(dst, &to, bar, head, row0);
-                else load_head_tile<HD>(dst, n & 1 ? &tk : &tv, bar, kv, (lo + (int32_t)((n - 1) >> 1)) * kRows);
-            });
+            uint32_t n = 0;                                  // places of the ring
+            int32_t t = 0, qs = 0, os = 0;                   // tiles begun, Q and dO loaded
+            bool ok = true;
+            auto put = [&](const CUtensorMap* map, int h, int32_t token) {
+                const Spot at(n);
+                if (n >= S::slots && !mbar_wait(&x.empty[at.slot], at.parity ^ 1, &x.abort_flag, a.err)) return false;
+                mbar_arrive_expect_tx(&x.full[at.slot], S::tile);
+                load_head_tile<HD>(ring + at.slot * S::tile, map, &x.full[at.slot], h, token);
+                ++n;
+                return true;
+            };
+            for (; ok && tile_at(t, c); ++t) {
+                if (t > 0) ok = mbar_wait(&x.q_free, (t - 1) & 1, &x.abort_flag, a.err);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&x.resident, S::tile);
+                load_head_tile<HD>(sQ, &tq, &x.resident, c.head, c.row0);
+                ++qs;
+                const int kv = c.head / a.group;
+                ok = put(&to, c.head, c.row0);
+                for (int32_t i = 0; ok && i < c.items; ++i) {
+                    ok = put(&tk, kv, (c.lo + i) * kRows) && put(&tv, kv, (c.lo + i) * kRows);
+                    if (i == 0) {
+                        if (t > 0) ok = ok && mbar_wait(&x.o_free, (t - 1) & 1, &x.abort_flag, a.err);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&x.o_full, S::tile);
+                        load_head_tile<HD>(sO, &td, &x.o_full, c.head, c.row0);
+                        ++os;
+                    }
+                }
+            }
+            if (*(volatile int*)&x.abort_flag) {             // no copy may land after the block has gone
+                if (qs > 0) mbar_wait_drain(&x.resident, (qs - 1) & 1);
+                if (os > 0) mbar_wait_drain(&x.o_full, (os - 1) & 1);
+                for (uint32_t m = n > S::slots ? n - S::slots : 0; m < n; ++m)
+                    mbar_wait_drain(&x.full[Spot(m).slot], Spot(m).parity);
+            }
         }
         __syncwarp();
     } else if (warp == 8) {
@@ -510,76 +561,108 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             tc_fence_after();
             return got;
         };
-        bool ok = wait(&x.resident, 0) && wait(&x.full[1], 0);
-        if (ok) nt(0, q_at, r_at + S::tile, &x.s_full);
-        ok = ok && wait(&x.full[2], 0);
-        if (ok) {
-            nt(kDP, o_at, r_at + 2 * S::tile, &x.dp_full);
-            if (lead) umma_commit(&x.empty[2]);
-        }
-        uint32_t phase = 0;
-        for (uint32_t i = 0; ok && i < items; ++i, phase ^= 1) {
-            const Spot k(2 * i + 1), k1(2 * i + 3), v1(2 * i + 4);
-            if (i + 1 < items) {
-                ok = landed(k1) && wait(&x.s_free, phase);
-                if (ok) nt(0, q_at, r_at + k1.slot * S::tile, &x.s_full);
-                ok = ok && landed(v1) && wait(&x.dp_free, phase);
-                if (ok) {
-                    nt(kDP, o_at, r_at + v1.slot * S::tile, &x.dp_full);
-                    if (lead) umma_commit(&x.empty[v1.slot]);
+        bool ok = true;
+        uint32_t n = 0, g = 0;                               // places of the ring, items
+        for (int32_t t = 0; ok && tile_at(t, c); ++t, n += 2 * c.items + 1) {
+            auto scores = [&](int32_t i) {
+                const Spot k(n + 2 * i + 1);
+                nt(0, q_at, r_at + k.slot * S::tile, &x.s_full);
+                if (lead && i == c.items - 1) umma_commit(&x.q_free);
+            };
+            auto products = [&](int32_t i) {
+                const Spot v(n + 2 * i + 2);
+                nt(kDP, o_at, r_at + v.slot * S::tile, &x.dp_full);
+                if (lead) umma_commit(&x.empty[v.slot]);
+            };
+            // item i: its tile of K or V is there, and the item before has been read out of the columns
+            auto k_there = [&](int32_t i) {
+                return landed(Spot(n + 2 * i + 1)) && (g == 0 && i == 0 || wait(&x.s_free, (g + i - 1) & 1));
+            };
+            auto v_there = [&](int32_t i) {
+                return landed(Spot(n + 2 * i + 2)) && (g == 0 && i == 0 || wait(&x.dp_free, (g + i - 1) & 1));
+            };
+            ok = wait(&x.resident, t & 1) && k_there(0);
+            if (ok) scores(0);
+            ok = ok && wait(&x.o_full, t & 1) && v_there(0);
+            if (ok) products(0);
+            for (int32_t i = 0; ok && i < c.items; ++i) {
+                if (i + 1 < c.items) {
+                    ok = k_there(i + 1);
+                    if (ok) scores(i + 1);
+                    ok = ok && v_there(i + 1);
+                    if (ok) products(i + 1);
                 }
-            }
-            ok = ok && wait(&x.ds_ready[i & 1], (i >> 1) & 1);
-            if (ok && lead) {
-                const uint32_t at = r_at + k.slot * S::tile;
+                const uint32_t b = (g + i) & 1;
+                ok = ok && wait(&x.ds_ready[b], ((g + i) >> 1) & 1);
+                if (ok && lead) {
+                    const Spot k(n + 2 * i + 1);
+                    const uint32_t at = r_at + k.slot * S::tile;
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    umma_ts_bf16(tb + kDQ, tb + kDS + 64 * (i & 1) + 8 * c, mnmajor_desc(at, kAtom, 16 * c), kIdG,
-                                 i > 0 || c > 0);
-                if (i == items - 1) {
-                    // the remainders of the diagonal tile, over the last scores
+                    for (int e = 0; e < 8; ++e)
+                        umma_ts_bf16(tb + kDQ, tb + kDS + 64 * b + 8 * e, mnmajor_desc(at, kAtom, 16 * e), kIdG, i > 0 || e > 0);
+                    if (i == c.items - 1) {
+                        // the remainders of the diagonal tile, over the last scores
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        umma_ts_bf16(tb + kDQ, tb + (c < 4 ? 8 * c : 64 + 8 * (c - 4)), mnmajor_desc(at, kAtom, 16 * c), kIdG, 1);
+                        for (int e = 0; e < 8; ++e)
+                            umma_ts_bf16(tb + kDQ, tb + (e < 4 ? 8 * e : 64 + 8 * (e - 4)), mnmajor_desc(at, kAtom, 16 * e),
+                                         kIdG, 1);
+                    }
+                    umma_commit(&x.empty[k.slot]);
+                    if (i == c.items - 1) umma_commit(&x.done);
                 }
-                umma_commit(&x.empty[k.slot]);
+                __syncwarp();
             }
-            __syncwarp();
+            g += c.items;
         }
-        if (lead) umma_commit(&x.done);
-        mbar_wait_drain(&x.done, 0);
+        if (!ok) {                                           // no product may run on in freed TMEM
+            if (lead) umma_commit(&x.drained);
+            mbar_wait_drain(&x.drained, 0);
+        }
     } else if (warp == 10) {
         started_sync();
         bool ok = true;
-        ok = mbar_wait(&x.d_done, 0, &x.abort_flag, a.err);
-        if (ok && lane == 0) {
-            mbar_arrive(&x.empty[0]);                        // O has been read
-            mbar_arrive(&x.empty[0]);
-        }
-        for (uint32_t n = 1; ok && n < 2 * items + 1; ++n) {
-            const Spot at(n);
-            const uint32_t i = (n - 1) >> 1;
-            ok = mbar_wait(&x.full[at.slot], at.parity, &x.abort_flag, a.err);
+        uint32_t n = 0;
+        for (int32_t t = 0; ok && tile_at(t, c); ++t) {
+            const int32_t full_from = doc_of(min(c.row0 + kRows, a.N) - 1, a.seg, a.seqlen).x;
+            ok = mbar_wait(&x.d_done, t & 1, &x.abort_flag, a.err);
             if (!ok) break;
-            if ((n & 1) && (i == items - 1 || (lo + (int32_t)i) * kRows < full_from) &&
-                tile_nonfinite(ring + at.slot * S::tile, S::tile, lane) && lane == 0)
-                x.again = 1;
+            if (lane == 0) {
+                x.again = 0;                                 // every warp has read the last tile's
+                mbar_arrive(&x.empty[Spot(n).slot]);         // O has been read
+                mbar_arrive(&x.empty[Spot(n).slot]);
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&x.empty[at.slot]);
+            ++n;
+            for (int32_t i = 0; ok && i < 2 * c.items; ++i, ++n) {
+                const Spot at(n);
+                ok = mbar_wait(&x.full[at.slot], at.parity, &x.abort_flag, a.err);
+                if (!ok) break;
+                if (!(i & 1) && (i >> 1 == c.items - 1 || (c.lo + (i >> 1)) * kRows < full_from) &&
+                    tile_nonfinite(ring + at.slot * S::tile, S::tile, lane) && lane == 0)
+                    x.again = 1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x.empty[at.slot]);
+            }
+            if (ok && lane == 0) mbar_arrive(&x.scanned);
         }
-        if (lane == 0) mbar_arrive(&x.scanned);
     } else if (warp < 8) {
         const int w = warp >> 2, row = (warp & 3) * 32 + lane;
-        const int32_t n = row0 + row;
         const float cs = a.scale * kLog2e;
-        const int32_t start = n < a.N ? doc_of(n, a.seg, a.seqlen).x : INT32_MAX;
-        const float ls = n < a.N ? -a.lse[(int64_t)head * a.N + n] * kLog2e : 0.f;
         started_sync();
         const uint32_t tb = x.tmem_base;
         const uint32_t at = tb + ((uint32_t)((warp & 3) * 32) << 16) + 64 * w;
         const uint32_t ds_at = tb + ((uint32_t)((warp & 3) * 32) << 16) + kDS + 32 * w;
-        bool ok = true, met = false;
-        uint32_t phase = 0;
+        bool ok = true, met;
+        uint32_t phase = 0, g = 0, place = 0;                // items, places of the ring before this tile
+        int32_t t = 0, n, start, full_from;
+        float ls, dl;
+        // a row's tile: its token, where its document starts, its lse (log2 units, negated)
+        auto begin = [&]() {
+            n = c.row0 + row;
+            start = n < a.N ? doc_of(n, a.seg, a.seqlen).x : INT32_MAX;
+            ls = n < a.N ? -a.lse[(int64_t)c.head * a.N + n] * kLog2e : 0.f;
+            full_from = doc_of(min(c.row0 + kRows, a.N) - 1, a.seg, a.seqlen).x;
+        };
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = mbar_wait(bar, parity, &x.abort_flag, a.err);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -591,22 +674,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        // D = dO . O of a row, half of the channels by each half of the warps, while the first products run
-        float dl;
-        {
-            wait(&x.resident, 0);
-            ok = ok && wait(&x.full[0], 0);
-            sX[w * kRows + row] = ok ? row_dot(sO + w * kAtom, ring + w * kAtom, row) : 0.f;
+        // D = dO . O
+        auto row_sum = [&]() {
+            const Spot o(place);
+            if (!wait(&x.o_full, t & 1) || !wait(&x.full[o.slot], o.parity)) return false;
+            const uint8_t* so = ring + o.slot * S::tile;
+            dl = -(row_dot(sO, so, row) + row_dot(sO + kAtom, so + kAtom, row));
             __syncwarp();
             if (lane == 0) mbar_arrive(&x.d_done);
-            element_sync();
-            dl = -(sX[row] + sX[kRows + row]);
-            element_sync();                                  // read before the last item's sums lie there
-        }
-        auto item = [&](auto with_mask, uint32_t i) {
+            return true;
+        };
+        auto item = [&](auto with_mask, int32_t i) {
             constexpr bool kMask = decltype(with_mask)::value;
-            const int32_t c0 = (lo + (int32_t)i) * kRows;
-            const bool final = kMask && i == items - 1;
+            const int32_t c0 = (c.lo + i) * kRows;
+            const bool final = kMask && i == c.items - 1;
             const int from = start - c0 - 64 * w, to = n - c0 - 64 * w;
             int see[2] = {kSeeAll, kSeeAll};
             uint32_t bits[2] = {~0u, ~0u};
@@ -637,6 +718,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 }
                 if (kMask && see[b] == kSeeSome) hide32(p[b], bits[b], 0.f);
             }
+            if (i == 0 && !row_sum()) return false;          // while the tiles' loads and products run
             if (!wait(&x.dp_full, phase)) return false;
             tmem_ld32(at + kDP, f[0]);
             tmem_ld32(at + kDP + 32, f[1]);
@@ -661,7 +743,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                 element_sync();
                 met = true;
                 if (start >= c0) dl = -(sX[row] + sX[kRows + row]);
-                if (w == 0 && n < a.N) a.delta[(int64_t)head * a.N + n] = -dl;
+                if (w == 0 && n < a.N) a.delta[(int64_t)c.head * a.N + n] = -dl;
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -672,44 +754,66 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
                         mul2v(f[b][e], f[b][e + 1], p[b][e], p[b][e + 1]);
                     }
                 }
-                store32(ds_at + 64 * (i & 1) + 16 * b, f[b]);
+                store32(ds_at + 64 * ((g + i) & 1) + 16 * b, f[b]);
                 if (final) {
                     remainder32(f[b]);
                     store32(at + 16 * b, f[b]);
                 }
             }
             tmem_wait_st();
-            signal(&x.ds_ready[i & 1]);
+            signal(&x.ds_ready[(g + i) & 1]);
             return true;
         };
-        for (uint32_t i = 0; ok && i < items; ++i, phase ^= 1) {
-            const bool masked = i == items - 1 || (lo + (int32_t)i) * kRows < full_from;
-            if (!(masked ? item(std::true_type{}, i) : item(std::false_type{}, i))) break;
-        }
-        if (!met) element_sync();                            // after an abort: the other warps may wait there
-        ok = ok && wait(&x.done, 0) && wait(&x.scanned, 0);
-        ok = !named_bar_any<1, 256>(!ok);                    // all warps go on, or none
-        if (ok && !x.again) {
-            // each half of the warps takes half of the channels, through Q's tile and TMA
+        bool more = tile_at(0, c);
+        if (more) begin();
+        while (more) {
+            met = false;
+            for (int32_t i = 0; i < c.items; ++i, phase ^= 1) {
+                const bool masked = i == c.items - 1 || (c.lo + i) * kRows < full_from;
+                if (!(masked ? item(std::true_type{}, i) : item(std::false_type{}, i))) break;
+            }
+            if (!met) element_sync();                        // after an abort: the other warps may wait there
+            const Tile now = c;
+            g += c.items;
+            place += 2 * c.items + 1;
+            more = tile_at(t + 1, c);
+            if (more) begin();
+            ok = ok && wait(&x.done, t & 1) && wait(&x.scanned, t & 1);
+            ok = !named_bar_any<1, 256>(!ok);                // all warps go on, or none
+            if (!ok) break;
+            if (!x.again) {
+                // each half of the warps takes half of the channels, through dO's tile
 #pragma unroll
-            for (int b = w * (HD / 64); b < (w + 1) * (HD / 64); ++b) {
-                float f[32];
-                tmem_ld32(tb + ((uint32_t)((warp & 3) * 32) << 16) + kDQ + 32 * b, f);
-                tmem_wait_ld();
-                tile_put32(sQ, row, b, f, a.scale);
+                for (int b = w * (HD / 64); b < (w + 1) * (HD / 64); ++b) {
+                    float f[32];
+                    tmem_ld32(tb + ((uint32_t)((warp & 3) * 32) << 16) + kDQ + 32 * b, f);
+                    tmem_wait_ld();
+                    tile_put32(sO, row, b, f, a.scale);
+                }
+                fence_async_smem();
+            } else {
+                const int32_t r = now.row0 + warp * 16;
+                dq_rows_again(a, now.head, r, min(16, a.N - r), lane);
             }
-            fence_async_smem();
-            element_sync();
-            if (threadIdx.x == 0) {
-                store_head_tile<HD>(&tdq, sQ, head, row0);
-                tma_store_commit();
-            }
-        } else if (ok) {
-            const int32_t r = row0 + warp * 16;
-            dq_rows_again(a, head, r, min(16, a.N - r), lane);
+            signal(&x.staged);
+            ++t;
         }
     } else {
-        started_sync();                                      // the twelfth warp
+        // the store of a tile's dQ, and dO's tile given back
+        started_sync();
+        bool ok = true;
+        for (int32_t t = 0; ok && tile_at(t, c); ++t) {
+            ok = mbar_wait(&x.staged, t & 1, &x.abort_flag, a.err);
+            if (ok && lane == 0) {
+                if (!*(volatile int*)&x.again) {
+                    store_head_tile<HD>(&tdq, sO, c.head, c.row0);
+                    tma_store_commit();
+                    tma_store_wait_read_all();
+                }
+                mbar_arrive(&x.o_free);
+            }
+            __syncwarp();
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -717,7 +821,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1) attn_dq_kernel(const __grid_co
         tc_fence_after();
         tmem_dealloc(x.tmem_base, 512);
     }
-    if (threadIdx.x == 0) tma_store_wait_read_all();          // dq has left shared memory
 }
 
 cudaError_t bwd_wide(const AttnProb& p, const BwdMaps& m, const AttnTcArgs& a, cudaStream_t st) {
@@ -726,7 +829,7 @@ cudaError_t bwd_wide(const AttnProb& p, const BwdMaps& m, const AttnTcArgs& a, c
     if (e == cudaSuccess) e = DC_SMEM_LIMIT(attn_dq_kernel, smem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kRows - 1) / kRows;
-    DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<<<(unsigned)(tiles * p.heads), kBwdThreads, smem, st>>>(m.q, m.k, m.v, m.d, m.o,
+    DC_LAUNCH(kAttnTcDq, st, attn_dq_kernel<<<(unsigned)std::min<int64_t>(tiles * p.heads, num_sms()), kBwdThreads, smem, st>>>(m.q, m.k, m.v, m.d, m.o,
                                                                                                    m.dq, a));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int ranks = dkv_ranks(p, tiles * p.kvh);
