@@ -44,12 +44,13 @@ bool stride_of(int64_t given, int64_t width, int64_t N, int64_t es, int64_t* out
     return *out >= width && fits(std::max<int64_t>(N, 1), *out, es);
 }
 
-// Tokens of a dense batch or a packed run, below 2^31.
+// Tokens of a dense batch or a packed run; a tile past the last token still has 31-bit indices.
+constexpr int64_t kMaxTokens = INT32_MAX - 255;
 dynconv_status tokens_of(int64_t batch, int64_t seqlen, int64_t* N) {
     if (batch < 0 || seqlen < 0) return invalid("negative batch/seqlen");
     if (__builtin_mul_overflow(batch, seqlen, N)) return invalid("batch * seqlen overflows 64 bits");
-    if (*N > INT32_MAX || seqlen > INT32_MAX) {
-        set_error("tokens must number below 2^31");
+    if (*N > kMaxTokens || seqlen > kMaxTokens) {
+        set_error("at most 2^31 - 256 tokens are supported");
         return DYNCONV_ERR_UNSUPPORTED;
     }
     return DYNCONV_OK;

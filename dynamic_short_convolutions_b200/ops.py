@@ -401,6 +401,7 @@ class AttnDecoder:
     def advance(self, kept=None):
         """Adds the tokens kept of the last step to ``lens``: all of them, or ``kept`` (int32 [batch]).  Idle
         slots stay idle.  Kept tokens of a tree have to lie in the cache in order (tokens 0 .. kept - 1)."""
+        _flat(kept, "kept", torch.int32, self.device, (self.batch,))
         self.lens.add_(torch.where(self.lens < 0, 0, self.tokens if kept is None else kept).to(torch.int32))
 
     def reset(self):
@@ -420,7 +421,7 @@ class QKVAttention(torch.autograd.Function):
         wq, wk = heads * head_dim, kv_heads * head_dim
         if C != wq + 2 * wk:
             raise ValueError(f"qkv must be [N, (heads + 2 kv_heads) * head_dim] = [N, {wq + 2 * wk}], got {list(qkv.shape)}")
-        if N % batch:
+        if batch < 1 or N % batch:
             raise ValueError(f"{N} tokens are not {batch} sequences of one length")
         if qkv.stride(1) != 1 or (N > 1 and qkv.stride(0) < C):
             qkv = qkv.contiguous()
@@ -431,22 +432,33 @@ class QKVAttention(torch.autograd.Function):
             qk = RopePlan(qkv.dtype, *rope, x_row_stride=row, device=qkv.device).apply(qk, cu_seqlens=cu_seqlens)
             qk_row = wq + wk
         q, k, v = qk[:, :wq], qk[:, wq:], qkv[:, wq + wk:]
-        plan = AttnPlan(qkv.dtype, batch, N // batch, heads, kv_heads, head_dim, scale, qk_row, qk_row, row, C, C, C,
-                        algo=algo, device=qkv.device)
-        o, lse = plan.forward(q, k, v, cu_seqlens, want_lse=True)
-        ctx.plan, ctx.rope, ctx.width = plan, rope, (C, wq, wk)
-        ctx.save_for_backward(qkv, qk, o, lse, cu_seqlens)
+        # columns that start off a 16-byte boundary (heads of odd widths) are copied out, and their gradients in
+        apart = any(n * qkv.element_size() % 16 for n in (wq, wk))
+        if apart:
+            q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        strides = (0,) * 6 if apart else (qk_row, qk_row, row, C, C, C)
+        plan = AttnPlan(qkv.dtype, batch, N // batch, heads, kv_heads, head_dim, scale, *strides, algo=algo,
+                        device=qkv.device)
+        train = ctx.needs_input_grad[0]
+        o, lse = plan.forward(q, k, v, cu_seqlens, want_lse=True) if train else (plan.forward(q, k, v, cu_seqlens), None)
+        ctx.plan, ctx.rope, ctx.apart, ctx.width = plan, rope, apart, (N, C, wq, wk)
+        if train:
+            ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
         return o
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, go):
-        qkv, qk, o, lse, cu_seqlens = ctx.saved_tensors
-        C, wq, wk = ctx.width
-        d = torch.empty((qkv.shape[0], C), dtype=qkv.dtype, device=qkv.device)
+        q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
+        N, C, wq, wk = ctx.width
+        d = torch.empty((N, C), dtype=q.dtype, device=q.device)
         out = {"dq": d[:, :wq], "dk": d[:, wq:wq + wk], "dv": d[:, wq + wk:]}
-        ctx.plan.backward(go.contiguous(), qk[:, :wq], qk[:, wq:wq + wk], qkv[:, wq + wk:], o, lse, cu_seqlens, out)
+        grads = ctx.plan.backward(go.contiguous(), q, k, v, o, lse, cu_seqlens, None if ctx.apart else out)
+        if ctx.apart:
+            for name, part in out.items():
+                part.copy_(grads[name])
         if ctx.rope is not None:
-            RopePlan(qkv.dtype, *ctx.rope, x_row_stride=C, y_row_stride=C, device=qkv.device).apply(
+            RopePlan(q.dtype, *ctx.rope, x_row_stride=C, y_row_stride=C, device=q.device).apply(
                 d[:, :wq + wk], y=d[:, :wq + wk], cu_seqlens=cu_seqlens, inverse=True)
         return d, None, None, None, None, None, None, None, None, None
 
@@ -455,7 +467,9 @@ def qkv_attention(qkv: torch.Tensor, heads: int, kv_heads: int, head_dim: int, t
                   batch: int = 1, cu_seqlens: Optional[torch.Tensor] = None, scale: float = 0.0,
                   layout: int = L.ROPE_INTERLEAVED, algo: int = L.ALGO_AUTO) -> torch.Tensor:
     """Functional form with autograd: rotary positions (``table``, see :func:`rope_table`) on the Q and K
-    columns of qkv [N, (heads + 2 kv_heads) * head_dim], then causal attention; o [N, heads * head_dim]."""
+    columns of qkv [N, (heads + 2 kv_heads) * head_dim], then causal attention; o [N, heads * head_dim].
+    The table has a row for every position; a packed document that is longer repeats the last one (a
+    :class:`RopePlan` of the caller's own reports that through ``dynconv_device_status``)."""
     return QKVAttention.apply(qkv, table, heads, kv_heads, head_dim, batch, cu_seqlens, scale, layout, algo)
 
 

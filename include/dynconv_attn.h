@@ -13,9 +13,10 @@
  * aligned; a host pointer is DYNCONV_ERR_INVALID); nothing is allocated; work is enqueued
  * on `stream` of the current device and nothing synchronises; arguments are validated
  * before any launch; a row stride of 0 means dense rows.  The workspace is zeroed once
- * before its first use, must not serve two calls that overlap on the device, and holds
- * the device error word that dynconv_device_status(ws, ...) reports and clears.
- * A call may be captured into a CUDA graph.
+ * before its first use, must not serve two calls that overlap on the device (two captured
+ * graphs may share one where they replay one after the other), and holds the device error word that dynconv_device_status(ws, ...) reports and clears.
+ * A call may be captured into a CUDA graph.  But for dynconv_rope in place, no output may
+ * overlap an input.
  */
 #ifndef DYNCONV_ATTN_H
 #define DYNCONV_ATTN_H
@@ -35,7 +36,7 @@ typedef struct {
     int32_t dtype;          /* dynconv_dtype of x and y */
     int32_t layout;         /* dynconv_rope_layout */
     int64_t batch;          /* sequences of seqlen tokens (packed documents: 1) */
-    int64_t seqlen;         /* tokens per sequence (packed documents: all N, below 2^31) */
+    int64_t seqlen;         /* tokens per sequence (packed documents: all N, up to 2^31 - 256) */
     int64_t heads;          /* heads per row */
     int64_t head_dim;       /* channels per head */
     int64_t rot_dim;        /* rotated channels of each head: even, 2..head_dim */
@@ -65,7 +66,7 @@ typedef struct {
     int32_t dtype;          /* dynconv_dtype of every tensor but lse */
     int32_t algo;           /* dynconv_algo: AUTO, SIMT (CUDA cores) or TC (tensor cores) */
     int64_t batch;          /* sequences of seqlen tokens (packed documents: 1) */
-    int64_t seqlen;         /* tokens per sequence (packed documents: all N, below 2^31) */
+    int64_t seqlen;         /* tokens per sequence (packed documents: all N, up to 2^31 - 256) */
     int64_t heads;          /* query heads; query head i reads key/value head i / (heads / kv_heads) */
     int64_t kv_heads;       /* divides heads */
     int64_t head_dim;       /* 1..128 */

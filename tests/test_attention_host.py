@@ -150,3 +150,21 @@ def test_reference_rotation_is_orthogonal_and_its_inverse_undoes_it():
         assert torch.allclose(y.norm(dim=1), x.norm(dim=1), rtol=1e-6)
         assert torch.allclose(rope(y, table, pos, 2, 12, half, inverse=True)[0], x, atol=1e-6)
         assert torch.equal(y[0], x[0]) and torch.equal(y.view(5, 2, 12)[..., 8:], x.view(5, 2, 12)[..., 8:])
+
+
+def test_token_limit():
+    """The last tile of the longest run still has 31-bit indices."""
+    from dynamic_short_convolutions_b200 import _lib as L
+
+    most = (1 << 31) - 256
+    assert L.dynconv_attn_workspace_bytes(_desc(batch=1, seqlen=most, heads=1, kv=1, hd=8)) > 0
+    assert L.dynconv_attn_workspace_bytes(_desc(batch=1, seqlen=most + 1, heads=1, kv=1, hd=8)) == 0
+    assert "2^31 - 256" in L.dynconv_last_error()
+
+
+def test_sequences_have_to_share_the_tokens():
+    from dynamic_short_convolutions_b200 import ops
+
+    for batch in (0, -1, 3):
+        with pytest.raises(ValueError):
+            ops.qkv_attention(torch.zeros((8, 512)), 4, 2, 64, batch=batch)
