@@ -201,6 +201,15 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
+// A thread's part of an accumulator row into shared memory.
+template <int HD>
+__device__ __forceinline__ void put_row(float* row, const float (&acc)[HD / 16], int tx) {
+#pragma unroll
+    for (int jj = 0; jj < HD / 64; ++jj)
+        *reinterpret_cast<float4*>(row + 4 * tx + 64 * jj) =
+            make_float4(acc[4 * jj], acc[4 * jj + 1], acc[4 * jj + 2], acc[4 * jj + 3]);
+}
+
 template <typename T, int HD>
 __device__ __forceinline__ void store_rows(T* dst, int64_t stride, int32_t row0, int32_t N, int hd,
                                            const float (&acc)[4][HD / 16], const float (&mul)[4], int ty, int tx) {
@@ -228,10 +237,12 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const T* __rest
     float* sQ = sm;
     float* ring = sQ + kTile * LD;         // stage s: K at ring + 2 s tiles, V behind it
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    const int head = blockIdx.x % a.heads, kv = head / a.group;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int head = (int)(blockIdx.x / ranks) % a.heads, kv = head / a.group;
     const int32_t tiles = (a.N + kTile - 1) / kTile;
-    const int32_t row0 = tile_of((int32_t)(blockIdx.x / a.heads), tiles, a.seqlen % kTile ? 0 : a.seqlen / kTile, a.order_q,
-                                 false) * kTile;
+    const int32_t row0 = tile_of((int32_t)(blockIdx.x / ranks / a.heads), tiles, a.seqlen % kTile ? 0 : a.seqlen / kTile,
+                                 a.order_q, false) * kTile;
     q += (int64_t)head * a.hd;
     o += (int64_t)head * a.hd;
     k += (int64_t)kv * a.hd;
@@ -258,12 +269,13 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const T* __rest
         }
         copies_close();
     };
-    const int32_t k_first = first_key / kTile * kTile;
+    // this block's tiles of keys: every ranks-th
+    const int32_t k_first = (first_key / kTile + rank) * kTile, step = ranks * kTile;
     if (NS == 2) fetch(k_first, 0);
     int at = 0;
-    for (int32_t k0 = k_first; k0 <= last; k0 += kTile, at ^= NS - 1) {
+    for (int32_t k0 = k_first; k0 <= last; k0 += step, at ^= NS - 1) {
         __syncthreads();                   // the stage fetched into now is read
-        fetch(NS == 2 ? k0 + kTile : k0, NS == 2 ? at ^ 1 : 0);
+        fetch(NS == 2 ? k0 + step : k0, NS == 2 ? at ^ 1 : 0);
         copies_wait<NS - 1>();
         __syncthreads();
         const float* sK = ring + 2 * at * kTile * LD;
@@ -307,6 +319,41 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const T* __rest
         if (odd) tile_nn<HD, true>(sP, sV, acc, ty, tx, lo, hi);
         else tile_nn<HD, false>(sP, sV, acc, ty, tx, lo, hi);
     }
+    if (ranks > 1) {
+        // partial rows of the cluster's blocks, joined in the order of their ranks, each block a share of the rows
+        copies_wait<0>();
+        __syncthreads();
+        float* stat = sQ + kTile * LD;                       // in the ring: m, then l of a row
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            l[i] = row_sum(l[i]);
+            put_row<HD>(sQ + (4 * ty + i) * LD, acc[i], tx);
+            if (tx == 0) {
+                stat[4 * ty + i] = m[i];
+                stat[kTile + 4 * ty + i] = l[i];
+            }
+        }
+        cluster.sync();
+        const int per = kTile / ranks;
+        for (int i = threadIdx.x; i < per * HD; i += kThreads) {
+            const int r = rank * per + i / HD, c = i % HD;
+            float mx = -INFINITY, sum = 0.f, x = 0.f;
+            for (int n = 0; n < ranks; ++n) mx = fmaxf(mx, cluster.map_shared_rank(stat, n)[r]);
+            const float use = mx == -INFINITY ? 0.f : mx;
+            for (int n = 0; n < ranks; ++n) {
+                const float* part = cluster.map_shared_rank(sQ, n);
+                const float w = exp2f(part[kTile * LD + r] - use);
+                sum = fmaf(w, part[kTile * LD + kTile + r], sum);
+                x = fmaf(w, part[r * LD + c], x);
+            }
+            const int32_t n = row0 + r;
+            if (n >= a.N) continue;
+            if (c < a.hd) o[(int64_t)n * a.os + c] = from_f32<T>(x * (sum > 0.f ? 1.f / sum : sum));
+            if (lse != nullptr && c == 0) lse[(int64_t)head * a.N + n] = (mx + log2f(sum)) * kLn2;
+        }
+        cluster.sync();                    // no block leaves while its part is read
+        return;
+    }
     float inv[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -331,10 +378,12 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restr
     float* sO = sQ + kTile * LD;
     float* ring = sO + kTile * LD;         // stage s: K at ring + 2 s tiles, V behind it
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    const int head = blockIdx.x % a.heads, kv = head / a.group;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int head = (int)(blockIdx.x / ranks) % a.heads, kv = head / a.group;
     const int32_t tiles = (a.N + kTile - 1) / kTile;
-    const int32_t row0 = tile_of((int32_t)(blockIdx.x / a.heads), tiles, a.seqlen % kTile ? 0 : a.seqlen / kTile, a.order_q,
-                                 false) * kTile;
+    const int32_t row0 = tile_of((int32_t)(blockIdx.x / ranks / a.heads), tiles, a.seqlen % kTile ? 0 : a.seqlen / kTile,
+                                 a.order_q, false) * kTile;
     load_tile<T, HD>(sQ, q + (int64_t)head * a.hd, a.qs, row0, a.N, a.hd, vec);
     load_tile<T, HD>(sO, d_o + (int64_t)head * a.hd, a.dos, row0, a.N, a.hd, vec);
     k += (int64_t)kv * a.hd;
@@ -362,12 +411,13 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restr
         }
         copies_close();
     };
-    const int32_t k_first = first_key / kTile * kTile;
+    // this block's tiles of keys: every ranks-th
+    const int32_t k_first = (first_key / kTile + rank) * kTile, step = ranks * kTile;
     if (NS == 2) fetch(k_first, 0);
     int at = 0;
-    for (int32_t k0 = k_first; k0 <= last; k0 += kTile, at ^= NS - 1) {
+    for (int32_t k0 = k_first; k0 <= last; k0 += step, at ^= NS - 1) {
         __syncthreads();                   // the stage fetched into now is read
-        fetch(NS == 2 ? k0 + kTile : k0, NS == 2 ? at ^ 1 : 0);
+        fetch(NS == 2 ? k0 + step : k0, NS == 2 ? at ^ 1 : 0);
         copies_wait<NS - 1>();
         __syncthreads();
         const float* sK = ring + 2 * at * kTile * LD;
@@ -395,7 +445,25 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restr
         if (odd) tile_nn<HD, true>(sD, sK, acc, ty, tx, lo, hi);
         else tile_nn<HD, false>(sD, sK, acc, ty, tx, lo, hi);
     }
-    store_rows<T, HD>(dq + (int64_t)head * a.hd, a.dqs, row0, a.N, a.hd, acc, mul, ty, tx);
+    dq += (int64_t)head * a.hd;
+    if (ranks == 1) {
+        store_rows<T, HD>(dq, a.dqs, row0, a.N, a.hd, acc, mul, ty, tx);
+        return;
+    }
+    // partial sums of the cluster's blocks, as in the forward
+    copies_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put_row<HD>(sQ + (4 * ty + i) * LD, acc[i], tx);
+    cluster.sync();
+    const int per = kTile / ranks;
+    for (int i = threadIdx.x; i < per * HD; i += kThreads) {
+        const int r = rank * per + i / HD, c = i % HD;
+        float x = 0.f;
+        for (int n = 0; n < ranks; ++n) x += cluster.map_shared_rank(sQ, n)[r * LD + c];
+        if (row0 + r < a.N && c < a.hd) dq[(int64_t)(row0 + r) * a.dqs + c] = from_f32<T>(x * a.scale);
+    }
+    cluster.sync();
 }
 
 // dk and dv of 64 keys of one key/value head: every head of the group, every tile of queries that sees
@@ -496,13 +564,10 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __rest
     // partial sums of the cluster's blocks, added in the order of their ranks, each block a share of the rows
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int jj = 0; jj < HD / 64; ++jj) {
-            const int at = (4 * ty + i) * LD + 4 * tx + 64 * jj;
-            *reinterpret_cast<float4*>(sQ + at) = make_float4(acck[i][4 * jj], acck[i][4 * jj + 1], acck[i][4 * jj + 2], acck[i][4 * jj + 3]);
-            *reinterpret_cast<float4*>(sO + at) = make_float4(accv[i][4 * jj], accv[i][4 * jj + 1], accv[i][4 * jj + 2], accv[i][4 * jj + 3]);
-        }
+    for (int i = 0; i < 4; ++i) {
+        put_row<HD>(sQ + (4 * ty + i) * LD, acck[i], tx);
+        put_row<HD>(sO + (4 * ty + i) * LD, accv[i], tx);
+    }
     cluster.sync();
     const int per = kTile / ranks;
     for (int i = threadIdx.x; i < per * HD; i += kThreads) {
@@ -548,17 +613,40 @@ int vec_ok(const AttnProb& p, bool bwd) {
     return p.hd % 4 == 0 && p.qs % 4 == 0 && p.ks % 4 == 0 && p.vs % 4 == 0 && (!bwd || p.dos % 4 == 0);
 }
 
+// Blocks of a cluster that share the work of one tile: a power of two up to `most`, while `blocks` tiles do not give
+// each multiprocessor three.
+int ranks_of(int64_t blocks, int most) {
+    int ranks = 1;
+    while (ranks * 2 <= std::min(most, 8) && blocks * ranks < 3 * num_sms()) ranks *= 2;
+    return ranks;
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), int64_t blocks, int ranks, size_t smem, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks * ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ranks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <typename T, int HD>
 cudaError_t fwd_t(const AttnProb& p, const void* q, const void* k, const void* v, void* o, float* lse,
                   cudaStream_t st) {
     constexpr size_t smem = sizeof(float) * (1 + 2 * stages_of<HD>()) * kTile * ld_of<HD>();
     cudaError_t e = DC_SMEM_LIMIT((attn_fwd_simt_kernel<T, HD>), smem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)((p.N + kTile - 1) / kTile * p.heads);
-    DC_LAUNCH(kAttnSimtFwd, st, attn_fwd_simt_kernel<T, HD><<<grid, kThreads, smem, st>>>(
-                                    static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
-                                    static_cast<T*>(o), lse, args_of(p), vec_ok(p, false)));
-    return cudaGetLastError();
+    const int64_t blocks = (p.N + kTile - 1) / kTile * p.heads;
+    DC_LAUNCH(kAttnSimtFwd, st, e = launch(attn_fwd_simt_kernel<T, HD>, blocks, ranks_of(blocks, 8), smem, st,
+                                           static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
+                                           static_cast<T*>(o), lse, args_of(p), vec_ok(p, false)));
+    return e;
 }
 
 template <typename T, int HD>
@@ -570,29 +658,16 @@ cudaError_t bwd_t(const AttnProb& p, const void* d_o, const void* q, const void*
     if (e == cudaSuccess) e = DC_SMEM_LIMIT((attn_dkv_simt_kernel<T, HD>), smem_kv);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kTile - 1) / kTile;
-    int ranks = 1;
-    while (ranks * 2 <= std::min(p.group, 8) && tiles * p.kvh * ranks < 2 * num_sms()) ranks *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * p.kvh * ranks));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_kv;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = ranks > 1 ? 1 : 0;
-    DC_LAUNCH(kAttnSimtDkv, st, e = cudaLaunchKernelEx(&cfg, attn_dkv_simt_kernel<T, HD>, static_cast<const T*>(d_o),
-                                                       static_cast<const T*>(q), static_cast<const T*>(k),
-                                                       static_cast<const T*>(v), lse, delta, static_cast<T*>(dk),
-                                                       static_cast<T*>(dv), args_of(p), vec_ok(p, true)));
+    const T *td = static_cast<const T*>(d_o), *tq = static_cast<const T*>(q), *tk = static_cast<const T*>(k),
+            *tv = static_cast<const T*>(v);
+    DC_LAUNCH(kAttnSimtDkv, st, e = launch(attn_dkv_simt_kernel<T, HD>, tiles * p.kvh, ranks_of(tiles * p.kvh, p.group),
+                                           smem_kv, st, td, tq, tk, tv, lse, delta, static_cast<T*>(dk),
+                                           static_cast<T*>(dv), args_of(p), vec_ok(p, true)));
     if (e != cudaSuccess) return e;
-    DC_LAUNCH(kAttnSimtDq, st, attn_dq_simt_kernel<T, HD><<<(unsigned)(tiles * p.heads), kThreads, smem_q, st>>>(
-                                   static_cast<const T*>(d_o), static_cast<const T*>(q), static_cast<const T*>(k),
-                                   static_cast<const T*>(v), lse, delta, static_cast<T*>(dq), args_of(p),
-                                   vec_ok(p, true)));
-    return cudaGetLastError();
+    DC_LAUNCH(kAttnSimtDq, st, e = launch(attn_dq_simt_kernel<T, HD>, tiles * p.heads, ranks_of(tiles * p.heads, 8), smem_q,
+                                          st, td, tq, tk, tv, lse, delta, static_cast<T*>(dq), args_of(p),
+                                          vec_ok(p, true)));
+    return e;
 }
 
 }  // namespace
