@@ -467,8 +467,7 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(const T* __restr
 }
 
 // dk and dv of 64 keys of one key/value head: every head of the group, every tile of queries that sees
-// a key of the tile, in order (no atomics).  Scores are held transposed: rows are keys.  With few key tiles the
-// heads of a group are shared out over a cluster of blocks.
+// a key of the tile, in order (no atomics).  Scores are held transposed: rows are keys.
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __restrict__ d_o, const T* __restrict__ q,
                                                                  const T* __restrict__ k, const T* __restrict__ v,
@@ -505,53 +504,60 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __rest
         for (int c = 0; c < HD / 16; ++c) acck[i][c] = accv[i][c] = 0.f;
     }
     const float cs = a.scale * kLog2e;
-    // this block's heads of the group
-    for (int head = kv * a.group + rank * a.group / ranks; head < kv * a.group + (rank + 1) * a.group / ranks; ++head) {
-        for (int32_t q0 = row0; q0 < e_last; q0 += kTile) {
-            __syncthreads();
-            fetch_tile<T, HD>(sQ, q + (int64_t)head * a.hd, a.qs, q0, a.N, a.hd, vec);
-            fetch_tile<T, HD>(sO, d_o + (int64_t)head * a.hd, a.dos, q0, a.N, a.hd, vec);
-            copies_close();
-            float ls[4], dl[4];
+    // this block's (head, tile of queries) pairs: every ranks-th
+    int head = kv * a.group;
+    int32_t q0 = row0 + rank * kTile;
+    const int32_t rows = (e_last - row0 + kTile - 1) / kTile * kTile;
+    auto settle = [&]() {
+        while (q0 >= row0 + rows) {
+            q0 -= rows;
+            ++head;
+        }
+    };
+    for (settle(); head < (kv + 1) * a.group; q0 += ranks * kTile, settle()) {
+        __syncthreads();
+        fetch_tile<T, HD>(sQ, q + (int64_t)head * a.hd, a.qs, q0, a.N, a.hd, vec);
+        fetch_tile<T, HD>(sO, d_o + (int64_t)head * a.hd, a.dos, q0, a.N, a.hd, vec);
+        copies_close();
+        float ls[4], dl[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int32_t n = min(q0 + tx + 16 * j, a.N - 1);
+            ls[j] = lse[(int64_t)head * a.N + n] * kLog2e;
+            dl[j] = delta[(int64_t)head * a.N + n];
+        }
+        copies_wait<0>();
+        __syncthreads();
+        float s[4][4], dp[4][4];
+        tile_nt<HD>(sK, sQ, s, ty, tx);
+        tile_nt<HD>(sV, sO, dp, ty, tx);
+        const bool masked = q0 < row0 + kTile || q0 + kTile > first_end;
+        int lo[4], hi[4];
+        bool odd = false;
+        if (masked) {
+            odd = tile_odd<HD>(sQ, true);
+            odd = tile_odd<HD>(sO, true) || odd;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = row0 + 4 * ty + i - q0;
+            hi[i] = end[i] - 1 - q0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int32_t n = min(q0 + tx + 16 * j, a.N - 1);
-                ls[j] = lse[(int64_t)head * a.N + n] * kLog2e;
-                dl[j] = delta[(int64_t)head * a.N + n];
+                const int c = tx + 16 * j;
+                const float p = exp2f(fmaf(s[i][j], cs, -ls[j]));
+                const bool hide = masked && (c < lo[i] || c > hi[i]);
+                sP[(4 * ty + i) * kLdP + c] = hide ? 0.f : p;
+                sD[(4 * ty + i) * kLdP + c] = hide ? 0.f : p * (dp[i][j] - dl[j]);
             }
-            copies_wait<0>();
-            __syncthreads();
-            float s[4][4], dp[4][4];
-            tile_nt<HD>(sK, sQ, s, ty, tx);
-            tile_nt<HD>(sV, sO, dp, ty, tx);
-            const bool masked = q0 < row0 + kTile || q0 + kTile > first_end;
-            int lo[4], hi[4];
-            bool odd = false;
-            if (masked) {
-                odd = tile_odd<HD>(sQ, true);
-                odd = tile_odd<HD>(sO, true) || odd;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lo[i] = row0 + 4 * ty + i - q0;
-                hi[i] = end[i] - 1 - q0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int c = tx + 16 * j;
-                    const float p = exp2f(fmaf(s[i][j], cs, -ls[j]));
-                    const bool hide = masked && (c < lo[i] || c > hi[i]);
-                    sP[(4 * ty + i) * kLdP + c] = hide ? 0.f : p;
-                    sD[(4 * ty + i) * kLdP + c] = hide ? 0.f : p * (dp[i][j] - dl[j]);
-                }
-            }
-            __syncthreads();
-            if (odd) {
-                tile_nn<HD, true>(sP, sO, accv, ty, tx, lo, hi);
-                tile_nn<HD, true>(sD, sQ, acck, ty, tx, lo, hi);
-            } else {
-                tile_nn<HD, false>(sP, sO, accv, ty, tx, lo, hi);
-                tile_nn<HD, false>(sD, sQ, acck, ty, tx, lo, hi);
-            }
+        }
+        __syncthreads();
+        if (odd) {
+            tile_nn<HD, true>(sP, sO, accv, ty, tx, lo, hi);
+            tile_nn<HD, true>(sD, sQ, acck, ty, tx, lo, hi);
+        } else {
+            tile_nn<HD, false>(sP, sO, accv, ty, tx, lo, hi);
+            tile_nn<HD, false>(sD, sQ, acck, ty, tx, lo, hi);
         }
     }
     dk += (int64_t)kv * a.hd;
@@ -562,6 +568,8 @@ __global__ void __launch_bounds__(kThreads) attn_dkv_simt_kernel(const T* __rest
         return;
     }
     // partial sums of the cluster's blocks, added in the order of their ranks, each block a share of the rows
+    copies_close();
+    copies_wait<0>();
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -613,11 +621,14 @@ int vec_ok(const AttnProb& p, bool bwd) {
     return p.hd % 4 == 0 && p.qs % 4 == 0 && p.ks % 4 == 0 && p.vs % 4 == 0 && (!bwd || p.dos % 4 == 0);
 }
 
-// Blocks of a cluster that share the work of one tile: a power of two up to `most`, while `blocks` tiles do not give
-// each multiprocessor three.
-int ranks_of(int64_t blocks, int most) {
+// Blocks of a cluster that share the work of one tile: a power of two up to 8, while the grid has fewer blocks than
+// `halves` / 2 per multiprocessor: 3 for the forward and dq, two of whose blocks fit a multiprocessor, 1.5 for dk and
+// dv, where one does.  Measured (fp32, 64 channels; one block a tile, then by this rule; forward / dk and dv / dq, us):
+// one sequence of 1024, 4 heads 93 / 157 / 126, 46 / 65 / 57; of 2048, 4 heads over 2: 178 / 308 / 243, 99 / 177 / 130;
+// 5 documents of about 550, 8 over 2: dq 134, 121.  With twice the limit: 116 / 222 / 149 at the second.
+int ranks_of(int64_t blocks, int halves) {
     int ranks = 1;
-    while (ranks * 2 <= std::min(most, 8) && blocks * ranks < 3 * num_sms()) ranks *= 2;
+    while (ranks < 8 && 2 * blocks * ranks < halves * num_sms()) ranks *= 2;
     return ranks;
 }
 template <typename... KArgs, typename... Args>
@@ -643,7 +654,7 @@ cudaError_t fwd_t(const AttnProb& p, const void* q, const void* k, const void* v
     cudaError_t e = DC_SMEM_LIMIT((attn_fwd_simt_kernel<T, HD>), smem);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (p.N + kTile - 1) / kTile * p.heads;
-    DC_LAUNCH(kAttnSimtFwd, st, e = launch(attn_fwd_simt_kernel<T, HD>, blocks, ranks_of(blocks, 8), smem, st,
+    DC_LAUNCH(kAttnSimtFwd, st, e = launch(attn_fwd_simt_kernel<T, HD>, blocks, ranks_of(blocks, 6), smem, st,
                                            static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
                                            static_cast<T*>(o), lse, args_of(p), vec_ok(p, false)));
     return e;
@@ -660,11 +671,11 @@ cudaError_t bwd_t(const AttnProb& p, const void* d_o, const void* q, const void*
     const int64_t tiles = (p.N + kTile - 1) / kTile;
     const T *td = static_cast<const T*>(d_o), *tq = static_cast<const T*>(q), *tk = static_cast<const T*>(k),
             *tv = static_cast<const T*>(v);
-    DC_LAUNCH(kAttnSimtDkv, st, e = launch(attn_dkv_simt_kernel<T, HD>, tiles * p.kvh, ranks_of(tiles * p.kvh, p.group),
+    DC_LAUNCH(kAttnSimtDkv, st, e = launch(attn_dkv_simt_kernel<T, HD>, tiles * p.kvh, ranks_of(tiles * p.kvh, 3),
                                            smem_kv, st, td, tq, tk, tv, lse, delta, static_cast<T*>(dk),
                                            static_cast<T*>(dv), args_of(p), vec_ok(p, true)));
     if (e != cudaSuccess) return e;
-    DC_LAUNCH(kAttnSimtDq, st, e = launch(attn_dq_simt_kernel<T, HD>, tiles * p.heads, ranks_of(tiles * p.heads, 8), smem_q,
+    DC_LAUNCH(kAttnSimtDq, st, e = launch(attn_dq_simt_kernel<T, HD>, tiles * p.heads, ranks_of(tiles * p.heads, 6), smem_q,
                                           st, td, tq, tk, tv, lse, delta, static_cast<T*>(dq), args_of(p),
                                           vec_ok(p, true)));
     return e;
