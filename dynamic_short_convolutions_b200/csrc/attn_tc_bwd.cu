@@ -43,8 +43,8 @@
 // tensor cores waiting for L2: 4250 cycles per item instead of ~2500).
 //   dkv: S(i+1) | dV(i) | dK(i) dP(i+1)    P and dS lie in the columns of dP, read into registers before
 //   dq:  S(i+1) | dP(i+1) | dQ(i)          dS has two buffers of its own
-// Measured at 16384 tokens, 16 heads of 128 over 4, in sequences of 2048: dkv 260 us (540 TFLOP/s of its four products,
-// 1.8 us per item), dq 249 (420 of its three, 1.4 us per item); 9 documents of 346 to 2716 tokens: 199 and 157.
+// Measured at 16384 tokens, 16 heads of 128 over 4, in sequences of 2048: dkv 260 us (1057 TFLOP/s of its four products,
+// 1.8 us per item), dq 249 (828 of its three, 1.4 us per item); 9 documents of 346 to 2716 tokens: 199 and 157.
 #include <algorithm>
 #include <type_traits>
 

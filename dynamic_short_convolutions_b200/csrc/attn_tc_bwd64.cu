@@ -7,7 +7,7 @@
 // items are 128 rows x 64 columns, so that S, dP and the gradients fit 256 columns:
 //   dkv: S 64, dP 64, dV 64, dK 64; P lies over S, dS over dP, dS's remainder behind it
 //   dq:  S 64, dP 64, dQ 64, dS two buffers of 32; dS's remainder over S
-// Measured at 8 sequences of 2048, 12 heads: dkv 166 us (204 as one block per SM with items of 128 x 128), dq 122 (160);
+// Measured at 8 sequences of 2048, 12 heads: dkv 166 us (620 TFLOP/s; 204 us as one block per SM with items of 128 x 128), dq 122 (633; 160);
 // an item takes 1.5 and 0.9 us of a block's time, what is outside the items about 8 us per block.  Both loads of scores
 // and dP before the exponentials made dq 142; D from tiles by TMA, as the wide kernel does it, 123.
 //
