@@ -26,6 +26,7 @@
 #include <algorithm>
 
 #include "attn.h"
+#include "attn_places.cuh"
 #include "common.cuh"
 #include "prof.h"
 #include "smem_limit.h"

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "attn.h"
+#include "attn_places.cuh"
 #include "common.cuh"
 #include "tc_common.cuh"
 #include "tmap.h"
