@@ -469,7 +469,9 @@ def qkv_attention(qkv: torch.Tensor, heads: int, kv_heads: int, head_dim: int, t
     """Functional form with autograd: rotary positions (``table``, see :func:`rope_table`) on the Q and K
     columns of qkv [N, (heads + 2 kv_heads) * head_dim], then causal attention; o [N, heads * head_dim].
     The table has a row for every position; a packed document that is longer repeats the last one (a
-    :class:`RopePlan` of the caller's own reports that through ``dynconv_device_status``)."""
+    :class:`RopePlan` of the caller's own reports that through ``dynconv_device_status``).  Calls and their
+    backward may be captured into a CUDA graph; as for any autograd function, no eager graph of the same leaves may
+    be alive then."""
     return QKVAttention.apply(qkv, table, heads, kv_heads, head_dim, batch, cu_seqlens, scale, layout, algo)
 
 
