@@ -19,10 +19,11 @@
 // q is kept as two bf16 (value and remainder), since nothing else rounds it.  fp32: FMAs, a warp per four rows.
 //
 // Measured: 64 sequences of ~3000 rows, 16 heads of 128 over 4, one token: 72 us, 5.57 TB/s (0.85 of the copy rate; 88
-// on 16-row tiles); one of ~700 rows, 12 heads of 64: 8.4 us, the chain length, rows, softmax, join; 13 of ~560 rows,
-// 3 tokens, fp32: 17.3 us (0.44 TB/s: 6 rows a key, each an FMA and shared-memory chain).
+// on 16-row tiles); one of ~700 rows, 12 heads of 64: 8.4 us, the chain length, rows, softmax, join.
+// fp32: the first 154 us (5.1 TB/s, 0.78), the second 11.3, 13 of ~560 rows with 3 tokens and 4 heads a group 14.6.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "attn_decode.cuh"
 #include "prof.h"
@@ -544,23 +545,30 @@ __global__ void __launch_bounds__(kThreads) attn_decode8_kernel(const __grid_con
 
 // ---------------------------------------------------------------- fp32
 constexpr int kTokF = 32;
-constexpr int kRowsF = 16;                           // four rows per warp
 
-template <int HD>
+// Four rows per warp; TW warps share the tokens of a tile where the rows do not fill the block (64 x 3000 cached rows,
+// 16 heads of 128 over 4, one token: 345 us where one warp of four worked, 173 with TW = 4).  The probabilities go
+// to the value loop through shared memory, four rows in a load: 154 us, with shuffles and a test per row 173.
+template <int HD, int TW>
 __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* __restrict__ q,
                                                                    const float* __restrict__ k,
                                                                    const float* __restrict__ v, float* k_cache,
                                                                    float* v_cache, float* __restrict__ o,
                                                                    const DecArgs a) {
     constexpr int C = HD / 4, E = HD / 32;                       // 16-byte chunks per row; channels per lane
+    constexpr int ROWS = TW == 1 ? 16 : 8, NT = kTokF / TW;      // rows of a block; tokens of a warp per tile
     constexpr uint32_t kHalf = kTokF * HD * 4;
     extern __shared__ __align__(128) uint8_t sm[];
-    __shared__ __align__(16) float sq[kRowsF][HD];
-    __shared__ float smax[kRowsF], ssum[kRowsF];
+    __shared__ __align__(16) float sq[ROWS][HD];
+    __shared__ float4 sp[kThreads / 32][NT];                     // a tile's probabilities
+    __shared__ float smax[TW * ROWS], ssum[TW * ROWS];
     __shared__ uint64_t seen[64];
     __shared__ const float* turn[64];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Place p = place_of<kRowsF>(a, kTokF);
+    const int tw = TW == 1 ? 0 : warp % TW, r0 = warp / TW * 4;  // a warp's share of the tokens; its rows
+    // scores: a lane's token, its part of the channels
+    const int tok = TW == 1 ? lane : tw * NT + lane % NT, part = TW == 1 ? 0 : lane / NT;
+    Place p = place_of<ROWS>(a, kTokF);
     const int64_t slot = (p.b * a.kvh + p.kv) * a.max_len;
     const uint32_t ring = smem_at(sm);
     const int tiles = (int)((p.to - p.from + kTokF - 1) / kTokF);
@@ -587,12 +595,12 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
     }
     if (p.idle) {
         copies_wait<0>();
-        zero_rows<float, kRowsF>(a, p, o);
+        zero_rows<float, ROWS>(a, p, o);
         return;
     }
 #pragma unroll 4
-    for (int i = threadIdx.x; i < kRowsF * C; i += kThreads) {
-        const int r = i / C, c = i % C, row = p.tile * kRowsF + r;
+    for (int i = threadIdx.x; i < ROWS * C; i += kThreads) {
+        const int r = i / C, c = i % C, row = p.tile * ROWS + r;
         float x[4] = {0.f, 0.f, 0.f, 0.f};
         if (row < a.rows && c * 4 < a.hd) {
             const int m = row / a.group, g = row - m * a.group;
@@ -610,7 +618,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
         for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
     }
     const float cs = a.scale * kLog2e;
-    const int rows_left = a.rows - p.tile * kRowsF - 4 * warp;   // real rows of this warp
+    const int rows_left = a.rows - p.tile * ROWS - r0;           // real rows of this warp
     const int drafts = p.tail ? (a.M + kTokF - 1) / kTokF : 0;
     for (int t = 0; t < tiles + drafts; ++t) {
         const bool draft = t >= tiles;
@@ -644,26 +652,28 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
         }
         const int left = (int)min((int64_t)kTokF, draft ? (int64_t)(a.M - d0) : p.to - p.from - (int64_t)t * kTokF);
         if (rows_left > 0) {
-            // scores: a lane per token, four rows
+            // scores: TW lanes per token, four rows
             float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-            for (int c = 0; c < C; ++c) {
-                const float4 x = *reinterpret_cast<const float4*>(tile + place(lane, c));
+            for (int c = part; c < C; c += TW) {
+                const float4 x = *reinterpret_cast<const float4*>(tile + place(tok, c));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float4 y = *reinterpret_cast<const float4*>(&sq[4 * warp + r][4 * c]);
+                    const float4 y = *reinterpret_cast<const float4*>(&sq[r0 + r][4 * c]);
                     s[r] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[r]))));
                 }
             }
             uint32_t see[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = min(p.tile * kRowsF + 4 * warp + r, a.rows - 1);
-                const bool mine = lane < left && (!draft || (seen[row / a.group] >> (d0 + lane) & 1));
+#pragma unroll
+                for (int x = NT; x < 32; x <<= 1) s[r] += __shfl_xor_sync(0xFFFFFFFFu, s[r], x);
+                const int row = min(p.tile * ROWS + r0 + r, a.rows - 1);
+                const bool mine = tok < left && (!draft || (seen[row / a.group] >> (d0 + tok) & 1));
                 see[r] = __ballot_sync(0xFFFFFFFFu, mine);
                 float top = mine ? s[r] * cs : -INFINITY;
 #pragma unroll
-                for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+                for (int x = NT / 2; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
                 const float now = fmaxf(mx[r], top), use = now == -INFINITY ? 0.f : now;
                 const float corr = exp2f(mx[r] - use);
                 mx[r] = now;
@@ -673,20 +683,28 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
                 for (int e = 0; e < E; ++e) acc[r][e] *= corr;
             }
             // values: a lane per E channels; a masked token's value is not touched
-            for (int n = 0; n < left; ++n) {
-                float x[E];
-                const int c = lane * E;
-                const float* row = reinterpret_cast<const float*>(tile + kHalf + place(n, c / 4)) + c % 4;
+            if (part == 0) sp[warp][lane % NT] = make_float4(s[0], s[1], s[2], s[3]);
+            __syncwarp();
+            const int count = min(NT, left - tw * NT), ch = lane * E;
+            auto values = [&](auto with_mask) {
+#pragma unroll 8
+                for (int n = 0; n < count; ++n) {
+                    const float* row = reinterpret_cast<const float*>(tile + kHalf + place(tw * NT + n, ch / 4)) + ch % 4;
+                    const float4 w4 = sp[warp][n];
+                    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+                    float x[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = row[e];
+                    for (int e = 0; e < E; ++e) x[e] = row[e];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float w = __shfl_sync(0xFFFFFFFFu, s[r], n);
-                    if (see[r] >> n & 1)
+                    for (int r = 0; r < 4; ++r)
+                        if (!decltype(with_mask)::value || (see[r] >> n & 1))
 #pragma unroll
-                        for (int e = 0; e < E; ++e) acc[r][e] = fmaf(w, x[e], acc[r][e]);
+                            for (int e = 0; e < E; ++e) acc[r][e] = fmaf(w[r], x[e], acc[r][e]);
                 }
-            }
+            };
+            if (draft) values(std::true_type{});
+            else values(std::false_type{});
+            __syncwarp();                                        // the probabilities are read
         }
         __syncthreads();
     }
@@ -696,23 +714,23 @@ __global__ void __launch_bounds__(kThreads) attn_decode_f32_kernel(const float* 
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
 #pragma unroll
-        for (int x = 16; x; x >>= 1) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], x);
+        for (int x = NT / 2; x; x >>= 1) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], x);
         if (lane == 0) {
-            smax[4 * warp + r] = mx[r];
-            ssum[4 * warp + r] = sum[r];
+            smax[tw * ROWS + r0 + r] = mx[r];
+            ssum[tw * ROWS + r0 + r] = sum[r];
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) so[(4 * warp + r) * HD + lane * E + e] = acc[r][e];
+        for (int e = 0; e < E; ++e) so[(tw * ROWS + r0 + r) * HD + lane * E + e] = acc[r][e];
     }
     __syncthreads();
-    finish<float, HD, kRowsF, 1>(a, p, so, smax, ssum, so + kRowsF * HD, o);
+    finish<float, HD, ROWS, TW>(a, p, so, smax, ssum, so + TW * ROWS * HD, o);
 }
 
 // Rows a block takes: 8, 16 or 32 where they are all there are (its warps then share out the tokens), else the 128 of
-// the tcgen05 kernel.
+// the tcgen05 kernel; fp32: 8 or 16.
 int tile_rows(const DecodeProb& p) {
-    if (p.dtype == 0) return kRowsF;
     const int64_t rows = (int64_t)p.M * p.group;
+    if (p.dtype == 0) return rows <= 8 ? 8 : 16;
     return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : kTcTile;
 }
 
@@ -726,11 +744,18 @@ cudaError_t launch(std::atomic<uint64_t>& limit, F* f, size_t smem, unsigned gri
                                                                static_cast<T*>(vc), static_cast<T*>(o), a));
     return cudaGetLastError();
 }
+template <int HD, int TW>
+cudaError_t launch_tw(unsigned grid, const void* q, const void* k, const void* v, void* kc, void* vc, void* o,
+                       const DecArgs& a, cudaStream_t st) {
+    static std::atomic<uint64_t> limit{0};
+    return launch<float>(limit, attn_decode_f32_kernel<HD, TW>, kStages * 2 * kTokF * HD * 4, grid, q, k, v, kc, vc, o, a, st);
+}
 template <int HD>
 cudaError_t launch_f32(unsigned grid, const void* q, const void* k, const void* v, void* kc, void* vc, void* o,
                        const DecArgs& a, cudaStream_t st) {
-    static std::atomic<uint64_t> limit{0};
-    return launch<float>(limit, attn_decode_f32_kernel<HD>, kStages * 2 * kTokF * HD * 4, grid, q, k, v, kc, vc, o, a, st);
+    return a.rows <= 4   ? launch_tw<HD, 4>(grid, q, k, v, kc, vc, o, a, st)
+           : a.rows <= 8 ? launch_tw<HD, 2>(grid, q, k, v, kc, vc, o, a, st)
+                         : launch_tw<HD, 1>(grid, q, k, v, kc, vc, o, a, st);
 }
 template <int HD>
 cudaError_t launch_8(const DecodeProb& p, unsigned grid, const void* q, const void* k, const void* v, void* kc, void* vc,
