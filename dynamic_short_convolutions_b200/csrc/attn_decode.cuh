@@ -174,6 +174,11 @@ __device__ __forceinline__ Place place_of(const DecArgs& a, int tokens_per_tile)
     p.tail = p.split == a.n_split - 1;
     return p;
 }
+// A row of the last run that sees nothing at all takes a weight of 1 on a value of zero (its o is zero); a sum of
+// zero is then that of a row without a finite score, which has no softmax (0 / 0).
+__device__ __forceinline__ bool sees_nothing(const DecArgs& a, const Place& p, const uint64_t* seen, int row) {
+    return p.tail && p.len == 0 && row < a.rows && seen[row / a.group] == 0;
+}
 // What each drafted token sees and the table row of its position; false where a position is outside the table.
 __device__ __forceinline__ bool look_up(const DecArgs& a, const Place& p, uint64_t* seen, const float** turn) {
     bool ok = true;
@@ -230,7 +235,7 @@ __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const f
             l += w * ssum[n * ROWS + r];
         }
         if (a.n_split == 1) {
-            if (c < a.hd) put(r, c, s, l > 0.f ? 1.f / l : l);
+            if (c < a.hd) put(r, c, s, 1.f / l);
         } else {
             *reinterpret_cast<float4*>(parts + ((int64_t)p.split * ROWS + r) * HD + c) = s;
             if (c == 0) *reinterpret_cast<float2*>(stats + (p.split * ROWS + r) * 2) = make_float2(mx, l);
@@ -265,7 +270,7 @@ __device__ __forceinline__ void finish(const DecArgs& a, const Place& p, const f
             w[n] = exp2f(w[n] - use);
             sum += w[n] * l[n];
         }
-        inverse[threadIdx.x] = sum > 0.f ? 1.f / sum : sum;
+        inverse[threadIdx.x] = 1.f / sum;
     }
     __syncthreads();
     float4 s[kItems];

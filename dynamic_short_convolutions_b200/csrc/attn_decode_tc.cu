@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(kBlock, 1) attn_decode_tc_kernel(const __grid_
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<float4*>(so + r * S::ld + 32 * b + e) = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
             }
+            if (l0 + l1 == 0.f && sees_nothing(a, p, seen, row)) m = 0.f, l0 = 1.f;
             smax[r] = m;
             ssum[r] = l0 + l1;
         }
@@ -412,8 +413,8 @@ __global__ void __launch_bounds__(kBlock, 1) attn_decode_tc_kernel(const __grid_
             s.x += w * x.x; s.y += w * x.y; s.z += w * x.z; s.w += w * x.w;
             l += w * cluster.map_shared_rank(ssum, n)[t];
         }
-        const float inv = l > 0.f ? 1.f / l : l;
         const int at = p.tile * kRows + t, m = at / a.group, g = at - m * a.group;
+        const float inv = 1.f / l;
         *reinterpret_cast<uint2*>(o + (p.b * a.M + m) * a.os + ((int64_t)p.kv * a.group + g) * a.hd + c) =
             make_uint2(pack_bf16(s.x * inv, s.y * inv), pack_bf16(s.z * inv, s.w * inv));
     }

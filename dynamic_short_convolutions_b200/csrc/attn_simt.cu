@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const T* __rest
             }
             const int32_t n = row0 + r;
             if (n >= a.N) continue;
-            if (c < a.hd) o[(int64_t)n * a.os + c] = from_f32<T>(x * (sum > 0.f ? 1.f / sum : sum));
+            if (c < a.hd) o[(int64_t)n * a.os + c] = from_f32<T>(x * (1.f / sum));
             if (lse != nullptr && c == 0) lse[(int64_t)head * a.N + n] = (mx + log2f(sum)) * kLn2;
         }
         cluster.sync();                    // no block leaves while its part is read
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(const T* __rest
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         l[i] = row_sum(l[i]);
-        inv[i] = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+        inv[i] = 1.f / l[i];               // every row sees its own key; no finite score: 0 / 0
         const int32_t n = row0 + 4 * ty + i;
         if (lse != nullptr && tx == 0 && n < a.N) lse[(int64_t)head * a.N + n] = (m[i] + log2f(l[i])) * kLn2;
     }

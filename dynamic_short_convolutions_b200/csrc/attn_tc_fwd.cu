@@ -76,7 +76,7 @@ __device__ __noinline__ void fwd_rows_again(const AttnTcArgs& a, int head, int32
             l = l * c + p;
             m = mx;
         }
-        const float inv = l > 0.f ? 1.f / l : l;
+        const float inv = 1.f / l;
         put4(a.o + (int64_t)n * a.os + (int64_t)head * a.hd, lane, a.hd,
              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
         if (a.lse != nullptr && lane == 0) a.lse[(int64_t)head * a.N + n] = (m + log2f(l)) * kLn2;
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2) attn_fwd_kernel(const __grid_c
         ok = ok && wait(&pv_done, (items - 1) & 1);
         ok = !named_bar_any<1, 128>(!ok);                    // every warp has looked; all go on, or none
         const float l = l0 + l1;
-        const float inv = l > 0.f ? 1.f / l : l;
+        const float inv = 1.f / l;                           // every row sees its own key; no finite score: 0 / 0
         if (ok && !again) {
             // O through Q's tile and TMA: rows from N on and channels from hd on are not written
 #pragma unroll

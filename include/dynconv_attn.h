@@ -89,7 +89,7 @@ DYNCONV_API dynconv_status dynconv_attn_query_family(const dynconv_attn_desc *de
  * with s(n) the first token of n's sequence (dense batch, cu_seqlens NULL) or document
  * (cu_seqlens: DEVICE int32 [n_docs + 1], batch 1; 0 ... N, non-decreasing; documents of no
  * tokens are allowed).  A token outside that range has no influence on o[n], whatever it holds
- * (infinities and NaN among it).
+ * (infinities and NaN among it).  A row without a finite score has no softmax: its o is NaN.
  *   q [N, heads * head_dim], k and v [N, kv_heads * head_dim], o [N, heads * head_dim]
  *   lse  nullable fp32 [heads, N]: log of the sum of exp(scale q.k), for the backward
  * Errors: DYNCONV_ERR_INVALID, _UNSUPPORTED (head_dim above 128, N * heads beyond the grid),
