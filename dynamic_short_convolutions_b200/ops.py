@@ -435,7 +435,8 @@ class QKVAttention(torch.autograd.Function):
         # columns that start off a 16-byte boundary (heads of odd widths) are copied out, and their gradients in
         apart = any(n * qkv.element_size() % 16 for n in (wq, wk))
         if apart:
-            q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+            # (not contiguous(), which gives back the slices of a single row as they are)
+            q, k, v = (t.clone(memory_format=torch.contiguous_format) for t in (q, k, v))
         strides = (0,) * 6 if apart else (qk_row, qk_row, row, C, C, C)
         plan = AttnPlan(qkv.dtype, batch, N // batch, heads, kv_heads, head_dim, scale, *strides, algo=algo,
                         device=qkv.device)
