@@ -112,6 +112,12 @@ def _on(device: torch.device, call, *args) -> None:
             call(*args)
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy where its rows are not dense or do not start on a 16-byte boundary (rows or columns out of the
+    middle of a larger buffer, as autograd hands them back through cat or split)."""
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
 def _like(t: torch.Tensor, rows: int, width: int) -> torch.Tensor:
     """An uninitialised [rows, width] tensor of t's type, on its device."""
     return torch.empty_like(t) if t.shape == (rows, width) and t.is_contiguous() else t.new_empty((rows, width))
@@ -423,8 +429,8 @@ class QKVAttention(torch.autograd.Function):
             raise ValueError(f"qkv must be [N, (heads + 2 kv_heads) * head_dim] = [N, {wq + 2 * wk}], got {list(qkv.shape)}")
         if batch < 1 or N % batch:
             raise ValueError(f"{N} tokens are not {batch} sequences of one length")
-        if qkv.stride(1) != 1 or (N > 1 and qkv.stride(0) < C):
-            qkv = qkv.contiguous()
+        if qkv.stride(1) != 1 or (N > 1 and qkv.stride(0) < C) or qkv.data_ptr() % 16:
+            qkv = qkv.clone(memory_format=torch.contiguous_format)
         row = qkv.stride(0) if N > 1 else C
         qk, rope, qk_row = qkv[:, :wq + wk], None, row
         if table is not None:
@@ -454,7 +460,7 @@ class QKVAttention(torch.autograd.Function):
         N, C, wq, wk = ctx.width
         d = torch.empty((N, C), dtype=q.dtype, device=q.device)
         out = {"dq": d[:, :wq], "dk": d[:, wq:wq + wk], "dv": d[:, wq + wk:]}
-        grads = ctx.plan.backward(go.contiguous(), q, k, v, o, lse, cu_seqlens, None if ctx.apart else out)
+        grads = ctx.plan.backward(_dense(go), q, k, v, o, lse, cu_seqlens, None if ctx.apart else out)
         if ctx.apart:
             for name, part in out.items():
                 part.copy_(grads[name])

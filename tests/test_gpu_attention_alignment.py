@@ -1,5 +1,5 @@
 """qkv_attention where columns, rows or gradients start off a 16-byte boundary: one token with heads of odd widths, whose
-column slices torch calls contiguous."""
+column slices torch calls contiguous; rows out of the middle of a larger buffer; gradients that arrive as views of one."""
 import pytest
 
 from attn_reference import attention, check
@@ -44,3 +44,44 @@ def test_one_token_of_odd_heads(dtype, heads, kv, hd, rot, packed):
         d = got[1]
         for name, t in (("o", got[0]), ("dq", d[:, :wq]), ("dk", d[:, wq:wq + wk]), ("dv", d[:, wq + wk:])):
             check(name, t, ref[name])
+
+
+@pytest.mark.parametrize("heads,kv,hd,rot", [(1, 1, 37, 0), (1, 1, 37, 4), (3, 1, 5, 2), (2, 1, 64, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_that_are_views(dtype, heads, kv, hd, rot):
+    """Outputs joined by cat along the tokens and along the channels: autograd hands back views of the joined gradient."""
+    from dynamic_short_convolutions_b200 import ops
+
+    table = ops.rope_table(3, rot) if rot else None
+    a, ga = _rows(3, heads, kv, hd, dtype, 3)
+    b, gb = _rows(3, heads, kv, hd, dtype, 4)
+    want = [_layer(x, g, heads, kv, hd, table)[1] for x, g in ((a, ga), (b, gb))]
+    a.requires_grad_()
+    b.requires_grad_()
+    outs = [ops.qkv_attention(x, heads, kv, hd, table) for x in (a, b)]
+    got = torch.autograd.grad(torch.cat(outs), (a, b), torch.cat((ga, gb)))
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    outs = [ops.qkv_attention(x[:1], heads, kv, hd, table) for x in (a, b)]
+    odd = ga.new_ones((1, 1))
+    got = torch.autograd.grad(torch.cat((odd, *outs), 1), (a, b), torch.cat((odd, ga[:1], gb[:1]), 1))
+    for x, g, d in ((a, ga, got[0]), (b, gb, got[1])):
+        assert torch.equal(d[:1], _layer(x[:1], g[:1], heads, kv, hd, table)[1]) and not d[1:].any()
+
+
+@pytest.mark.parametrize("heads,kv,hd,rot", [(1, 1, 37, 0), (3, 1, 5, 2), (2, 1, 64, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_of_a_larger_buffer(dtype, heads, kv, hd, rot):
+    """qkv that starts at an odd row, or at an odd column, of a buffer."""
+    from dynamic_short_convolutions_b200 import ops
+
+    table = ops.rope_table(4, rot) if rot else None
+    rows, go = _rows(4, heads, kv, hd, dtype, 5)
+    want = _layer(rows, go, heads, kv, hd, table)
+    flat = torch.empty(rows.numel() + 1, dtype=rows.dtype, device="cuda")
+    wide = torch.empty((4, rows.shape[1] + 3), dtype=rows.dtype, device="cuda")
+    for view in (flat[1:].view(rows.shape), wide[:, 3:]):
+        view.copy_(rows)
+        assert view.data_ptr() % 16
+        got = _layer(view, go, heads, kv, hd, table)
+        # 64 channels: strided rows run on other kernels than dense ones, and the copy on those of dense ones
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
