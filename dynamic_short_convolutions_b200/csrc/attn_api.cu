@@ -63,6 +63,16 @@ dynconv_status check_cu(const int32_t* cu, int64_t n_docs, int64_t batch) {
     return validate_ptr(cu, "cu_seqlens", true);
 }
 
+// Attention searches cu_seqlens with 32-bit sums of two indices (the rotation with 64-bit ones).
+constexpr int64_t kMaxDocs = int64_t(1) << 30;
+dynconv_status check_docs(const int32_t* cu, int64_t n_docs, int64_t batch) {
+    if (n_docs > kMaxDocs) {
+        set_error("at most 2^30 documents are supported");
+        return DYNCONV_ERR_UNSUPPORTED;
+    }
+    return check_cu(cu, n_docs, batch);
+}
+
 dynconv_status make_attn(const dynconv_attn_desc* d, AttnProb* p) {
     *p = AttnProb{};
     if (!d) return invalid("desc is NULL");
@@ -277,7 +287,7 @@ dynconv_status dynconv_attn_fwd(const dynconv_attn_desc* desc, const int32_t* cu
     AttnProb p;
     dynconv_status s = make_attn(desc, &p);
     if (s != DYNCONV_OK) return s;
-    if (cu_seqlens && (s = check_cu(cu_seqlens, n_docs, desc->batch)) != DYNCONV_OK) return s;
+    if (cu_seqlens && (s = check_docs(cu_seqlens, n_docs, desc->batch)) != DYNCONV_OK) return s;
     p.cu = cu_seqlens;
     p.n_docs = n_docs;
     if (p.N == 0) return DYNCONV_OK;
@@ -300,7 +310,7 @@ dynconv_status dynconv_attn_bwd(const dynconv_attn_desc* desc, const int32_t* cu
     AttnProb p;
     dynconv_status s = make_attn(desc, &p);
     if (s != DYNCONV_OK) return s;
-    if (cu_seqlens && (s = check_cu(cu_seqlens, n_docs, desc->batch)) != DYNCONV_OK) return s;
+    if (cu_seqlens && (s = check_docs(cu_seqlens, n_docs, desc->batch)) != DYNCONV_OK) return s;
     p.cu = cu_seqlens;
     p.n_docs = n_docs;
     if (p.N == 0) return DYNCONV_OK;

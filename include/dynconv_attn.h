@@ -92,9 +92,9 @@ DYNCONV_API dynconv_status dynconv_attn_query_family(const dynconv_attn_desc *de
  * (infinities and NaN among it).  A row without a finite score has no softmax: its o is NaN.
  *   q [N, heads * head_dim], k and v [N, kv_heads * head_dim], o [N, heads * head_dim]
  *   lse  nullable fp32 [heads, N]: log of the sum of exp(scale q.k), for the backward
- * Errors: DYNCONV_ERR_INVALID, _UNSUPPORTED (head_dim above 128, N * heads beyond the grid),
- * _WORKSPACE, _CUDA; a malformed cu_seqlens raises the device check (the call's results are
- * then undefined, every access stays inside the tensors). */
+ * Errors: DYNCONV_ERR_INVALID, _UNSUPPORTED (head_dim above 128, N * heads beyond the grid, more than
+ * 2^30 documents), _WORKSPACE, _CUDA; a malformed cu_seqlens raises the device check (the call's
+ * results are then undefined, every access stays inside the tensors). */
 DYNCONV_API dynconv_status dynconv_attn_fwd(const dynconv_attn_desc *desc, const int32_t *cu_seqlens, int64_t n_docs,
                                             const void *q, const void *k, const void *v, void *o, float *lse,
                                             void *ws, size_t ws_bytes, void *stream);
