@@ -103,13 +103,8 @@ def _device(device) -> torch.device:
     return torch.device(d.type, torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
 
 
-def _on(device: torch.device, call, *args) -> None:
-    """call(*args) with `device` current (kernels launch on the current device)."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        call(*args)
-    else:
-        with torch.cuda.device(device):
-            call(*args)
+# The handle of a device's current stream.
+_current = L._raw_stream or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _dense(t: torch.Tensor) -> torch.Tensor:
@@ -246,7 +241,61 @@ def dynamic_short_conv(u: torch.Tensor, h: torch.Tensor, A: Optional[torch.Tenso
     return DynamicShortConv.apply(u, h, A, B_or_W, ksize, head_dim, batch, cu_seqlens, algo)
 
 
-class RopePlan:
+class _Plan:
+    """What the plans of rotary positions and attention share: the zeroed workspace on ``device``, and the order of the
+    streams they are made, called and given their tensors on.
+
+    A call runs on the current stream, or on ``stream``: there it comes behind what the current stream holds by
+    then, its outputs belong to that stream, and its inputs and the plan may be dropped at once.  A call on another
+    stream than the one the plan was made on waits for that one; not so inside a capture, which cannot wait for
+    anything outside it: synchronise before."""
+
+    def _workspace(self, nbytes: int, one_stream: bool) -> None:
+        """Last in the making of a plan; one_stream: never called on another stream than this one."""
+        self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self._made, self._index = None, self.device.index
+        if self.device.type == "cuda" and not one_stream and not torch.cuda.is_current_stream_capturing():
+            here = torch.cuda.current_stream(self.device)
+            self._made, self._behind = here.record_event(), {here.cuda_stream}
+
+    def _run(self, call, *args) -> None:
+        here = None if self._index is None else _current(self._index)
+        if self._made is not None and here not in self._behind and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).wait_event(self._made)
+            self._behind.add(here)
+        if self._index is None or self._index == torch.cuda.current_device():
+            call(*args, here)
+        else:                                   # kernels launch on the current device
+            with torch.cuda.device(self._index):
+                call(*args, here)
+
+    def _other(self, stream) -> Optional[torch.cuda.Stream]:
+        """`stream` (a stream, or a handle) where it is another than the current one."""
+        if self._index is None:
+            return None
+        at = L._stream(stream, None)
+        if at == _current(self._index):
+            return None
+        return torch.cuda.ExternalStream(at, device=self.device) if at else torch.cuda.default_stream(self.device)
+
+    def _call_on(self, stream: torch.cuda.Stream, call, *args):
+        """call(*args) with `stream` current, behind what the stream that is current now holds."""
+        here = torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(here):
+            captured = torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(stream):
+            if captured or not torch.cuda.is_current_stream_capturing():
+                stream.wait_stream(here)
+            result = call(*args)
+            if not torch.cuda.is_current_stream_capturing():
+                for t in (*args, *vars(self).values()):
+                    for x in t.values() if isinstance(t, dict) else (t,):
+                        if isinstance(x, torch.Tensor):
+                            x.record_stream(stream)
+        return result
+
+
+class RopePlan(_Plan):
     """Rotary positions for rows of ``heads`` heads of ``head_dim`` channels, the first
     ``table.shape[1]`` channels of each head rotated.
 
@@ -256,7 +305,8 @@ class RopePlan:
     [max_pos, rotated channels], see :func:`rope_table`."""
 
     def __init__(self, dtype: torch.dtype, batch: int, seqlen: int, heads: int, head_dim: int, table: torch.Tensor,
-                 layout: int = L.ROPE_INTERLEAVED, x_row_stride: int = 0, y_row_stride: int = 0, device=None):
+                 layout: int = L.ROPE_INTERLEAVED, x_row_stride: int = 0, y_row_stride: int = 0, device=None,
+                 _one_stream: bool = False):
         if dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"storage dtype must be bf16 or fp32, got {dtype}")
         _table(table, "table")
@@ -266,12 +316,14 @@ class RopePlan:
         code = L.BF16 if dtype == torch.bfloat16 else L.F32
         self.desc = [L.make_rope_desc(code, layout, batch, seqlen, heads, head_dim, table, inv, x_row_stride,
                                       y_row_stride) for inv in (0, 1)]
-        self.ws = torch.zeros(256, dtype=torch.uint8, device=self.device)
         self.dtype, self.N, self.width = dtype, batch * seqlen, heads * head_dim
         self.strides = (x_row_stride, y_row_stride)
+        self._workspace(256, _one_stream)
 
     def apply(self, x, y=None, positions=None, cu_seqlens=None, inverse: bool = False, stream=None):
         """y = R(p) x, or the transposed rotation (the backward).  ``y=x`` rotates in place."""
+        if stream is not None and (other := self._other(stream)) is not None:
+            return self._call_on(other, self.apply, x, y, positions, cu_seqlens, inverse)
         _rows(x, "x", self.N, self.width, self.dtype, self.strides[0], self.device)
         if y is None:
             if self.strides[1] not in (0, self.width):
@@ -281,11 +333,11 @@ class RopePlan:
             _rows(y, "y", self.N, self.width, self.dtype, self.strides[1], self.device)
         _flat(positions, "positions", torch.int32, self.device, (self.N,))
         _cu(cu_seqlens, self.device)
-        _on(self.device, L.dynconv_rope, self.desc[int(inverse)], cu_seqlens, positions, x, y, self.ws, stream)
+        self._run(L.dynconv_rope, self.desc[int(inverse)], cu_seqlens, positions, x, y, self.ws)
         return y
 
 
-class AttnPlan:
+class AttnPlan(_Plan):
     """Causal attention for one problem shape: q [N, heads * head_dim], k and v
     [N, kv_heads * head_dim], N = batch * seqlen, rows optionally strided (column slices of a fused
     QKV buffer).  For packed documents pass ``cu_seqlens`` (int32 device tensor [docs + 1]) and
@@ -294,7 +346,7 @@ class AttnPlan:
     def __init__(self, dtype: torch.dtype, batch: int, seqlen: int, heads: int, kv_heads: int, head_dim: int,
                  scale: float = 0.0, q_row_stride: int = 0, k_row_stride: int = 0, v_row_stride: int = 0,
                  dq_row_stride: int = 0, dk_row_stride: int = 0, dv_row_stride: int = 0, algo: int = L.ALGO_AUTO,
-                 device=None):
+                 device=None, _one_stream: bool = False):
         if dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"storage dtype must be bf16 or fp32, got {dtype}")
         self.desc = L.make_attn_desc(L.BF16 if dtype == torch.bfloat16 else L.F32, batch, seqlen, heads, kv_heads,
@@ -304,11 +356,11 @@ class AttnPlan:
         if nbytes == 0:
             raise L.DynConvError(1, L.dynconv_last_error() or "invalid descriptor")
         self.device = _device(device)
-        self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.dtype, self.N, self.heads = dtype, batch * seqlen, heads
         self.wq, self.wk = heads * head_dim, kv_heads * head_dim
         self.strides = (q_row_stride, k_row_stride, v_row_stride)
         self.grad_strides = (dq_row_stride, dk_row_stride, dv_row_stride)
+        self._workspace(nbytes, _one_stream)
 
     def _inputs(self, q, k, v, cu_seqlens):
         _rows(q, "q", self.N, self.wq, self.dtype, self.strides[0], self.device)
@@ -318,18 +370,22 @@ class AttnPlan:
 
     def forward(self, q, k, v, cu_seqlens=None, o=None, want_lse: bool = False, stream=None):
         """o [N, heads * head_dim]; with ``want_lse`` (o, lse), lse fp32 [heads, N] for :meth:`backward`."""
+        if stream is not None and (other := self._other(stream)) is not None:
+            return self._call_on(other, self.forward, q, k, v, cu_seqlens, o, want_lse)
         self._inputs(q, k, v, cu_seqlens)
         if o is None:
             o = _like(q, self.N, self.wq)
         else:
             _rows(o, "o", self.N, self.wq, self.dtype, 0, self.device)
         lse = torch.empty((self.heads, self.N), dtype=torch.float32, device=self.device) if want_lse else None
-        _on(self.device, L.dynconv_attn_fwd, self.desc, cu_seqlens, q, k, v, o, lse, self.ws, stream)
+        self._run(L.dynconv_attn_fwd, self.desc, cu_seqlens, q, k, v, o, lse, self.ws)
         return (o, lse) if want_lse else o
 
     def backward(self, d_o, q, k, v, o, lse, cu_seqlens=None, out=None, stream=None):
         """{"dq", "dk", "dv"} from the forward's o and lse; ``out`` gives tensors to write (dq_row_stride and
         so on apart), for instance column slices of one gradient buffer."""
+        if stream is not None and (other := self._other(stream)) is not None:
+            return self._call_on(other, self.backward, d_o, q, k, v, o, lse, cu_seqlens, out)
         self._inputs(q, k, v, cu_seqlens)
         if out is None:
             if any(self.grad_strides):
@@ -343,12 +399,12 @@ class AttnPlan:
         if lse is None:
             raise ValueError("the backward needs the forward's lse (want_lse=True)")
         _flat(lse, "lse", torch.float32, self.device, (self.heads, self.N))
-        _on(self.device, L.dynconv_attn_bwd, self.desc, cu_seqlens, d_o, q, k, v, o, lse, out["dq"], out["dk"], out["dv"],
-            self.ws, stream)
+        self._run(L.dynconv_attn_bwd, self.desc, cu_seqlens, d_o, q, k, v, o, lse, out["dq"], out["dk"], out["dv"],
+                  self.ws)
         return out
 
 
-class AttnDecoder:
+class AttnDecoder(_Plan):
     """Serving steps of ``batch`` sequences over a key/value cache: each step takes ``tokens`` new or drafted
     tokens per sequence, rotates their q and k (``rope_table``, see :func:`rope_table`), appends k and v to the
     caches and returns their attention.
@@ -381,16 +437,21 @@ class AttnDecoder:
         _flat(self.v_cache, "v_cache", dtype, self.device, shape)
         _flat(self.lens, "lens", torch.int32, self.device, (batch,))
         _flat(rope_table, "rope_table", torch.float32, self.device)
-        self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self.dtype, self.batch, self.tokens = dtype, batch, tokens
         self.wq, self.wk = heads * head_dim, kv_heads * head_dim
         self.strides = (q_row_stride, k_row_stride, v_row_stride)
+        self._stepped = None                    # the last step, where it ran on a stream of its own
+        self._workspace(nbytes, False)
 
     def step(self, q, k, v, ancestors=None, o=None, stream=None):
         """o [batch * tokens, heads * head_dim] of q [batch * tokens, heads * head_dim], k and v
         [batch * tokens, kv_heads * head_dim] (rows by sequence, then token).  ``ancestors`` (int64
         [batch, tokens]): bit j of an entry set where that token sees drafted token j, its own bit included;
         None: a chain."""
+        if stream is not None and (other := self._other(stream)) is not None:
+            o = self._call_on(other, self.step, q, k, v, ancestors, o)
+            self._stepped = other.record_event()
+            return o
         rows = self.batch * self.tokens
         _rows(q, "q", rows, self.wq, self.dtype, self.strides[0], self.device)
         if o is None:
@@ -400,18 +461,26 @@ class AttnDecoder:
         _rows(k, "k", rows, self.wk, self.dtype, self.strides[1], self.device)
         _rows(v, "v", rows, self.wk, self.dtype, self.strides[2], self.device)
         _flat(ancestors, "ancestors", torch.int64, self.device, (self.batch, self.tokens))
-        _on(self.device, L.dynconv_attn_decode, self.desc, q, k, v, self.k_cache, self.v_cache, self.lens, ancestors, o,
-            self.ws, stream)
+        self._run(L.dynconv_attn_decode, self.desc, q, k, v, self.k_cache, self.v_cache, self.lens, ancestors, o,
+                  self.ws)
         return o
 
     def advance(self, kept=None):
         """Adds the tokens kept of the last step to ``lens``: all of them, or ``kept`` (int32 [batch]).  Idle
         slots stay idle.  Kept tokens of a tree have to lie in the cache in order (tokens 0 .. kept - 1)."""
         _flat(kept, "kept", torch.int32, self.device, (self.batch,))
+        self._settle()
         self.lens.add_(torch.where(self.lens < 0, 0, self.tokens if kept is None else kept).to(torch.int32))
 
     def reset(self):
+        self._settle()
         self.lens.zero_()
+
+    def _settle(self):
+        """The current stream behind a step that ran on a stream of its own and may still read lens."""
+        if self._stepped is not None:
+            torch.cuda.current_stream(self.device).wait_event(self._stepped)
+            self._stepped = None
 
 
 class QKVAttention(torch.autograd.Function):
@@ -435,7 +504,8 @@ class QKVAttention(torch.autograd.Function):
         qk, rope, qk_row = qkv[:, :wq + wk], None, row
         if table is not None:
             rope = (batch, N // batch, heads + kv_heads, head_dim, table, layout)
-            qk = RopePlan(qkv.dtype, *rope, x_row_stride=row, device=qkv.device).apply(qk, cu_seqlens=cu_seqlens)
+            qk = RopePlan(qkv.dtype, *rope, x_row_stride=row, device=qkv.device, _one_stream=True).apply(
+                qk, cu_seqlens=cu_seqlens)
             qk_row = wq + wk
         q, k, v = qk[:, :wq], qk[:, wq:], qkv[:, wq + wk:]
         # columns that start off a 16-byte boundary (heads of odd widths) are copied out, and their gradients in
@@ -445,7 +515,7 @@ class QKVAttention(torch.autograd.Function):
             q, k, v = (t.clone(memory_format=torch.contiguous_format) for t in (q, k, v))
         strides = (0,) * 6 if apart else (qk_row, qk_row, row, C, C, C)
         plan = AttnPlan(qkv.dtype, batch, N // batch, heads, kv_heads, head_dim, scale, *strides, algo=algo,
-                        device=qkv.device)
+                        device=qkv.device, _one_stream=True)
         train = ctx.needs_input_grad[0]
         o, lse = plan.forward(q, k, v, cu_seqlens, want_lse=True) if train else (plan.forward(q, k, v, cu_seqlens), None)
         ctx.plan, ctx.rope, ctx.apart, ctx.width = plan, rope, apart, (N, C, wq, wk)
@@ -465,7 +535,7 @@ class QKVAttention(torch.autograd.Function):
             for name, part in out.items():
                 part.copy_(grads[name])
         if ctx.rope is not None:
-            RopePlan(q.dtype, *ctx.rope, x_row_stride=C, y_row_stride=C, device=q.device).apply(
+            RopePlan(q.dtype, *ctx.rope, x_row_stride=C, y_row_stride=C, device=q.device, _one_stream=True).apply(
                 d[:, :wq + wk], y=d[:, :wq + wk], cu_seqlens=cu_seqlens, inverse=True)
         return d, None, None, None, None, None, None, None, None, None
 
