@@ -152,6 +152,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, ref: torch.Tensor):
+    if type(stream) is int:
+        return stream
     if stream is not None:
         return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     dev = ref.device if ref is not None and ref.is_cuda else None

@@ -107,6 +107,18 @@ def _device(device) -> torch.device:
 _current = L._raw_stream or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _check_errors(t: torch.Tensor, device: torch.device) -> None:
+    """What a caller gives for the device errors of an autograd call."""
+    _flat(t, "errors", torch.uint8, device)
+    if t.numel() < 256 or t.data_ptr() % 16:
+        raise ValueError("errors must hold 256 bytes or more, on a 16-byte boundary")
+
+
+def _report(errors: torch.Tensor, ws: torch.Tensor) -> None:
+    """The error bits of a plan's workspace into the caller's `errors`."""
+    errors[:4].view(torch.int32).bitwise_or_(ws[:4].view(torch.int32))
+
+
 def _dense(t: torch.Tensor) -> torch.Tensor:
     """t, or a copy where its rows are not dense or do not start on a 16-byte boundary (rows or columns out of the
     middle of a larger buffer, as autograd hands them back through cat or split)."""
@@ -204,7 +216,9 @@ class DynamicShortConv(torch.autograd.Function):
     dtype (accumulated in fp32 by the kernels)."""
 
     @staticmethod
-    def forward(ctx, u, h, A, B_or_W, ksize: int, head_dim: int, batch: int, cu_seqlens, algo: int):
+    def forward(ctx, u, h, A, B_or_W, ksize: int, head_dim: int, batch: int, cu_seqlens, algo: int, errors=None):
+        if errors is not None:
+            _check_errors(errors, u.device)
         d = h.shape[1]
         kind = L.LOWRANK if A is not None else L.HEADWISE
         rank = A.shape[1] if A is not None else 0
@@ -221,7 +235,9 @@ class DynamicShortConv(torch.autograd.Function):
         R = rank if A is not None else (C // head_dim) * ksize
         z = torch.empty((N, R), dtype=u.dtype, device=u.device)    # generator output, reused by backward
         y = plan.forward(u, h, A, B_or_W, cu_seqlens, z_save=z)
-        ctx.plan = plan
+        if errors is not None:
+            _report(errors, plan.ws)
+        ctx.plan, ctx.errors = plan, errors
         ctx.save_for_backward(u, h, A, B_or_W, cu_seqlens, z)
         return y
 
@@ -229,16 +245,19 @@ class DynamicShortConv(torch.autograd.Function):
     def backward(ctx, gy):
         u, h, A, B_or_W, cu_seqlens, z = ctx.saved_tensors
         out = ctx.plan.backward(gy.contiguous(), u, h, A, B_or_W, cu_seqlens, z_saved=z)
+        if ctx.errors is not None:
+            _report(ctx.errors, ctx.plan.ws)
         dA = out["dA"].to(A.dtype) if A is not None else None
-        return out["du"], out["dh"], dA, out["dBW"].to(B_or_W.dtype), None, None, None, None, None
+        return out["du"], out["dh"], dA, out["dBW"].to(B_or_W.dtype), None, None, None, None, None, None
 
 
 def dynamic_short_conv(u: torch.Tensor, h: torch.Tensor, A: Optional[torch.Tensor], B_or_W: torch.Tensor,
                        ksize: int, head_dim: int = 0, batch: int = 1,
-                       cu_seqlens: Optional[torch.Tensor] = None, algo: int = L.ALGO_AUTO) -> torch.Tensor:
+                       cu_seqlens: Optional[torch.Tensor] = None, algo: int = L.ALGO_AUTO,
+                       errors: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Functional form with autograd: u [N, C] token-major (N = batch * seqlen) or
-    [batch, C, seqlen] channel-first; h [N, d]."""
-    return DynamicShortConv.apply(u, h, A, B_or_W, ksize, head_dim, batch, cu_seqlens, algo)
+    [batch, C, seqlen] channel-first; h [N, d].  ``errors``: as in :func:`qkv_attention`."""
+    return DynamicShortConv.apply(u, h, A, B_or_W, ksize, head_dim, batch, cu_seqlens, algo, errors)
 
 
 class _Plan:
@@ -250,23 +269,26 @@ class _Plan:
     stream than the one the plan was made on waits for that one; not so inside a capture, which cannot wait for
     anything outside it: synchronise before."""
 
+    _made = None
+
     def _workspace(self, nbytes: int, one_stream: bool) -> None:
         """Last in the making of a plan; one_stream: never called on another stream than this one."""
         self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-        self._made, self._index = None, self.device.index
-        if self.device.type == "cuda" and not one_stream and not torch.cuda.is_current_stream_capturing():
+        self._index = self.device.index
+        if not one_stream and self._index is not None and not torch.cuda.is_current_stream_capturing():
             here = torch.cuda.current_stream(self.device)
             self._made, self._behind = here.record_event(), {here.cuda_stream}
 
     def _run(self, call, *args) -> None:
-        here = None if self._index is None else _current(self._index)
+        index = self._index
+        here = None if index is None else _current(index)
         if self._made is not None and here not in self._behind and not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(self.device).wait_event(self._made)
             self._behind.add(here)
-        if self._index is None or self._index == torch.cuda.current_device():
+        if index is None or index == torch.cuda.current_device():
             call(*args, here)
         else:                                   # kernels launch on the current device
-            with torch.cuda.device(self._index):
+            with torch.cuda.device(index):
                 call(*args, here)
 
     def _other(self, stream) -> Optional[torch.cuda.Stream]:
@@ -491,8 +513,10 @@ class QKVAttention(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, qkv, table, heads: int, kv_heads: int, head_dim: int, batch: int, cu_seqlens, scale: float,
-                layout: int, algo: int):
+                layout: int, algo: int, errors=None):
         N, C = qkv.shape
+        if errors is not None:
+            _check_errors(errors, qkv.device)
         wq, wk = heads * head_dim, kv_heads * head_dim
         if C != wq + 2 * wk:
             raise ValueError(f"qkv must be [N, (heads + 2 kv_heads) * head_dim] = [N, {wq + 2 * wk}], got {list(qkv.shape)}")
@@ -504,8 +528,10 @@ class QKVAttention(torch.autograd.Function):
         qk, rope, qk_row = qkv[:, :wq + wk], None, row
         if table is not None:
             rope = (batch, N // batch, heads + kv_heads, head_dim, table, layout)
-            qk = RopePlan(qkv.dtype, *rope, x_row_stride=row, device=qkv.device, _one_stream=True).apply(
-                qk, cu_seqlens=cu_seqlens)
+            turn = RopePlan(qkv.dtype, *rope, x_row_stride=row, device=qkv.device, _one_stream=True)
+            qk = turn.apply(qk, cu_seqlens=cu_seqlens)
+            if errors is not None:
+                _report(errors, turn.ws)
             qk_row = wq + wk
         q, k, v = qk[:, :wq], qk[:, wq:], qkv[:, wq + wk:]
         # columns that start off a 16-byte boundary (heads of odd widths) are copied out, and their gradients in
@@ -518,7 +544,9 @@ class QKVAttention(torch.autograd.Function):
                         device=qkv.device, _one_stream=True)
         train = ctx.needs_input_grad[0]
         o, lse = plan.forward(q, k, v, cu_seqlens, want_lse=True) if train else (plan.forward(q, k, v, cu_seqlens), None)
-        ctx.plan, ctx.rope, ctx.apart, ctx.width = plan, rope, apart, (N, C, wq, wk)
+        if errors is not None:
+            _report(errors, plan.ws)
+        ctx.plan, ctx.rope, ctx.apart, ctx.width, ctx.errors = plan, rope, apart, (N, C, wq, wk), errors
         if train:
             ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
         return o
@@ -534,30 +562,38 @@ class QKVAttention(torch.autograd.Function):
         if ctx.apart:
             for name, part in out.items():
                 part.copy_(grads[name])
+        if ctx.errors is not None:
+            _report(ctx.errors, ctx.plan.ws)
         if ctx.rope is not None:
-            RopePlan(q.dtype, *ctx.rope, x_row_stride=C, y_row_stride=C, device=q.device, _one_stream=True).apply(
-                d[:, :wq + wk], y=d[:, :wq + wk], cu_seqlens=cu_seqlens, inverse=True)
-        return d, None, None, None, None, None, None, None, None, None
+            turn = RopePlan(q.dtype, *ctx.rope, x_row_stride=C, y_row_stride=C, device=q.device, _one_stream=True)
+            turn.apply(d[:, :wq + wk], y=d[:, :wq + wk], cu_seqlens=cu_seqlens, inverse=True)
+            if ctx.errors is not None:
+                _report(ctx.errors, turn.ws)
+        return (d,) + (None,) * 10
 
 
 def qkv_attention(qkv: torch.Tensor, heads: int, kv_heads: int, head_dim: int, table: Optional[torch.Tensor] = None,
                   batch: int = 1, cu_seqlens: Optional[torch.Tensor] = None, scale: float = 0.0,
-                  layout: int = L.ROPE_INTERLEAVED, algo: int = L.ALGO_AUTO) -> torch.Tensor:
+                  layout: int = L.ROPE_INTERLEAVED, algo: int = L.ALGO_AUTO,
+                  errors: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Functional form with autograd: rotary positions (``table``, see :func:`rope_table`) on the Q and K
     columns of qkv [N, (heads + 2 kv_heads) * head_dim], then causal attention; o [N, heads * head_dim].
-    The table has a row for every position; a packed document that is longer repeats the last one (a
-    :class:`RopePlan` of the caller's own reports that through ``dynconv_device_status``).  Calls and their
+    The table has a row for every position; a packed document that is longer repeats the last one.  ``errors``
+    (uint8, 256 bytes, zeroed once, for the calls of one stream): what the device finds wrong in the forward or the
+    backward -- such a document, a malformed cu_seqlens (undefined results), a pipeline wait that ran out (outputs not
+    written) -- is kept there for ``dynconv_device_status(errors)``; without it nothing tells of them.  Calls and their
     backward may be captured into a CUDA graph; as for any autograd function, no eager graph of the same leaves may
     be alive then."""
-    return QKVAttention.apply(qkv, table, heads, kv_heads, head_dim, batch, cu_seqlens, scale, layout, algo)
+    return QKVAttention.apply(qkv, table, heads, kv_heads, head_dim, batch, cu_seqlens, scale, layout, algo, errors)
 
 
 def dynamic_conv_attention(u: torch.Tensor, h: torch.Tensor, A: Optional[torch.Tensor], B_or_W: torch.Tensor,
                            ksize: int, heads: int, kv_heads: int, head_dim: int, table: Optional[torch.Tensor] = None,
                            filter_head_dim: int = 0, batch: int = 1, cu_seqlens: Optional[torch.Tensor] = None,
-                           scale: float = 0.0, layout: int = L.ROPE_INTERLEAVED, algo: int = L.ALGO_AUTO) -> torch.Tensor:
+                           scale: float = 0.0, layout: int = L.ROPE_INTERLEAVED, algo: int = L.ALGO_AUTO,
+                           errors: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The QKV placement as a layer runs it: the dynamic short convolution of the fused QKV rows u [N, C]
     (C = (heads + 2 kv_heads) * head_dim; head-wise filters where filter_head_dim > 0), rotary positions on
-    Q and K, causal attention.  With autograd; o [N, heads * head_dim]."""
-    y = dynamic_short_conv(u, h, A, B_or_W, ksize, filter_head_dim, batch, cu_seqlens, algo)
-    return qkv_attention(y, heads, kv_heads, head_dim, table, batch, cu_seqlens, scale, layout, algo)
+    Q and K, causal attention.  With autograd; o [N, heads * head_dim].  ``errors``: as in :func:`qkv_attention`."""
+    y = dynamic_short_conv(u, h, A, B_or_W, ksize, filter_head_dim, batch, cu_seqlens, algo, errors)
+    return qkv_attention(y, heads, kv_heads, head_dim, table, batch, cu_seqlens, scale, layout, algo, errors)
