@@ -527,8 +527,8 @@ class QKVAttention(torch.autograd.Function):
         row = qkv.stride(0) if N > 1 else C
         qk, rope, qk_row = qkv[:, :wq + wk], None, row
         if table is not None:
-            rope = (batch, N // batch, heads + kv_heads, head_dim, table, layout)
-            turn = RopePlan(qkv.dtype, *rope, x_row_stride=row, device=qkv.device, _one_stream=True)
+            rope = (qkv.dtype, batch, N // batch, heads + kv_heads, head_dim)
+            turn = RopePlan(*rope, table, layout, x_row_stride=row, device=qkv.device, _one_stream=True)
             qk = turn.apply(qk, cu_seqlens=cu_seqlens)
             if errors is not None:
                 _report(errors, turn.ws)
@@ -546,15 +546,16 @@ class QKVAttention(torch.autograd.Function):
         o, lse = plan.forward(q, k, v, cu_seqlens, want_lse=True) if train else (plan.forward(q, k, v, cu_seqlens), None)
         if errors is not None:
             _report(errors, plan.ws)
-        ctx.plan, ctx.rope, ctx.apart, ctx.width, ctx.errors = plan, rope, apart, (N, C, wq, wk), errors
+        ctx.plan, ctx.rope, ctx.layout, ctx.apart, ctx.errors = plan, rope, layout, apart, errors
+        ctx.width = N, C, wq, wk
         if train:
-            ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
+            ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, table)
         return o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, go):
-        q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
+        q, k, v, o, lse, cu_seqlens, table = ctx.saved_tensors
         N, C, wq, wk = ctx.width
         d = torch.empty((N, C), dtype=q.dtype, device=q.device)
         out = {"dq": d[:, :wq], "dk": d[:, wq:wq + wk], "dv": d[:, wq + wk:]}
@@ -565,7 +566,8 @@ class QKVAttention(torch.autograd.Function):
         if ctx.errors is not None:
             _report(ctx.errors, ctx.plan.ws)
         if ctx.rope is not None:
-            turn = RopePlan(q.dtype, *ctx.rope, x_row_stride=C, y_row_stride=C, device=q.device, _one_stream=True)
+            turn = RopePlan(*ctx.rope, table, ctx.layout, x_row_stride=C, y_row_stride=C, device=q.device,
+                            _one_stream=True)
             turn.apply(d[:, :wq + wk], y=d[:, :wq + wk], cu_seqlens=cu_seqlens, inverse=True)
             if ctx.errors is not None:
                 _report(ctx.errors, turn.ws)
