@@ -6,7 +6,8 @@
 // sequence, so all heads of the group and all its tokens (rows r = m * group + g) share each key and value
 // read, and one of n_split runs of the cached rows, because batch x kv_heads alone would not fill the GPU;
 // runs follow the sequence's own length.  Tiles of K and V come through a ring of 16-byte asynchronous
-// copies (rows beyond L are zero-filled, never read).  The drafted rows are a last tile that the block
+// copies (rows beyond L are zero-filled, never read; the 8-row kernel's and the tcgen05 kernel's TMA boxes do read
+// them, mask their scores and set their values to zero).  The drafted rows are a last tile that the block
 // of the last run fills from k and v (rotated, rounded to the storage type as the cache holds them) and also
 // writes to the cache.  Partial results of the runs are joined in their order by the block that finishes
 // last (a counter per head and sequence, reset by it), so results repeat bitwise.

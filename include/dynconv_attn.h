@@ -144,8 +144,9 @@ DYNCONV_API size_t dynconv_attn_decode_workspace_bytes(const dynconv_attn_decode
  *              drafted token j (its own bit included; an entry may be 0: it then sees the cached
  *              rows only, and its o is zero where there are none).  depth(m) counts the bits
  *              other than m.  NULL: token m sees tokens 0 .. m (a chain).
- * Rows of the cache at L + tokens and beyond are neither read nor written, and what a masked
- * row holds (infinities and NaN among it) does not reach o.
+ * Rows of the cache at L + tokens and beyond are not written.  They may be read, whole tiles at a
+ * time, up to max_len, so nothing may write to them meanwhile; what they and masked rows hold
+ * (infinities and NaN among it) does not reach o.
  * Errors: DYNCONV_ERR_INVALID, _UNSUPPORTED, _WORKSPACE, _CUDA; L + tokens above max_len, or a
  * position at or beyond rope_max_pos, raises the device check and the sequence is treated as idle. */
 DYNCONV_API dynconv_status dynconv_attn_decode(const dynconv_attn_decode_desc *desc, const void *q, const void *k,
