@@ -265,40 +265,49 @@ class _Plan:
     streams they are made, called and given their tensors on.
 
     A call runs on the current stream, or on ``stream``: there it comes behind what the current stream holds by
-    then, its outputs belong to that stream, and its inputs and the plan may be dropped at once.  A call on another
-    stream than the one the plan was made on waits for that one; not so inside a capture, which cannot wait for
-    anything outside it: synchronise before."""
+    then, its outputs belong to that stream, and its inputs and the plan may be dropped at once.  The first call on
+    another stream than the one the plan was made on waits for that one; not so inside a capture, which cannot wait
+    for anything outside it: synchronise before."""
 
-    _made = None
+    _behind = None                              # handles of the streams that are behind the zeroing, the first its own
 
     def _workspace(self, nbytes: int, one_stream: bool) -> None:
         """Last in the making of a plan; one_stream: never called on another stream than this one."""
         self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
         self._index = self.device.index
         if not one_stream and self._index is not None and not torch.cuda.is_current_stream_capturing():
-            here = torch.cuda.current_stream(self.device)
-            self._made, self._behind = here.record_event(), {here.cuda_stream}
+            self._behind = [_current(self._index)]
 
     def _run(self, call, *args) -> None:
         index = self._index
         here = None if index is None else _current(index)
-        if self._made is not None and here not in self._behind and not torch.cuda.is_current_stream_capturing():
-            torch.cuda.current_stream(self.device).wait_event(self._made)
-            self._behind.add(here)
+        if self._behind is not None and here not in self._behind:
+            self._order(here)
         if index is None or index == torch.cuda.current_device():
             call(*args, here)
         else:                                   # kernels launch on the current device
             with torch.cuda.device(index):
                 call(*args, here)
 
+    def _order(self, here: int) -> None:
+        if torch.cuda.is_current_stream_capturing():
+            return
+        made = self._stream(self._behind[0])
+        with torch.cuda.stream(made):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if not capturing:                       # else the zeroing was over before the capture began
+            torch.cuda.current_stream(self.device).wait_stream(made)
+        self._behind.append(here)
+
+    def _stream(self, handle: int) -> torch.cuda.Stream:
+        return torch.cuda.ExternalStream(handle, self.device) if handle else torch.cuda.default_stream(self.device)
+
     def _other(self, stream) -> Optional[torch.cuda.Stream]:
         """`stream` (a stream, or a handle) where it is another than the current one."""
         if self._index is None:
             return None
         at = L._stream(stream, None)
-        if at == _current(self._index):
-            return None
-        return torch.cuda.ExternalStream(at, device=self.device) if at else torch.cuda.default_stream(self.device)
+        return None if at == _current(self._index) else self._stream(at)
 
     def _call_on(self, stream: torch.cuda.Stream, call, *args):
         """call(*args) with `stream` current, behind what the stream that is current now holds."""
