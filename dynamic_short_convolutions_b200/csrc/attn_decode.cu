@@ -19,9 +19,10 @@
 // attn_decode_tc.cu); P is rounded to bf16 because the tensor cores take it so, its sum is taken before; the rotated
 // q is kept as two bf16 (value and remainder), since nothing else rounds it.  fp32: FMAs, a warp per four rows.
 //
-// Measured: 64 sequences of ~3000 rows, 16 heads of 128 over 4, one token: 72 us, 5.57 TB/s (0.85 of the copy rate; 88
-// on 16-row tiles); one of ~700 rows, 12 heads of 64: 8.4 us, the chain length, rows, softmax, join.
-// fp32: the first 154 us (5.1 TB/s, 0.78), the second 11.3, 13 of ~560 rows with 3 tokens and 4 heads a group 14.6.
+// Measured: 64 sequences of ~3000 rows, 16 heads of 128 over 4, one token: 71 us, 5.6 TB/s (0.85 of the copy rate; 88
+// on 16-row tiles); 64 of 3000, 4 tokens (16 rows): 75 us, 5.3 TB/s; 8 tokens (32 rows): 99 us, 4.0 TB/s, where the
+// barriers of a tile and 255 registers tell; one of ~700 rows, 12 heads of 64: 8.3 us, the chain length, rows, softmax,
+// join.  fp32: the first 154 us (5.1 TB/s, 0.78), the second 11.3, 13 of ~560 rows with 3 tokens and 4 heads a group 14.9.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -15,7 +15,7 @@
 // Warps: 0-3 softmax (a row per thread); 4-7 the drafted tile, meanwhile; both rotate q before; 8 issues the MMAs;
 // 9 the TMA loads.
 //
-// Measured: 8 sequences of ~2200 rows, trees of 24 tokens, 16 heads of 128 over 4: 28.6 us (1.3 TB/s; 48 with mma.sync and
+// Measured: 8 sequences of ~2200 rows, trees of 24 tokens, 16 heads of 128 over 4: 25.7 us (1.5 TB/s; 48 with mma.sync and
 // a join through memory).  About 10 us are the set-up, q's rotation and the join; a tile of 128 rows takes 2 us.
 #include <cooperative_groups.h>
 

@@ -19,6 +19,10 @@
 // of the grid, which halves the distinct rows a warp reads, changed nothing; two blocks of dk and dv per
 // multiprocessor at 128 registers neither.
 //
+// The backward takes p again from the lse, which the forward rounded to fp32, and D from the o it rounded: two roundings
+// more than a form that keeps p.  They show where a row sees few keys and dp - D cancels: dq of documents of 2 tokens is
+// off by 4.4e-7 rel-L2 (a plain fp32 form 1.9e-7), of 8 by 2.8e-7 (1.4e-7), of 64 by 2.7e-7 (2.4e-7).
+//
 // Masked places: the score is replaced before the maximum, and in masked tiles a product with a
 // masked probability is not added at all (0 x NaN would be NaN).
 #include <cooperative_groups.h>

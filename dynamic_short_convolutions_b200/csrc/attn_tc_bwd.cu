@@ -9,8 +9,9 @@
 // keys of one key/value head and walks the query tiles of every head of the group; attn_dq_kernel takes 128
 // queries of one head and walks the key tiles.  S and dP are computed in both (7 products of a tile pair
 // where one fused kernel needs 5), because the fused kernel would add a 128 x 128 fp32 tile of dQ into global
-// memory for every tile pair -- 64 KB per 2.6 us of tensor work and SM, above what L2 reduces --
-// and in an order that changes from run to run.  Here nothing is added atomically and results repeat bitwise.
+// memory for every tile pair, in an order that changes from run to run.  Here nothing is added atomically and results
+// repeat bitwise.  What that costs is open: bulk tensor reductions alone run at 4.6 (a block per SM) to 5.1 TB/s (two)
+// for the 1141 MB that 8 sequences of 2048, 16 heads of 128 would add (224 to 248 us, as long as either kernel takes).
 //
 // No operand passes through shared memory by hand: the transposed scores S^T = K Q^T put keys on the TMEM
 // lanes, P^T and dS^T are written back to TMEM as bf16 and are the A operands of dV and dK; in attn_dq_kernel

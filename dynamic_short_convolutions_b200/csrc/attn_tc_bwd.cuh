@@ -145,6 +145,8 @@ __device__ __forceinline__ void join_parts(const AttnTcArgs& a, cg::cluster_grou
 
 // Blocks that share the heads of a group, a power of two up to 8, while key tiles are few.  Measured at HD = 128:
 // 312 tiles of documents of many lengths 205 us with 2, 283 with 1, 301 with 4; 512 equal ones 451 with 1, 503 with 2.
+// At 64 channels, two blocks per multiprocessor: 32 tiles, groups of 8: 99 us with 8, 601 with 1; 96, groups of 4: 72
+// with 4, 160 with 1; 128: 85 with 4, 97 with 2; 256: 131 with 2, 171 with 1, 153 with 4; 512: 230 with 1, 225 with 2.
 inline int dkv_ranks(const AttnProb& p, int64_t blocks) {
     int ranks = 1;
     while (ranks * 2 <= std::min(p.group, 8) && blocks * ranks < 3 * num_sms()) ranks *= 2;

@@ -10,7 +10,9 @@
 // Measured at 8 sequences of 2048, 12 heads: dkv 166 us (620 TFLOP/s; 204 us as one block per SM with items of 128 x 128), dq 122 (633; 160);
 // an item takes 1.5 and 0.9 us of a block's time, what is outside the items about 8 us per block.  Both loads of scores
 // and dP before the exponentials made dq 142; D from tiles by TMA, as the wide kernel does it, 123;
-// blocks that walk their tiles, as wide dq's do, 157 (an item 1.06 us: the two blocks of an SM keep in step).
+// blocks that walk their tiles, as wide dq's do, 157 (an item 1.06 us: the two blocks of an SM keep in step).  One fused
+// kernel would take each exponential once and add 428 MB of dQ here, for which bulk tensor reductions alone take 78 to
+// 82 us (5.2 to 5.5 TB/s): untried, its sums would change with the order of the blocks.
 //
 // Warps: 0-3 the element work (a lane is a row, all 64 columns) and the look for infinities and NaN in masked
 // tiles; 4 issues the MMAs; 5 the TMA loads and (dkv) the items' lse and D.

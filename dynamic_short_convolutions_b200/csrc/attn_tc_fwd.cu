@@ -21,10 +21,12 @@
 // among the values of tiles that are masked for some row; where they find one, the rows of the CTA are computed
 // again one by one over the tokens they see.
 //
-// Measured: 4 sequences of 4096, 16 heads of 128 over 4: 256 us, 1073 TFLOP/s (0.65 of the measured matrix-product
-// rate; the tensor cores are what bounds it, at the card's power limit); one of 16384 about 1200; 8 of 2048, 12 heads
-// of 64: 106 us, 490 TFLOP/s (the exponentials, one per 256 operations here, take 45 of them); one of 77: 7.2 us,
-// the length of one tile's chain from the first load to the last store.
+// Measured: 4 sequences of 4096, 16 heads of 128 over 4: 263 us at 1965 MHz, 1045 TFLOP/s (0.64 of the measured
+// matrix-product rate), and 299 to 304 us in calls that follow one another, where the power cap (989 W) holds the clock
+// at 1605 to 1627 MHz: the same number of cycles.  The tensor pipe is busy for 52 % of them, that of the exponentials
+// for 52 %; the rest is the chain of an item's steps that two blocks do not hide.  One of 16384 about 1200 TFLOP/s;
+// 8 of 2048, 12 heads of 64: 104 us at 1965 MHz with no cap, 495 TFLOP/s (exponentials, one per 256 operations here:
+// 50 %, tensor pipe 24 %); one of 77: 6.0 us, the length of one tile's chain from the first load to the last store.
 #include <algorithm>
 #include <type_traits>
 

@@ -267,9 +267,10 @@ class _Plan:
     A call runs on the current stream, or on ``stream``: there it comes behind what the current stream holds by
     then, its outputs belong to that stream, and its inputs and the plan may be dropped at once.  The first call on
     another stream than the one the plan was made on waits for that one; not so inside a capture, which cannot wait
-    for anything outside it: synchronise before."""
+    for anything outside it: synchronise before.  Calls of one plan share its workspace: one must be over on the device
+    before another starts, whatever their streams."""
 
-    _behind = None                              # handles of the streams that are behind the zeroing, the first its own
+    _behind = None          # handles of the streams that are behind the zeroing, the first the one it ran on
 
     def _workspace(self, nbytes: int, one_stream: bool) -> None:
         """Last in the making of a plan; one_stream: never called on another stream than this one."""
@@ -442,7 +443,8 @@ class AttnDecoder(_Plan):
 
     ``k_cache``, ``v_cache`` [batch, kv_heads, max_len, head_dim] and ``lens`` (int32 [batch]: tokens cached, a
     negative entry for an idle slot) are made here, empty, or taken from the caller.  A step reads ``lens`` and
-    leaves it: :meth:`advance` adds the tokens that are kept."""
+    leaves it: :meth:`advance` adds the tokens that are kept.  Behind a convolution tokens is 1, as
+    :class:`DynConvDecoder` takes one token per step."""
 
     def __init__(self, dtype: torch.dtype, batch: int, heads: int, kv_heads: int, head_dim: int, max_len: int,
                  tokens: int = 1, scale: float = 0.0, rope_table: Optional[torch.Tensor] = None,
