@@ -267,9 +267,12 @@ class _Plan:
     A call runs on the current stream, or on ``stream``: there it comes behind what the current stream holds by
     then, its outputs belong to that stream, and its inputs and the plan may be dropped at once.  The first call on
     another stream than the one the plan was made on waits for that one; not so inside a capture, which cannot wait
-    for anything outside it: synchronise before.  Calls of one plan share its workspace: one must be over on the device
-    before another starts, whatever their streams."""
+    for anything outside it: synchronise before.  In a capture the current stream waits for ``stream`` at once.
 
+    Calls of one plan share its workspace, so one must be over on the device before the next starts: a call that was
+    given ``stream`` is waited for, the rest is the order of the streams that are current."""
+
+    _last = None            # the last call, where it ran on a stream of its own
     _behind = None          # handles of the streams that are behind the zeroing, the first the one it ran on
 
     def _workspace(self, nbytes: int, one_stream: bool) -> None:
@@ -284,11 +287,19 @@ class _Plan:
         here = None if index is None else _current(index)
         if self._behind is not None and here not in self._behind:
             self._order(here)
+        if self._last is not None:
+            self._settle()
         if index is None or index == torch.cuda.current_device():
             call(*args, here)
         else:                                   # kernels launch on the current device
             with torch.cuda.device(index):
                 call(*args, here)
+
+    def _settle(self) -> None:
+        """The current stream behind the last call, where that ran on a stream of its own."""
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.device).wait_event(self._last)
+            self._last = None
 
     def _order(self, here: int) -> None:
         if torch.cuda.is_current_stream_capturing():
@@ -320,10 +331,13 @@ class _Plan:
                 stream.wait_stream(here)
             result = call(*args)
             if not torch.cuda.is_current_stream_capturing():
+                self._last = stream.record_event()
                 for t in (*args, *vars(self).values()):
                     for x in t.values() if isinstance(t, dict) else (t,):
                         if isinstance(x, torch.Tensor):
                             x.record_stream(stream)
+        if captured:                            # a branch of the capture ends where the call does
+            here.wait_stream(stream)
         return result
 
 
@@ -473,7 +487,6 @@ class AttnDecoder(_Plan):
         self.dtype, self.batch, self.tokens = dtype, batch, tokens
         self.wq, self.wk = heads * head_dim, kv_heads * head_dim
         self.strides = (q_row_stride, k_row_stride, v_row_stride)
-        self._stepped = None                    # the last step, where it ran on a stream of its own
         self._workspace(nbytes, False)
 
     def step(self, q, k, v, ancestors=None, o=None, stream=None):
@@ -482,9 +495,7 @@ class AttnDecoder(_Plan):
         [batch, tokens]): bit j of an entry set where that token sees drafted token j, its own bit included;
         None: a chain."""
         if stream is not None and (other := self._other(stream)) is not None:
-            o = self._call_on(other, self.step, q, k, v, ancestors, o)
-            self._stepped = other.record_event()
-            return o
+            return self._call_on(other, self.step, q, k, v, ancestors, o)
         rows = self.batch * self.tokens
         _rows(q, "q", rows, self.wq, self.dtype, self.strides[0], self.device)
         if o is None:
@@ -502,18 +513,14 @@ class AttnDecoder(_Plan):
         """Adds the tokens kept of the last step to ``lens``: all of them, or ``kept`` (int32 [batch]).  Idle
         slots stay idle.  Kept tokens of a tree have to lie in the cache in order (tokens 0 .. kept - 1)."""
         _flat(kept, "kept", torch.int32, self.device, (self.batch,))
-        self._settle()
+        if self._last is not None:              # a step that may still read lens
+            self._settle()
         self.lens.add_(torch.where(self.lens < 0, 0, self.tokens if kept is None else kept).to(torch.int32))
 
     def reset(self):
-        self._settle()
+        if self._last is not None:              # a step that may still read lens
+            self._settle()
         self.lens.zero_()
-
-    def _settle(self):
-        """The current stream behind a step that ran on a stream of its own and may still read lens."""
-        if self._stepped is not None:
-            torch.cuda.current_stream(self.device).wait_event(self._stepped)
-            self._stepped = None
 
 
 class QKVAttention(torch.autograd.Function):
@@ -557,9 +564,9 @@ class QKVAttention(torch.autograd.Function):
         o, lse = plan.forward(q, k, v, cu_seqlens, want_lse=True) if train else (plan.forward(q, k, v, cu_seqlens), None)
         if errors is not None:
             _report(errors, plan.ws)
-        ctx.plan, ctx.rope, ctx.layout, ctx.apart, ctx.errors = plan, rope, layout, apart, errors
-        ctx.width = N, C, wq, wk
         if train:
+            ctx.plan, ctx.rope, ctx.layout, ctx.apart, ctx.errors = plan, rope, layout, apart, errors
+            ctx.width = N, C, wq, wk
             ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, table)
         return o
 

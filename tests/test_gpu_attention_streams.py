@@ -162,3 +162,47 @@ def test_the_current_stream_by_name_and_in_a_capture():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_steps_on_a_branch_of_a_capture():
+    """The branch is joined by the call; lens moves on behind it in the graph, and eagerly afterwards."""
+    q, k, v, _ = _rows(2, 5)
+    a, b = _decoder(700), _decoder(700)
+    want = []
+    for _ in range(3):
+        want.append(a.step(q, k, v))
+        a.advance()
+    side, fork = torch.cuda.Stream(), torch.cuda.Stream()
+    b.step(q, k, v)                                  # rows 700 are written again by the graph
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        o = b.step(q, k, v, stream=fork)
+        b.advance()
+    for w in want[:2]:
+        o.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, w)
+    assert torch.equal(b.step(q, k, v, stream=fork), want[2])
+    b.advance()
+    torch.cuda.synchronize()
+    assert torch.equal(b.lens, a.lens)
+
+
+@pytest.mark.parametrize("tokens", [1, 24])
+def test_the_next_call_waits_for_one_on_a_stream_of_its_own(tokens):
+    """Steps that share counters and parts, the first of each pair held back on its stream."""
+    rows = [_rows(2 * tokens, s)[:3] for s in (6, 7, 8)]
+    a, b = _decoder(3500, tokens), _decoder(3500, tokens)
+    want = [a.step(*r) for r in rows]
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for r, s in zip(rows, (sides[0], None, sides[1])):
+        if s is not None:
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(HOLD // 2)
+        got.append(b.step(*r, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
