@@ -39,6 +39,32 @@ def test_causal_rows(dtype, hd, algo):
     check("lse", lse[:, keep], ref["lse"])
 
 
+@pytest.mark.parametrize("hd,algo", [(64, 0), (128, 0), (128, 1), (37, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradients_of_other_documents(dtype, hd, algo):
+    """Tiles that hold the end of a document of such rows and the beginning of another: the other's gradients."""
+    from dynamic_short_convolutions_b200 import _lib as L, ops
+
+    heads, kv, cu = 4, 2, [0, 70, 300, 431]
+    N = cu[-1]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda n: torch.randn((N, n * hd), generator=g, device="cuda").to(DT[dtype])
+    q, k, v, do = rnd(heads), rnd(kv), rnd(kv), rnd(heads)
+    q.view(N, heads, hd)[:, :, 0].abs_().add_(0.5)
+    ref = attention(q, k, v, cu, heads, kv, hd, do, 0.0, EPS[dtype])
+    k.view(N, kv, hd)[cu[1]:cu[2], :, 0] = -float("inf")
+    plan = ops.AttnPlan(DT[dtype], 1, N, heads, kv, hd, algo=algo)
+    cu_t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o, lse = plan.forward(q, k, v, cu_t, want_lse=True)
+    d = plan.backward(do, q, k, v, o, lse, cu_t)
+    assert L.dynconv_device_status(plan.ws) == 0
+    keep = torch.ones(N, dtype=torch.bool, device="cuda")
+    keep[cu[1]:cu[2]] = False
+    for name, t in dict(o=o, **d).items():
+        check(name, t[keep], [x[keep] for x in ref[name]])
+    assert torch.isnan(o[~keep]).all()
+
+
 # lens of the sequences: all cached scores lost, half of them, none cached, idle; tokens, heads, kv_heads
 STEPS = [(1, 4, 2), (2, 8, 2), (4, 8, 2), (7, 8, 2), (24, 8, 2)]
 
